@@ -28,3 +28,14 @@ from .binding import (  # noqa: F401
     tf_verify_round,
     tf_wait_limit_test,
 )
+from .serving import (  # noqa: F401
+    SERVE_EXPORTS,
+    Q8Cache,
+    tf_kv_append_q8,
+    tf_kv_read_q8,
+    tf_logprob_rows,
+    tf_paged_attn_q8,
+    tf_paged_attn_q8_workspace_bytes,
+    tf_paged_attn_shared,
+    tf_paged_attn_shared_workspace_bytes,
+)

@@ -2,7 +2,8 @@
 
     python -m paged_kv_cache_segment_b200.build [--verbose-ptxas]
 
-The shared library exports exactly the C ABI of include/tfpaged.h.
+The shared library exports exactly the C ABI of include/tfpaged.h and
+include/tfserve.h.
 """
 from __future__ import annotations
 
@@ -27,7 +28,7 @@ def sources() -> list[str]:
 
 def headers() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(HERE, "..", "include", "tfpaged.h")])
+                  + glob.glob(os.path.join(HERE, "..", "include", "*.h")))
 
 
 def stale() -> bool:

@@ -8,6 +8,7 @@
 #include <vector>
 #include <cuda_runtime.h>
 
+#include "api_common.h"
 #include "tf_internal.h"
 
 using namespace tfp;
@@ -22,54 +23,6 @@ uint64_t test_wait_runout_ns() { return g_wait_runout_ns; }
 }  // namespace tfp
 
 namespace {
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int log2_exact(int x) {
-    if (x <= 0 || (x & (x - 1))) return -1;
-    int r = 0;
-    while ((1 << r) < x) ++r;
-    return r;
-}
-
-bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
-
-tf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TF_OK : TF_ERR_CUDA; }
-
-int split_len(int n_keys, int split_keys, int n_splits_max, int page_size) {
-    if (split_keys > 0) return split_keys;
-    int per = (n_keys + n_splits_max - 1) / n_splits_max;
-    return (per + page_size - 1) / page_size * page_size;
-}
-
-// Checks of a host copy of a segment table; see tf_paged_attn_decode.
-tf_status check_segs_host(const tf_seg *sh, int n_segs, int n_rows_total, int page_table_len, int page_size,
-                          int n_pages, const int32_t *pt_host, int split_keys, int n_splits_max, int *max_rows,
-                          bool full = false) {
-    int mr = 0;
-    for (int s = 0; s < n_segs; ++s) {
-        const tf_seg e = sh[s];
-        if (e.q_row < 0 || e.n_rows < 0 || (int64_t)e.q_row + e.n_rows > n_rows_total ||
-            e.n_keys < (full ? (e.n_rows > 0 ? 1 : 0) : e.n_rows) ||
-            e.pt_base < 0 || e.n_pages < 0 || (int64_t)e.pt_base + e.n_pages > page_table_len)
-            return TF_ERR_ARG;
-        if ((int64_t)e.n_keys > (int64_t)e.n_pages * page_size) return TF_ERR_PAST_PAGES;
-        if (e.n_rows > 0 && n_splits_max > 0) {
-            const int per = split_len(e.n_keys, split_keys, n_splits_max, page_size);
-            if ((e.n_keys + per - 1) / per > n_splits_max) return TF_ERR_ARG;
-        }
-        if (pt_host) {
-            const int used = (e.n_keys + page_size - 1) / page_size;
-            for (int k = 0; k < used; ++k) {
-                const int pid = pt_host[e.pt_base + k];
-                if (pid < 0 || pid >= n_pages) return TF_ERR_BAD_PAGE;
-            }
-        }
-        if (e.n_rows > mr) mr = e.n_rows;
-    }
-    *max_rows = mr;
-    return TF_OK;
-}
 
 tf_status ring_merge(const float *po, const float *pm, const float *pl, const uint8_t *pf, int n_segs, int n_q_heads,
                      int head_dim, int n_splits_max, int n_rows_total, const tf_ring_seg *rsegs, int split_slots,
@@ -131,7 +84,7 @@ double partial_makespan(const tf_seg *sh, int n_segs, int n_kv_heads, int rt, in
 
 // Split-KV partials of every row of every stream (the causal count, or with
 // `full` every row over all of its stream's keys).
-static tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
+tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                                const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads,
                                int32_t head_dim, const int32_t *page_table, int32_t page_table_len,
                                const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host,

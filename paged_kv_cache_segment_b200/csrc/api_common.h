@@ -1,0 +1,121 @@
+// api_common.h - argument checks shared by the extern "C" entry points.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/tfserve.h"
+#include "tf_internal.h"
+
+namespace tfp {
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int log2_exact(int x) {
+    if (x <= 0 || (x & (x - 1))) return -1;
+    int r = 0;
+    while ((1 << r) < x) ++r;
+    return r;
+}
+
+inline bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+inline tf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TF_OK : TF_ERR_CUDA; }
+
+inline int split_len(int n_keys, int split_keys, int n_splits_max, int page_size) {
+    if (split_keys > 0) return split_keys;
+    int per = (n_keys + n_splits_max - 1) / n_splits_max;
+    return (per + page_size - 1) / page_size * page_size;
+}
+
+// Checks of a host copy of a segment table; see tf_paged_attn_decode.
+inline tf_status check_segs_host(const tf_seg *sh, int n_segs, int n_rows_total, int page_table_len, int page_size,
+                          int n_pages, const int32_t *pt_host, int split_keys, int n_splits_max, int *max_rows,
+                          bool full = false) {
+    int mr = 0;
+    for (int s = 0; s < n_segs; ++s) {
+        const tf_seg e = sh[s];
+        if (e.q_row < 0 || e.n_rows < 0 || (int64_t)e.q_row + e.n_rows > n_rows_total ||
+            e.n_keys < (full ? (e.n_rows > 0 ? 1 : 0) : e.n_rows) ||
+            e.pt_base < 0 || e.n_pages < 0 || (int64_t)e.pt_base + e.n_pages > page_table_len)
+            return TF_ERR_ARG;
+        if ((int64_t)e.n_keys > (int64_t)e.n_pages * page_size) return TF_ERR_PAST_PAGES;
+        if (e.n_rows > 0 && n_splits_max > 0) {
+            const int per = split_len(e.n_keys, split_keys, n_splits_max, page_size);
+            if ((e.n_keys + per - 1) / per > n_splits_max) return TF_ERR_ARG;
+        }
+        if (pt_host) {
+            const int used = (e.n_keys + page_size - 1) / page_size;
+            for (int k = 0; k < used; ++k) {
+                const int pid = pt_host[e.pt_base + k];
+                if (pid < 0 || pid >= n_pages) return TF_ERR_BAD_PAGE;
+            }
+        }
+        if (e.n_rows > mr) mr = e.n_rows;
+    }
+    *max_rows = mr;
+    return TF_OK;
+}
+
+// An 8-bit cache's type and sizes, its pointers, their alignment.
+inline tf_status check_q8_shape(const tf_q8_cache &c) {
+    if (c.n_pages < 0 || c.n_kv_heads <= 0 || (c.kv_type != TF_KV_E4M3 && c.kv_type != TF_KV_INT8)) return TF_ERR_ARG;
+    const int lp = log2_exact(c.page_size);
+    return head_dim_ok(c.head_dim) && lp >= 3 && lp <= 10 ? TF_OK : TF_ERR_UNSUPPORTED;
+}
+
+// Bytes of partials [n_rows_total][n_q_heads][n_splits]: o, m, l, flag, each
+// part's start a multiple of 16 bytes from the last.
+inline size_t part_bytes(int64_t n_rows_total, int n_q_heads, int head_dim, int n_splits) {
+    const size_t parts = (size_t)n_rows_total * n_q_heads * n_splits;
+    return (parts * ((size_t)head_dim * 4 + 9) + 255) / 256 * 256;
+}
+struct PartBuffers {
+    float *o, *m, *l;
+    uint8_t *flag;
+};
+inline PartBuffers part_buffers(void *at, int64_t n_rows_total, int n_q_heads, int head_dim, int n_splits) {
+    const size_t parts = (size_t)n_rows_total * n_q_heads * n_splits;
+    PartBuffers b;
+    b.o = static_cast<float *>(at);
+    b.m = b.o + parts * head_dim;
+    b.l = b.m + parts;
+    b.flag = reinterpret_cast<uint8_t *>(b.l + parts);
+    return b;
+}
+
+inline bool q8_pointers(const tf_q8_cache &c) { return c.k_codes && c.v_codes && c.k_scale && c.v_scale; }
+inline bool q8_aligned(const tf_q8_cache &c) {
+    return aligned16(c.k_codes) && aligned16(c.v_codes) && aligned16(c.k_scale) && aligned16(c.v_scale);
+}
+
+
+// SMs of the current device.
+inline int device_sms() {
+    int dev = 0, n = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
+                                                  cudaSuccess || n < 1)
+        n = 148;
+    return n;
+}
+
+// A split size for a host table: enough items (streams x kv-heads x splits) to
+// give each of `slots` resident CTAs about `per_slot` of them, in whole 64-key
+// tiles, at least `least` keys, at most n_splits_max splits a stream.
+inline int choose_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t slots, int per_slot, int least,
+                        int n_splits_max) {
+    int64_t keys = 0, longest = 1;
+    for (int s = 0; s < n_segs; ++s) {
+        if (sh[s].n_rows == 0) continue;
+        keys += sh[s].n_keys;
+        if (sh[s].n_keys > longest) longest = sh[s].n_keys;
+    }
+    int64_t len = keys * n_kv_heads / (slots * per_slot);
+    if (len < least) len = least;
+    const int64_t fit = (longest + n_splits_max - 1) / n_splits_max;
+    if (len < fit) len = fit;
+    len = (len + 63) / 64 * 64;
+    return len > 0x40000000 ? 0x40000000 : (int)len;
+}
+
+}  // namespace tfp

@@ -1,0 +1,106 @@
+// api_q8.cu - tf_paged_attn_q8: attention over an 8-bit cache, partials and
+// merge in one call (include/tfserve.h).  Argument checks on the host, then
+// two stream-ordered launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "api_common.h"
+#include "tf_internal.h"
+
+using namespace tfp;
+
+extern "C" {
+
+size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
+                                        int32_t n_splits_max) {
+    if (n_rows_total < 0 || n_q_heads <= 0 || head_dim <= 0 || n_splits_max <= 0) return 0;
+    return part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+}
+
+tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_heads, const tf_q8_cache *cache_host,
+                           const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
+                           const tf_seg *segs_host, const int32_t *page_table_host, float scale, int32_t full,
+                           int32_t split_keys, int32_t n_splits_max, void *workspace, size_t workspace_bytes,
+                           void *out, int32_t out_dtype, uint8_t *flags, uint32_t *status, tf_stream_t stream) {
+    if (!cache_host || n_rows_total < 0 || n_q_heads <= 0 || page_table_len < 0 || n_segs < 0 || split_keys < 0 ||
+        n_splits_max <= 0 || !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
+        return TF_ERR_ARG;
+    const tf_q8_cache c = *cache_host;
+    tf_status rc = check_q8_shape(c);
+    if (rc != TF_OK) return rc;
+    if (n_q_heads % c.n_kv_heads != 0 || (split_keys > 0 && split_keys < 16)) return TF_ERR_UNSUPPORTED;
+    if (n_segs > 65535 || n_splits_max > (1 << 24)) return TF_ERR_UNSUPPORTED;
+    if (n_segs == 0 || n_rows_total == 0) return TF_OK;
+    if (!q || !page_table || !segs || !workspace || !out || !flags || !status || !q8_pointers(c)) return TF_ERR_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !q8_aligned(c)) return TF_ERR_ALIGN;
+    if (workspace_bytes < tf_paged_attn_q8_workspace_bytes(n_rows_total, n_q_heads, c.head_dim, n_splits_max))
+        return TF_ERR_WORKSPACE;
+    const int group = n_q_heads / c.n_kv_heads;
+    int max_rows = n_rows_total, splits = n_splits_max, split = split_keys;
+    if (segs_host) {
+        rc = check_segs_host(segs_host, n_segs, n_rows_total, page_table_len, c.page_size, c.n_pages, page_table_host,
+                             split_keys, n_splits_max, &max_rows, full != 0);
+        if (rc != TF_OK) return rc;
+        if (max_rows == 0) return TF_OK;
+        if (split == 0)
+            split = choose_split(segs_host, n_segs, c.n_kv_heads, (int64_t)device_sms() * 2, 2, 256, n_splits_max);
+        // as many partial slots as the longest stream takes: the merge's reads stay close together
+        int longest = 1;
+        for (int s = 0; s < n_segs; ++s)
+            if (segs_host[s].n_rows > 0) longest = std::max(longest, (int)segs_host[s].n_keys);
+        splits = (int)(((int64_t)longest + split - 1) / split);
+    }
+    const int64_t n_qgroups = ((int64_t)max_rows * group + 63) / 64;
+    if (n_qgroups * c.n_kv_heads > 65535 || (int64_t)max_rows * n_q_heads > ((int64_t)1 << 31))
+        return TF_ERR_UNSUPPORTED;
+    const PartBuffers b = part_buffers(workspace, n_rows_total, n_q_heads, c.head_dim, splits);
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+
+    AttnParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.n_rows_total = n_rows_total;
+    p.hq = n_q_heads;
+    p.hkv = c.n_kv_heads;
+    p.group = group;
+    p.k_codes = static_cast<const uint8_t *>(c.k_codes);
+    p.v_codes = static_cast<const uint8_t *>(c.v_codes);
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.kv_type = c.kv_type;
+    p.n_pages = c.n_pages;
+    p.log2_page = log2_exact(c.page_size);
+    p.pt_len = page_table_len;
+    p.page_table = page_table;
+    p.segs = segs;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.split_keys = split;
+    p.n_splits_max = splits;
+    p.n_qgroups = (int)n_qgroups;
+    p.full = full ? 1 : 0;
+    p.part_o = b.o;
+    p.part_m = b.m;
+    p.part_l = b.l;
+    p.part_flag = b.flag;
+    p.status = status;
+    const dim3 grid((unsigned)splits, (unsigned)(n_qgroups * c.n_kv_heads), (unsigned)n_segs);
+    if (launch_attn_partial(p, c.head_dim, false, false, grid, st) != cudaSuccess) return TF_ERR_CUDA;
+
+    MergeSegsParams m{};
+    m.own = PartSet{b.o, b.m, b.l, b.flag, splits, split};
+    m.segs = segs;
+    m.n_segs = n_segs;
+    m.max_rows = max_rows;
+    m.n_rows_total = n_rows_total;
+    m.hq = n_q_heads;
+    m.log2_page = p.log2_page;
+    m.pt_len = page_table_len;
+    m.full = p.full;
+    m.out = out;
+    m.out_bf16 = out_dtype == TF_OUT_BF16;
+    m.flags = flags;
+    return cuda_status(launch_merge_segs(m, c.head_dim, st));
+}
+
+}  // extern "C"

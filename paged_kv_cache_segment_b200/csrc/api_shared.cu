@@ -1,0 +1,125 @@
+// api_shared.cu - tf_paged_attn_shared: attention of streams that share long
+// prefixes (include/tfserve.h).  The rows of a prefix form one segment whose
+// keys every row sees, so the prefix's partials come from the FULL partial
+// kernels with all of those rows as queries and its keys are read once for
+// them; the streams' own keys take the causal ones, and one merge joins both
+// sets.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "api_common.h"
+#include "tf_internal.h"
+
+using namespace tfp;
+
+extern "C" {
+
+size_t tf_paged_attn_shared_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
+                                            int32_t n_prefix_splits, int32_t n_splits_max) {
+    if (n_rows_total < 0 || n_q_heads <= 0 || head_dim <= 0 || n_prefix_splits <= 0 || n_splits_max <= 0) return 0;
+    return part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits) +
+           part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+}
+
+tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
+                               const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads,
+                               int32_t head_dim, const int32_t *page_table, int32_t page_table_len,
+                               const tf_seg *prefixes, int32_t n_prefixes, const tf_seg *prefixes_host,
+                               const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host,
+                               const int32_t *page_table_host, float scale, int32_t split_keys,
+                               int32_t n_prefix_splits, int32_t n_splits_max, void *workspace, size_t workspace_bytes,
+                               void *out, int32_t out_dtype, uint8_t *flags, uint32_t *status, tf_stream_t stream) {
+    if (n_rows_total < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_pages < 0 || page_table_len < 0 ||
+        n_prefixes < 0 || n_segs < 0 || split_keys < 0 || n_prefix_splits <= 0 || n_splits_max <= 0 ||
+        !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
+        return TF_ERR_ARG;
+    const int lp = log2_exact(page_size);
+    if (n_q_heads % n_kv_heads != 0 || !head_dim_ok(head_dim) || lp < 3 || lp > 10 ||
+        (split_keys > 0 && split_keys < 16) || n_segs > 65535 || n_prefixes > 65535 || n_splits_max > (1 << 24) ||
+        n_prefix_splits > (1 << 24))
+        return TF_ERR_UNSUPPORTED;
+    if (n_segs == 0 || n_rows_total == 0) return TF_OK;
+    if (!q || !k_pool || !v_pool || !page_table || (n_prefixes > 0 && !prefixes) || !segs || !workspace || !out ||
+        !flags || !status)
+        return TF_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(workspace))
+        return TF_ERR_ALIGN;
+    if (workspace_bytes < tf_paged_attn_shared_workspace_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits,
+                                                              n_splits_max))
+        return TF_ERR_WORKSPACE;
+    const int group = n_q_heads / n_kv_heads;
+    int max_rows = n_rows_total, own_splits = n_splits_max, own_split = split_keys;
+    int pre_rows = n_rows_total, pre_splits = n_prefix_splits, pre_split = split_keys;
+    // a table's checks, its split size and the partial slots it needs
+    auto plan = [&](const tf_seg *host, int n, bool full, int &rows, int &splits, int &split) -> tf_status {
+        const tf_status rc = check_segs_host(host, n, n_rows_total, page_table_len, page_size, n_pages,
+                                             page_table_host, split_keys, splits, &rows, full);
+        if (rc != TF_OK || rows == 0) return rc;
+        const int64_t q_tiles = full ? ((int64_t)rows * group + 127) / 128 : 1;
+        if (split == 0)
+            split = choose_split(host, n, n_kv_heads, (int64_t)device_sms() * 2 / std::min<int64_t>(q_tiles, 64) + 1,
+                                 full ? 1 : 2, 256, splits);
+        int longest = 1;
+        for (int s = 0; s < n; ++s)
+            if (host[s].n_rows > 0) longest = std::max(longest, (int)host[s].n_keys);
+        splits = (int)(((int64_t)longest + split - 1) / split);
+        return TF_OK;
+    };
+    if (segs_host) {
+        const tf_status rc = plan(segs_host, n_segs, false, max_rows, own_splits, own_split);
+        if (rc != TF_OK) return rc;
+    }
+    if (prefixes_host && n_prefixes > 0) {
+        const tf_status rc = plan(prefixes_host, n_prefixes, true, pre_rows, pre_splits, pre_split);
+        if (rc != TF_OK) return rc;
+        // a row belongs to one prefix
+        for (int a = 0; a < n_prefixes; ++a)
+            for (int b = 0; b < a; ++b) {
+                const tf_seg x = prefixes_host[a], y = prefixes_host[b];
+                if (x.n_rows > 0 && y.n_rows > 0 && x.q_row < y.q_row + y.n_rows && y.q_row < x.q_row + x.n_rows)
+                    return TF_ERR_ARG;
+            }
+    }
+    if (max_rows == 0) return TF_OK;
+    // what either partial launch would refuse, before the first one
+    const int64_t most_rows = n_prefixes > 0 ? std::max(max_rows, pre_rows) : max_rows;
+    if ((most_rows * group + 63) / 64 * n_kv_heads > 65535 || most_rows * n_q_heads > ((int64_t)1 << 31))
+        return TF_ERR_UNSUPPORTED;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    const PartBuffers pre = part_buffers(ws, n_rows_total, n_q_heads, head_dim, pre_splits);
+    const PartBuffers own = part_buffers(ws + part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits),
+                                         n_rows_total, n_q_heads, head_dim, own_splits);
+    if (n_prefixes > 0 && pre_rows > 0) {
+        const tf_status rc = paged_partials(true, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
+                                            n_kv_heads, head_dim, page_table, page_table_len, prefixes, n_prefixes,
+                                            prefixes_host, page_table_host, scale, pre_split, pre_splits, pre.o,
+                                            pre.m, pre.l, pre.flag, status, stream);
+        if (rc != TF_OK) return rc;
+    }
+    const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
+                                        n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
+                                        page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
+                                        status, stream);
+    if (rc != TF_OK) return rc;
+
+    MergeSegsParams m{};
+    m.own = PartSet{own.o, own.m, own.l, own.flag, own_splits, own_split};
+    m.prefix = PartSet{pre.o, pre.m, pre.l, pre.flag, pre_splits, pre_split};
+    m.segs = segs;
+    m.prefixes = prefixes;
+    m.n_segs = n_segs;
+    m.n_prefixes = n_prefixes;
+    m.max_rows = max_rows;
+    m.n_rows_total = n_rows_total;
+    m.hq = n_q_heads;
+    m.log2_page = lp;
+    m.pt_len = page_table_len;
+    m.out = out;
+    m.out_bf16 = out_dtype == TF_OUT_BF16;
+    m.flags = flags;
+    return cuda_status(launch_merge_segs(m, head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

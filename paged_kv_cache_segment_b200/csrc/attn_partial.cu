@@ -41,6 +41,7 @@
 
 #include "tf_common.cuh"
 #include "tf_internal.h"
+#include "tf_q8.cuh"
 
 namespace tfp {
 
@@ -66,7 +67,9 @@ struct Cfg {
     static constexpr int kSmemBytes = kQOffset + kQBytes;
 };
 
-enum class Src { kPaged, kRing };
+// kE4M3, kInt8: pages of an 8-bit cache, whose rows become the bf16 values they
+// stand for as they enter shared memory (exact, so everything after is the same)
+enum class Src { kPaged, kRing, kE4M3, kInt8 };
 
 struct WorkState {
     int s, g, c, q0, nq;
@@ -194,6 +197,9 @@ __device__ __forceinline__ void fold_tile(uint32_t sQ, uint32_t sK, uint32_t sV,
 template <int D, Src SRC, bool DIRECT>
 __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_kernel(const AttnParams p) {
     using C = Cfg<D>;
+    constexpr bool PAGED = SRC != Src::kRing;
+    constexpr bool Q8 = SRC == Src::kE4M3 || SRC == Src::kInt8;
+    constexpr int TYPE = SRC == Src::kInt8 ? TF_KV_INT8 : TF_KV_E4M3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ int s_pid[C::kStages + 1][kMaxPg];
     __shared__ uint32_t s_vbad[2];
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
 
     // ---- resolve the work item from the table --------------------------------
     int per;
-    if constexpr (SRC == Src::kPaged) {
+    if constexpr (PAGED) {
         const tf_seg sg = p.seg_inline ? p.seg0 : p.segs[w.s];
         w.q_row = sg.q_row;
         w.n_rows = sg.n_rows;
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
 
     // page ids of tile t into s_pid[slot] (paged source only)
     auto load_ids = [&](int t) {
-        if constexpr (SRC == Src::kPaged) {
+        if constexpr (PAGED) {
             if (tid < kMaxPg) {
                 const int kt = w.key_lo + t * kTK;
                 const int idx = (kt >> log2p) + tid;
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
             const int j = kt + row;
             bool ok = j < w.key_hi_eff;
             int64_t off = 0;
-            if constexpr (SRC == Src::kPaged) {
+            if constexpr (PAGED) {
                 const int pid = s_pid[t % (C::kStages + 1)][(j >> log2p) - (kt >> log2p)];
                 if (ok && pid < 0) {
                     bad_page = true;
@@ -341,6 +347,19 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
                 off = ((w.ring_base + sl) * p.hkv + w.g) * D + col * 8;
             }
             const uint32_t so = swz(row, col, C::kRowBytes);
+            if constexpr (Q8) {
+                uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
+                if (ok) {
+                    const uint2 kc = __ldg(reinterpret_cast<const uint2 *>(p.k_codes + off));
+                    const uint2 vc = __ldg(reinterpret_cast<const uint2 *>(p.v_codes + off));
+                    kx = q8_to_bf16x8<TYPE>(kc, e8m0_f32(__ldg(p.k_scale + off / D)));
+                    vx = q8_to_bf16x8<TYPE>(vc, e8m0_f32(__ldg(p.v_scale + off / D)));
+                }
+                unsigned char *st = smem + (t % C::kStages) * C::kStageBytes;
+                *reinterpret_cast<uint4 *>(st + so) = kx;
+                *reinterpret_cast<uint4 *>(st + C::kTileBytes + so) = vx;
+                continue;
+            }
             cp_async_16(stK + so, ok ? (const void *)(kg + off) : (const void *)kg, ok ? 16u : 0u);
             cp_async_16(stV + so, ok ? (const void *)(vg + off) : (const void *)vg, ok ? 16u : 0u);
         }
@@ -765,6 +784,8 @@ static cudaError_t launch_partial_d(const AttnParams &p, int head_dim, dim3 grid
 
 cudaError_t launch_attn_partial(const AttnParams &p, int head_dim, bool ring, bool direct, dim3 grid,
                                 cudaStream_t st) {
+    if (p.kv_type == TF_KV_E4M3) return launch_partial_d<Src::kE4M3, false>(p, head_dim, grid, st);
+    if (p.kv_type == TF_KV_INT8) return launch_partial_d<Src::kInt8, false>(p, head_dim, grid, st);
     if (ring) return launch_partial_d<Src::kRing, false>(p, head_dim, grid, st);
     if (direct) return launch_partial_d<Src::kPaged, true>(p, head_dim, grid, st);
     return launch_partial_d<Src::kPaged, false>(p, head_dim, grid, st);

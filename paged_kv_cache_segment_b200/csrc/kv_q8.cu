@@ -1,0 +1,243 @@
+// kv_q8.cu - the 8-bit cache written and read: new K/V rows quantised into
+// their pages (tf_kv_append_q8) and cached keys read back into bf16 pages
+// (tf_kv_read_q8).
+//
+// Both move rows and do next to no arithmetic: per (row, kv-head) of K and of V
+// 2 D bytes of bf16 on one side and D + 1 bytes on the other, so HBM bounds
+// them (and the launch, for a decode step's few rows).  A group of D / 8 lanes
+// owns a (row, kv-head): every lane moves one 16-byte chunk of bf16 of K and
+// one of V and the 8-byte runs of codes they become, so each side is whole
+// contiguous runs of D (codes) or 2 D (bf16) bytes and both tensors' loads are
+// in flight at once.  The row's largest magnitude is an integer maximum of the
+// bf16 magnitude patterns over the group (its order is the values' order, and
+// the all-ones exponent of a NaN or an infinity tops every finite pattern).
+#include <climits>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "api_common.h"
+#include "tf_internal.h"
+#include "tf_q8.cuh"
+
+namespace tfp {
+namespace {
+
+constexpr int kQ8Threads = 256;
+
+struct KvQ8Params {
+    const uint16_t *k_rows, *v_rows;  // append: bf16 [n_rows_total][hkv][D]
+    uint8_t *k_codes, *v_codes;       // u8 [n_pages][hkv][P][D]
+    uint8_t *k_scale, *v_scale;       // u8 [n_pages][hkv][P]
+    uint16_t *k_pool, *v_pool;        // read: bf16 [n_pages_dst][hkv][P][D]
+    int n_rows_total, hkv, n_pages, n_pages_dst, log2_page, pt_len;
+    const int32_t *page_table, *dst_page_table;
+    const tf_seg *segs;
+    uint32_t *status;
+};
+
+// Stream blockIdx.y's entry; false (and the status bit) when it is bad.
+__device__ __forceinline__ bool kv_q8_seg(const KvQ8Params &p, bool rows_used, tf_seg &e) {
+    e = p.segs[blockIdx.y];
+    uint32_t bit = 0;
+    if ((rows_used && (e.q_row < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total)) || e.n_rows < 0 ||
+        e.n_keys < e.n_rows || e.pt_base < 0 || e.n_pages < 0 || (int64_t)e.pt_base + e.n_pages > p.pt_len)
+        bit = TF_DEV_BAD_SEG;
+    else if ((int64_t)e.n_keys > ((int64_t)e.n_pages << p.log2_page))
+        bit = TF_DEV_PAST_PAGES;
+    if (bit && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, bit);
+    return bit == 0;
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kQ8Threads) kv_append_q8_kernel(const KvQ8Params p) {
+    constexpr int L = D / 8;  // lanes of a group
+    tf_seg e;
+    if (!kv_q8_seg(p, true, e)) return;
+    const int lane = threadIdx.x % L;
+    const int64_t n_units = (int64_t)e.n_rows * p.hkv;
+    const int64_t u = (int64_t)blockIdx.x * (kQ8Threads / L) + threadIdx.x / L;  // (row, kv-head) of this group
+    const bool live = u < n_units;
+    const int i = live ? (int)(u / p.hkv) : 0, g = live ? (int)(u - (int64_t)i * p.hkv) : 0;
+    const int j = e.n_keys - e.n_rows + i;
+    int page = -1;
+    if (live) page = p.page_table[e.pt_base + (j >> p.log2_page)];
+    const bool ok = live && page >= 0 && page < p.n_pages;
+    if (live && !ok && lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
+    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (ok) {
+        const int64_t src = ((int64_t)(e.q_row + i) * p.hkv + g) * D + lane * 8;
+        x[0] = __ldg(reinterpret_cast<const uint4 *>(p.k_rows + src));
+        x[1] = __ldg(reinterpret_cast<const uint4 *>(p.v_rows + src));
+    }
+    const int64_t slot = (((int64_t)page * p.hkv + g) << p.log2_page) | (j & ((1 << p.log2_page) - 1));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const bool nf = amax >= 0x7f80u;
+        const int k2 = q8_exponent<TYPE>(amax);
+        const float s = __uint_as_float((uint32_t)(kE8Bias - k2) << 23);  // 2^-k2, exact
+        uint2 c;
+        c.x = q8_encode4<TYPE>(bf16_lo_to_f32(w[0]) * s, bf16_hi_to_f32(w[0]) * s, bf16_lo_to_f32(w[1]) * s,
+                               bf16_hi_to_f32(w[1]) * s);
+        c.y = q8_encode4<TYPE>(bf16_lo_to_f32(w[2]) * s, bf16_hi_to_f32(w[2]) * s, bf16_lo_to_f32(w[3]) * s,
+                               bf16_hi_to_f32(w[3]) * s);
+        if (nf) c = make_uint2(0u, 0u);
+        if (ok) {
+            reinterpret_cast<uint2 *>((t ? p.v_codes : p.k_codes) + slot * D)[lane] = c;
+            if (lane == 0) (t ? p.v_scale : p.k_scale)[slot] = (uint8_t)(nf ? kE8Nan : (uint32_t)(k2 + kE8Bias));
+        }
+    }
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kQ8Threads) kv_read_q8_kernel(const KvQ8Params p) {
+    constexpr int L = D / 8;
+    tf_seg e;
+    if (!kv_q8_seg(p, false, e)) return;
+    const int lane = threadIdx.x % L;
+    const int64_t u = (int64_t)blockIdx.x * (kQ8Threads / L) + threadIdx.x / L;
+    if (u >= (int64_t)e.n_rows * p.hkv) return;
+    const int i = (int)(u / p.hkv), g = (int)(u - (int64_t)i * p.hkv);
+    const int j = e.n_keys - e.n_rows + i, at = e.pt_base + (j >> p.log2_page);
+    const int page = p.page_table[at], to = p.dst_page_table[at];
+    if (page < 0 || page >= p.n_pages || to < 0 || to >= p.n_pages_dst) {
+        if (lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
+        return;
+    }
+    const int in_page = j & ((1 << p.log2_page) - 1);
+    const int64_t src = (((int64_t)page * p.hkv + g) << p.log2_page) | in_page;
+    const int64_t dst = (((int64_t)to * p.hkv + g) << p.log2_page) | in_page;
+    const uint2 ck = __ldg(reinterpret_cast<const uint2 *>(p.k_codes + src * D) + lane);
+    const uint2 cv = __ldg(reinterpret_cast<const uint2 *>(p.v_codes + src * D) + lane);
+    const float sk = e8m0_f32(__ldg(p.k_scale + src)), sv = e8m0_f32(__ldg(p.v_scale + src));
+    reinterpret_cast<uint4 *>(p.k_pool + dst * D)[lane] = q8_to_bf16x8<TYPE>(ck, sk);
+    reinterpret_cast<uint4 *>(p.v_pool + dst * D)[lane] = q8_to_bf16x8<TYPE>(cv, sv);
+}
+
+template <int D, int TYPE>
+cudaError_t launch_kv_q8(const KvQ8Params &p, bool read, int n_segs, int max_rows, cudaStream_t st) {
+    constexpr int kGroups = kQ8Threads / (D / 8);
+    const int64_t units = (int64_t)max_rows * p.hkv;
+    const dim3 grid((unsigned)((units + kGroups - 1) / kGroups), (unsigned)n_segs);
+    if (read)
+        kv_read_q8_kernel<D, TYPE><<<grid, kQ8Threads, 0, st>>>(p);
+    else
+        kv_append_q8_kernel<D, TYPE><<<grid, kQ8Threads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int TYPE>
+cudaError_t launch_kv_q8_d(const KvQ8Params &p, bool read, int head_dim, int n_segs, int max_rows, cudaStream_t st) {
+    switch (head_dim) {
+        case 64: return launch_kv_q8<64, TYPE>(p, read, n_segs, max_rows, st);
+        case 128: return launch_kv_q8<128, TYPE>(p, read, n_segs, max_rows, st);
+        case 256: return launch_kv_q8<256, TYPE>(p, read, n_segs, max_rows, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_kv_q8_t(const KvQ8Params &p, bool read, const tf_q8_cache &c, int n_segs, int max_rows,
+                           cudaStream_t st) {
+    return c.kv_type == TF_KV_E4M3 ? launch_kv_q8_d<TF_KV_E4M3>(p, read, c.head_dim, n_segs, max_rows, st)
+                                   : launch_kv_q8_d<TF_KV_INT8>(p, read, c.head_dim, n_segs, max_rows, st);
+}
+
+KvQ8Params cache_params(const tf_q8_cache &c) {
+    KvQ8Params p{};
+    p.k_codes = static_cast<uint8_t *>(c.k_codes);
+    p.v_codes = static_cast<uint8_t *>(c.v_codes);
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.hkv = c.n_kv_heads;
+    p.n_pages = c.n_pages;
+    p.log2_page = log2_exact(c.page_size);
+    return p;
+}
+
+}  // namespace
+}  // namespace tfp
+
+using namespace tfp;
+
+extern "C" {
+
+tf_status tf_kv_append_q8(const void *k_rows, const void *v_rows, int32_t n_rows_total,
+                          const tf_q8_cache *cache_host, const int32_t *page_table, int32_t page_table_len,
+                          const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host, const int32_t *page_table_host,
+                          uint32_t *status, tf_stream_t stream) {
+    if (!cache_host || n_rows_total < 0 || page_table_len < 0 || n_segs < 0) return TF_ERR_ARG;
+    const tf_q8_cache c = *cache_host;
+    tf_status rc = check_q8_shape(c);
+    if (rc != TF_OK) return rc;
+    if (n_segs > 65535) return TF_ERR_UNSUPPORTED;
+    if (n_segs == 0 || n_rows_total == 0) return TF_OK;
+    if (!k_rows || !v_rows || !page_table || !segs || !status || !q8_pointers(c)) return TF_ERR_ARG;
+    if (!aligned16(k_rows) || !aligned16(v_rows) || !q8_aligned(c)) return TF_ERR_ALIGN;
+    int max_rows = n_rows_total;
+    if (segs_host) {
+        rc = check_segs_host(segs_host, n_segs, n_rows_total, page_table_len, c.page_size, c.n_pages, page_table_host,
+                             0, 0, &max_rows);
+        if (rc != TF_OK) return rc;
+        if (max_rows == 0) return TF_OK;
+    }
+    if ((int64_t)max_rows * c.n_kv_heads > ((int64_t)1 << 33)) return TF_ERR_UNSUPPORTED;
+    KvQ8Params p = cache_params(c);
+    p.k_rows = static_cast<const uint16_t *>(k_rows);
+    p.v_rows = static_cast<const uint16_t *>(v_rows);
+    p.n_rows_total = n_rows_total;
+    p.pt_len = page_table_len;
+    p.page_table = page_table;
+    p.segs = segs;
+    p.status = status;
+    return cuda_status(launch_kv_q8_t(p, false, c, n_segs, max_rows, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *page_table, int32_t page_table_len,
+                        const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host, const int32_t *page_table_host,
+                        void *k_pool, void *v_pool, int32_t n_pages_dst, const int32_t *dst_page_table,
+                        const int32_t *dst_page_table_host, uint32_t *status, tf_stream_t stream) {
+    if (!cache_host || page_table_len < 0 || n_segs < 0 || n_pages_dst < 0) return TF_ERR_ARG;
+    const tf_q8_cache c = *cache_host;
+    tf_status rc = check_q8_shape(c);
+    if (rc != TF_OK) return rc;
+    if (n_segs > 65535) return TF_ERR_UNSUPPORTED;
+    if (n_segs == 0) return TF_OK;
+    if (!page_table || !dst_page_table || !segs || !status || !k_pool || !v_pool || !q8_pointers(c)) return TF_ERR_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !q8_aligned(c)) return TF_ERR_ALIGN;
+    // without a host table a stream may have as many keys as its pages hold
+    int64_t max_rows = (int64_t)page_table_len * c.page_size;
+    if (segs_host) {
+        max_rows = 0;
+        for (int s = 0; s < n_segs; ++s) {
+            tf_seg e = segs_host[s];
+            e.q_row = 0;  // not used by this call
+            int rows = 0;
+            rc = check_segs_host(&e, 1, INT_MAX, page_table_len, c.page_size, c.n_pages, page_table_host, 0, 0, &rows);
+            if (rc == TF_OK && dst_page_table_host)
+                rc = check_segs_host(&e, 1, INT_MAX, page_table_len, c.page_size, n_pages_dst, dst_page_table_host, 0,
+                                     0, &rows);
+            if (rc != TF_OK) return rc;
+            if (rows > max_rows) max_rows = rows;
+        }
+    }
+    if (max_rows == 0) return TF_OK;
+    if (max_rows > INT_MAX) max_rows = INT_MAX;
+    if (max_rows * c.n_kv_heads > ((int64_t)1 << 33)) return TF_ERR_UNSUPPORTED;
+    KvQ8Params p = cache_params(c);
+    p.k_pool = static_cast<uint16_t *>(k_pool);
+    p.v_pool = static_cast<uint16_t *>(v_pool);
+    p.n_pages_dst = n_pages_dst;
+    p.pt_len = page_table_len;
+    p.page_table = page_table;
+    p.dst_page_table = dst_page_table;
+    p.segs = segs;
+    p.status = status;
+    return cuda_status(launch_kv_q8_t(p, true, c, n_segs, (int)max_rows, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -14,6 +14,9 @@ struct AttnParams {
     const uint16_t *q;
     int n_rows_total, hq, hkv, group;
     const uint16_t *k, *v;  // pool [pages][Hkv][P][D] or ring [slots][Hkv][D]
+    // an 8-bit cache (kv_type TF_KV_*, 0: none): codes [pages][Hkv][P][D], scale bytes [pages][Hkv][P]
+    const uint8_t *k_codes, *v_codes, *k_scale, *v_scale;
+    int kv_type;
     // paged source
     int n_pages, log2_page, pt_len;
     const int32_t *page_table;
@@ -128,6 +131,36 @@ struct ArgmaxParams {
 // and tensor-core kernels launched on this host thread issue no loads and
 // give up their bounded waits after this many nanoseconds (0: hook off).
 uint64_t test_wait_runout_ns();
+
+// Split-KV partials of tf_paged_attn_decode / tf_paged_attn_block, arguments
+// checked (csrc/api.cu).
+tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
+                         const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                         const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
+                         const tf_seg *segs_host, const int32_t *page_table_host, float scale, int32_t split_keys,
+                         int32_t n_splits_max, float *part_o, float *part_m, float *part_l, uint8_t *part_flag,
+                         uint32_t *status, tf_stream_t stream);
+
+// Partials of one kind for the merge of tf_paged_attn_q8 and
+// tf_paged_attn_shared: arrays [n_rows_total][hq][n_splits](*D), of which a row
+// of an entry with N keys has ceil(N / len), len being the split rule's.
+struct PartSet {
+    const float *o, *m, *l;
+    const uint8_t *flag;
+    int n_splits, split_keys;
+};
+struct MergeSegsParams {
+    PartSet own, prefix;
+    const tf_seg *segs, *prefixes;
+    int n_segs, n_prefixes;  // n_prefixes = 0: no prefix partials
+    int max_rows;            // rows a stream has at most
+    int n_rows_total, hq, log2_page, pt_len;
+    int full;
+    void *out;
+    int out_bf16;
+    uint8_t *flags;
+};
+cudaError_t launch_merge_segs(const MergeSegsParams &p, int head_dim, cudaStream_t st);
 
 cudaError_t launch_attn_partial(const AttnParams &p, int head_dim, bool ring, bool direct, dim3 grid,
                                 cudaStream_t st);

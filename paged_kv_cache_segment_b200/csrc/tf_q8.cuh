@@ -1,0 +1,98 @@
+// tf_q8.cuh - the 8-bit cache's number format on the device: codes (e4m3 or
+// signed bytes) to f16 and bf16, scale bytes to floats, and a row's scale.
+//
+// An element is code * 2^(e - 127).  A code has at most 8 significant bits,
+// so it is exact in f16, and code * 2^(e - 127) is exact in bf16 for every
+// scale byte an append writes (27 to 249).
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/tfserve.h"
+#include "tf_common.cuh"
+
+namespace tfp {
+
+constexpr int kE8Bias = 127;
+constexpr int kE8MinExp = -100;   // the smallest exponent an append writes
+constexpr uint32_t kE8Nan = 255;  // the scale byte of a row that held a NaN or an infinity
+
+// 2^(e - 127) (e = 0: the subnormal 2^-127), NaN for 255.
+__device__ __forceinline__ float e8m0_f32(uint32_t e) {
+    return __uint_as_float(e == kE8Nan ? 0x7fc00000u : (e == 0 ? 0x00400000u : e << 23));
+}
+
+// Four codes (a 32-bit word, lowest byte first) to f16 pairs (0, 1) and (2, 3).
+template <int TYPE>
+__device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t &p01, uint32_t &p23) {
+    if constexpr (TYPE == TF_KV_E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(p01), "=r"(p23)
+            : "r"(w));
+    } else {
+        // u = code + 128 as a byte under the exponent of 1,024: f16 1,024 + u, less 1,152
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p01) : "r"(a), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p23) : "r"(b), "r"(0x64806480u));
+    }
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t p) {
+    __half2 h;
+    *reinterpret_cast<uint32_t *>(&h) = p;
+    return __half22float2(h);
+}
+
+// Eight codes times s (a power of two) as bf16: exact (see above).
+template <int TYPE>
+__device__ __forceinline__ uint4 q8_to_bf16x8(uint2 w, float s) {
+    uint32_t p[4];
+    q8_to_f16<TYPE>(w.x, p[0], p[1]);
+    q8_to_f16<TYPE>(w.y, p[2], p[3]);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = f16x2_to_f32(p[i]);
+        r[i] = pack_bf16x2(f.x * s, f.y * s);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The scale exponent of a row whose largest magnitude has these bf16 bits
+// (finite, sign cleared): the smallest k >= -100 with amax <= Q * 2^k.  With
+// amax = 1.f * 2^(E - 127) and Q = 1.75 * 2^8 (448) or 1.984375 * 2^6 (127),
+// k is E - 127 less Q's exponent, and one more when 1.f is above Q's mantissa.
+template <int TYPE>
+__device__ __forceinline__ int q8_exponent(uint32_t amax) {
+    const int E = (int)(amax >> 7), man = (int)(amax & 0x7fu);
+    const int k = TYPE == TF_KV_E4M3 ? E - 127 - 8 + (man > 0x60 ? 1 : 0) : E - 127 - 6 + (man > 0x7e ? 1 : 0);
+    return k > kE8MinExp ? k : kE8MinExp;
+}
+
+// Four values already scaled into the code range, to codes (nearest, ties to
+// even; lowest byte first).
+template <int TYPE>
+__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d) {
+    if constexpr (TYPE == TF_KV_E4M3) {
+        uint32_t r;
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+            "mov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
+        return r;
+    } else {
+        const uint32_t x = (uint32_t)__float2int_rn(a), y = (uint32_t)__float2int_rn(b);
+        const uint32_t z = (uint32_t)__float2int_rn(c), w = (uint32_t)__float2int_rn(d);
+        return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+    }
+}
+
+}  // namespace tfp
