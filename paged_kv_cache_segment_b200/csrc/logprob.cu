@@ -6,23 +6,27 @@
 //   log p(x) = scale * d - ln l,  lse = scale * m + ln l,  H = ln l - scale * t / l.
 // d <= 0, so both terms of H are >= 0 and nothing cancels; d is exact or rounded
 // once, where x * c - m * c would carry the rounding of m * c into every term.
+// Every thread keeps its own m, l and t; they are joined once a row.
 //
 // A CTA (512 threads) owns a row's columns, or 1/CL of them with a cluster of CL
 // CTAs a row when there are few rows.  It walks them in chunks that a thread
 // holds in registers (four 16-byte vectors), the next chunk's loads in flight
-// while the current one folds, across the row's end too.  Vectors are aligned to
-// 16 bytes whatever the row's own alignment: the grid of vectors starts up to 15
-// bytes before the row, and only the vectors that cross its ends load by element.
+// while the current one folds, across the row's end too, and without a barrier
+// inside the row.  Vectors are aligned to 16 bytes whatever the row's own
+// alignment: the grid of vectors starts up to 15 bytes before the row, and only
+// the vectors that cross its ends load by element.
 //
 // Top k: elements are ordered by a 64-bit key, the value's order-preserving image
 // above the complement of the column, so keys are distinct and ties go to the
-// lower column.  The 32 half-warps keep the largest key each has seen; the
-// smallest of those 32 is a threshold that at least 32 >= k elements reach, so
-// only elements at or above it can be among the top k.  They are few (a few
-// dozen to a few hundred of a row) and go to a list in shared memory, from which
-// the k largest are ranked by counting.  A chunk that would overflow the list (a
-// half-warp that holds only masked columns leaves the threshold at nothing) is
-// searched by k block-wide maxima instead: slower, but never wrong.
+// lower column.  During the pass a thread keeps only its largest value.  The k-th
+// largest of the 128 largest values of groups of four threads is a threshold
+// that at least k elements reach, and few others do (some k + k^2 / 256 of random
+// rows): only the threads whose own maximum reaches it read their columns again,
+// from L2, and put the elements that do on a list in shared memory, which is
+// ranked by counting.  Should the list overflow (a thousand columns tied at the
+// threshold), the k largest keys are taken one at a time: every thread holds its
+// best remaining key, and after each block-wide maximum only the thread that held
+// it looks for its next one.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -43,10 +47,11 @@ constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpBatch = 4;       // 16-byte vectors a thread holds of a chunk
 constexpr int kLpMaxTop = 32;
-constexpr int kLpGroups = 2 * kLpWarps;  // half-warps, each with its largest key
-constexpr int kLpList = 1024;            // candidates of a row
+constexpr int kLpGroups = kLpThreads / 4;  // groups of four threads, each with its largest value
+constexpr int kLpList = 1024;              // candidates of a row's columns in a CTA
 constexpr int kLpMaxCluster = 8;
-static_assert(kLpGroups >= kLpMaxTop, "the threshold needs a group for every alternative");
+// With fewer columns than would fill kLpMaxTop groups, the list holds them all.
+static_assert(kLpMaxTop * 4 * 8 <= kLpList, "a row without k filled groups must fit the list");
 
 struct LogprobParams {
     const void *logits;
@@ -105,16 +110,49 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
 }
 
 // Ranks the n distinct keys of `list` and puts the k largest, largest first,
-// into `top` (0 past the n-th).  The whole CTA calls it.
+// into `top` (0 past the n-th): a warp a key, 32 of the others at a time.
 __device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uint64_t *top) {
-    for (int i = threadIdx.x; i < n; i += kLpThreads) {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {
         const uint64_t mine = list[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += list[j] > mine ? 1 : 0;
-        if (rank < k) top[rank] = mine;
+        for (int j = 0; j < n; j += 32)
+            rank += __popc(__ballot_sync(0xffffffffu, j + lane < n && list[min(j + lane, n - 1)] > mine));
+        if (lane == 0 && rank < k) top[rank] = mine;
     }
     for (int i = n + threadIdx.x; i < k; i += kLpThreads) top[i] = 0ull;
 }
+
+// Two floats as one 64-bit operand of the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpk2(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A masked column (-infinity) enters the sums as this finite value, whose term
+// is 0 and whose product with 0 is 0; x - m cannot overflow from it.  It also
+// stands in for logits below it, so a thread whose maximum is not far above it
+// takes the careful form instead.
+constexpr float kLpFloor = -0x1p126f, kLpCareful = -0x1p125f;
 
 template <typename T>
 struct Elem;
@@ -122,6 +160,14 @@ template <>
 struct Elem<float> {
     static constexpr int kPer = 4;  // elements of a 16-byte vector
     static __device__ __forceinline__ float get(const uint32_t (&w)[4], int e) { return __uint_as_float(w[e]); }
+    // elements 2 i and 2 i + 1, no lower than kLpFloor (a NaN stays)
+    static __device__ __forceinline__ uint64_t pair(const uint32_t (&w)[4], int i) {
+        return pk2(max_nan(get(w, 2 * i), kLpFloor), max_nan(get(w, 2 * i + 1), kLpFloor));
+    }
+    // the largest of a vector's elements (NaN ignored)
+    static __device__ __forceinline__ float most(const uint32_t (&w)[4]) {
+        return fmaxf(fmaxf(get(w, 0), get(w, 1)), fmaxf(get(w, 2), get(w, 3)));
+    }
     static __device__ __forceinline__ float load(const float *p) { return __ldg(p); }
     static __device__ __forceinline__ void put(uint32_t (&w)[4], int e, float x) { w[e] = __float_as_uint(x); }
 };
@@ -130,6 +176,18 @@ struct Elem<uint16_t> {
     static constexpr int kPer = 8;
     static __device__ __forceinline__ float get(const uint32_t (&w)[4], int e) {
         return (e & 1) ? bf16_hi_to_f32(w[e >> 1]) : bf16_lo_to_f32(w[e >> 1]);
+    }
+    static __device__ __forceinline__ uint64_t pair(const uint32_t (&w)[4], int i) {
+        uint32_t y;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[i]), "r"(0xfe80fe80u));  // kLpFloor in bf16
+        return pk2(bf16_lo_to_f32(y), bf16_hi_to_f32(y));
+    }
+    static __device__ __forceinline__ float most(const uint32_t (&w)[4]) {
+        uint32_t a, b;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+        return fmaxf(bf16_lo_to_f32(a), bf16_hi_to_f32(a));
     }
     static __device__ __forceinline__ float load(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
     static __device__ __forceinline__ void put(uint32_t (&w)[4], int e, float x) {
@@ -146,7 +204,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
     const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __shared__ Stat w_stat[kLpWarps];
-    __shared__ uint64_t s_group[2][kLpGroups];
+    __shared__ float s_group[TOP ? kLpGroups : 1], s_tau;
     __shared__ uint64_t s_list[TOP ? kLpList : 1], s_top[kLpMaxTop], s_best[kLpWarps];
     __shared__ int s_n;
     // rank 0's slots, filled by every CTA of the cluster, two buffers by row parity
@@ -172,27 +230,27 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
         w.n_chunks = max(1, (w.v1 - w.v0 + kLpBatch * kLpThreads - 1) / (kLpBatch * kLpThreads));
         return w;
     };
-    auto load = [&](const Row &w, int chunk, uint32_t (&x)[kLpBatch][4]) {
+    // vector v of a row; columns outside the row (and vectors past this CTA's) are masked
+    auto load_vec = [&](const Row &w, int v, uint32_t (&x)[4]) {
+        const int c0 = v * EPV - w.mis;
+        if (v < w.v1 && c0 >= 0 && c0 + EPV <= p.n_cols) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(w.at + c0));
+            x[0] = y.x;
+            x[1] = y.y;
+            x[2] = y.z;
+            x[3] = y.w;
+        } else {
+            x[0] = x[1] = x[2] = x[3] = EPV == 4 ? 0xff800000u : 0xff80ff80u;
+            if (v < w.v1) {
 #pragma unroll
-        for (int k = 0; k < kLpBatch; ++k) {
-            const int v = w.v0 + (chunk * kLpBatch + k) * kLpThreads + tid;
-            const int c0 = v * EPV - w.mis;
-            if (v < w.v1 && c0 >= 0 && c0 + EPV <= p.n_cols) {
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(w.at + c0));
-                x[k][0] = y.x;
-                x[k][1] = y.y;
-                x[k][2] = y.z;
-                x[k][3] = y.w;
-            } else {
-                const uint32_t none = EPV == 4 ? 0xff800000u : 0xff80ff80u;
-                x[k][0] = x[k][1] = x[k][2] = x[k][3] = none;
-                if (v < w.v1) {
-#pragma unroll
-                    for (int e = 0; e < EPV; ++e)
-                        if (c0 + e >= 0 && c0 + e < p.n_cols) E::put(x[k], e, E::load(w.at + c0 + e));
-                }
+                for (int e = 0; e < EPV; ++e)
+                    if (c0 + e >= 0 && c0 + e < p.n_cols) E::put(x, e, E::load(w.at + c0 + e));
             }
         }
+    };
+    auto load = [&](const Row &w, int chunk, uint32_t (&x)[kLpBatch][4]) {
+#pragma unroll
+        for (int k = 0; k < kLpBatch; ++k) load_vec(w, w.v0 + (chunk * kLpBatch + k) * kLpThreads + tid, x[k]);
     };
 
     uint32_t cur[kLpBatch][4], nxt[kLpBatch][4];
@@ -205,7 +263,6 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
     load(w, 0, cur);
     for (; row < p.n_rows; row += gridDim.y, ++it) {
         Stat st{-INFINITY, 0.f, 0.f};
-        uint64_t group_best = 0, tau = 0;  // this half-warp's largest key, the threshold
         const int next_row = row + (int)gridDim.y;
         Row wn = w;
         if constexpr (TOP) {
@@ -219,126 +276,123 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
                 wn = open(next_row);
                 load(wn, 0, nxt);
             }
-            // ---- statistics
             float mx = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) mx = fmaxf(mx, E::get(cur[k], e));
+            for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(cur[k]));
             if (mx > st.m) st.to(mx, c);
-            // (all masked so far: the reference is 0, every term 2^-inf = 0 or a NaN)
-            const float ref = st.m == -INFINITY ? 0.f : st.m;
+            if (st.m > kLpCareful || st.m == -INFINITY) {
+                // (all masked so far: the reference is 0, every term 0 or a NaN)
+                const float ref = st.m == -INFINITY ? 0.f : -st.m;
+                const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
+                uint64_t l2 = pk2(st.l, 0.f), t2 = pk2(st.t, 0.f);
 #pragma unroll
-            for (int k = 0; k < kLpBatch; ++k)
+                for (int k = 0; k < kLpBatch; ++k)
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    const float d = max_nan(E::get(cur[k], e) - ref, -FLT_MAX);  // a masked column: 0 * finite
-                    const float q = ex2(d * c);
-                    st.l += q;
-                    st.t = fmaf(q, d, st.t);
-                }
-            if constexpr (TOP) {
-                // ---- candidates of this chunk
-                auto col_of = [&](int k, int e) {
-                    return (w.v0 + (ch * kLpBatch + k) * kLpThreads + tid) * EPV - w.mis + e;
-                };
-                uint64_t best = 0;
-                if (key32(mx) != 0u && key32(mx) >= (uint32_t)(tau >> 32)) {
-                    int col = INT_MAX;
-#pragma unroll
-                    for (int k = kLpBatch - 1; k >= 0; --k)
-#pragma unroll
-                        for (int e = EPV - 1; e >= 0; --e)
-                            if (E::get(cur[k], e) == mx) col = col_of(k, e);
-                    best = key64(mx, col);
-                }
-                uint64_t gb = best;
-#pragma unroll
-                for (int o = 8; o; o >>= 1) {
-                    const uint64_t y = __shfl_xor_sync(0xffffffffu, gb, o);
-                    gb = y > gb ? y : gb;
-                }
-                group_best = gb > group_best ? gb : group_best;
-                if ((lane & 15) == 0) s_group[ch & 1][warp * 2 + (lane >> 4)] = group_best;
-                __syncthreads();
-                const int n_before = s_n;
-                tau = s_group[ch & 1][lane];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    const uint64_t y = __shfl_xor_sync(0xffffffffu, tau, o);
-                    tau = y < tau ? y : tau;
-                }
-                __syncthreads();  // every thread has read s_n
-                if (best != 0 && best >= tau) {
-#pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e) {
-                            const uint64_t y = key64(E::get(cur[k], e), col_of(k, e));
-                            if (y != 0 && y >= tau) {
-                                const int at = atomicAdd(&s_n, 1);
-                                if (at < kLpList) s_list[at] = y;
-                            }
-                        }
-                }
-                __syncthreads();
-                if (s_n > kLpList) {
-                    // too many: k block-wide maxima over the chunk and the list as it was
-                    uint64_t last = ~0ull;
-                    for (int q = 0; q < K; ++q) {
-                        uint64_t b = 0;
-#pragma unroll
-                        for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                            for (int e = 0; e < EPV; ++e) {
-                                const uint64_t y = key64(E::get(cur[k], e), col_of(k, e));
-                                if (y < last && y > b) b = y;
-                            }
-                        for (int i = tid; i < n_before; i += kLpThreads) {
-                            const uint64_t y = s_list[i];
-                            if (y < last && y > b) b = y;
-                        }
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) {
-                            const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
-                            b = y > b ? y : b;
-                        }
-                        if (lane == 0) s_best[warp] = b;
-                        __syncthreads();
-#pragma unroll
-                        for (int i = 0; i < kLpWarps; ++i) b = s_best[i] > b ? s_best[i] : b;
-                        if (tid == 0) s_top[q] = b;
-                        last = b;
-                        __syncthreads();
-                        if (b == 0) {  // no more elements
-                            for (int i = q + 1 + tid; i < K; i += kLpThreads) s_top[i] = 0ull;
-                            break;
-                        }
+                    for (int e = 0; e < EPV / 2; ++e) {
+                        const uint64_t d2 = add2(E::pair(cur[k], e), ref2);
+                        float y0, y1;
+                        unpk2(mul2(d2, c2), y0, y1);
+                        const uint64_t q2 = pk2(ex2(y0), ex2(y1));
+                        l2 = add2(l2, q2);
+                        t2 = fma2(q2, d2, t2);
                     }
-                    __syncthreads();
-                    if (tid < K) s_list[tid] = s_top[tid];
-                    __syncthreads();
-                    if (tid == 0) {
-                        int n = 0;
-                        while (n < K && s_list[n] != 0) ++n;
-                        s_n = n;
+                float a, b;
+                unpk2(l2, a, b);
+                st.l = a + b;
+                unpk2(t2, a, b);
+                st.t = a + b;
+            } else {
+#pragma unroll
+                for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e) {
+                        const float d = max_nan(E::get(cur[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
+                        const float q = ex2(d * c);
+                        st.l += q;
+                        st.t = fmaf(q, d, st.t);
                     }
-                    __syncthreads();
-                } else if (s_n > kLpList / 2 && ch + 1 < w.n_chunks) {
-                    // keep the k largest
-                    const int n = s_n;
-                    rank_top(s_list, n, K, s_top);
-                    __syncthreads();
-                    if (tid < K) s_list[tid] = s_top[tid];
-                    if (tid == 0) s_n = K;
-                    __syncthreads();
-                }
             }
             if (ch + 1 < w.n_chunks) {
 #pragma unroll
                 for (int k = 0; k < kLpBatch; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) cur[k][e] = nxt[k][e];
+            }
+        }
+        if constexpr (TOP) {
+            const float mine = st.m;  // this thread's largest logit
+            // ---- the threshold: the K-th largest of the groups' largest values
+            float gm = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+            if ((lane & 3) == 0) s_group[tid >> 2] = gm;
+            __syncthreads();
+            {
+                float v[kLpGroups / 32];
+#pragma unroll
+                for (int i = 0; i < kLpGroups / 32; ++i) v[i] = s_group[32 * i + lane];
+#pragma unroll
+                for (int j = 0; j < kLpGroups / kLpWarps; ++j) {
+                    const int at = warp * (kLpGroups / kLpWarps) + j;
+                    const float x = s_group[at];
+                    int rank = 0;
+#pragma unroll
+                    for (int i = 0; i < kLpGroups / 32; ++i)  // equal values rank by place
+                        rank += __popc(__ballot_sync(0xffffffffu, v[i] > x || (v[i] == x && 32 * i + lane < at)));
+                    if (lane == 0 && rank == K - 1) s_tau = x;
+                }
+            }
+            __syncthreads();
+            const float tau = s_tau;
+            // ---- the threads that reach it go over their columns again
+            auto scan = [&](auto &&f) {  // f(value, column) for every unmasked column of this thread
+                for (int v = w.v0 + tid; v < w.v1; v += kLpBatch * kLpThreads) {
+                    uint32_t x[kLpBatch][4];
+#pragma unroll
+                    for (int k = 0; k < kLpBatch; ++k) load_vec(w, v + k * kLpThreads, x[k]);
+#pragma unroll
+                    for (int k = 0; k < kLpBatch; ++k) {
+                        const int c0 = (v + k * kLpThreads) * EPV - w.mis;
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e) f(E::get(x[k], e), c0 + e);
+                    }
+                }
+            };
+            if (mine >= tau && mine > -INFINITY)
+                scan([&](float x, int col) {
+                    if (x >= tau && x > -INFINITY) {
+                        const int at = atomicAdd(&s_n, 1);
+                        if (at < kLpList) s_list[at] = key64(x, col);
+                    }
+                });
+            __syncthreads();
+            if (s_n > kLpList) {
+                // one at a time: the largest key below the last one taken
+                uint64_t best = 0;
+                auto look = [&](uint64_t below) {
+                    best = 0;
+                    scan([&](float x, int col) {
+                        const uint64_t y = key64(x, col);
+                        if (y < below && y > best) best = y;
+                    });
+                };
+                look(~0ull);
+                for (int q = 0; q < K; ++q) {
+                    uint64_t b = best;
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) {
+                        const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
+                        b = y > b ? y : b;
+                    }
+                    if (lane == 0) s_best[warp] = b;
+                    __syncthreads();
+#pragma unroll
+                    for (int i = 0; i < kLpWarps; ++i) b = s_best[i] > b ? s_best[i] : b;
+                    if (tid == 0) s_top[q] = b;
+                    if (b != 0 && b == best) look(b);
+                    __syncthreads();
+                }
+            } else {
+                rank_top(s_list, s_n, K, s_top);
             }
         }
         // ---- the CTA's statistics and top k
@@ -349,7 +403,6 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
             st = join(st, y, c);
         }
         if (lane == 0) w_stat[warp] = st;
-        if constexpr (TOP) rank_top(s_list, s_n, K, s_top);
         if (!joined) {  // remote shared memory only once every CTA of the cluster runs
             asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
             joined = true;
@@ -369,16 +422,27 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
                 all = x_stat[buf][0];
                 for (int i = 1; i < CL; ++i) all = join(all, x_stat[buf][i], c);
                 if constexpr (TOP) {
-                    // empty places (0) share a rank past every real key
+                    // a key's rank: its place in its own sorted list and, in each of the
+                    // others, how many are larger; empty places (0) come last
                     for (int i = tid; i < CL * K; i += kLpThreads) {
                         const uint64_t mine = x_top[buf][i];
-                        int r = 0;
-                        for (int j = 0; j < CL * K; ++j) r += x_top[buf][j] > mine ? 1 : 0;
-                        if (mine != 0 && r < K) s_top[r] = mine;
+                        int r = i % K;
+                        for (int a = 0; a < CL; ++a) {
+                            if (a == i / K) continue;
+                            const uint64_t *list = x_top[buf] + a * K;
+                            int lo = 0, hi = K;  // list[0 .. lo) > mine
+                            while (lo < hi) {
+                                const int mid = (lo + hi) >> 1;
+                                // equal only when both are empty: by list, so that every place is taken once
+                                if (list[mid] > mine || (list[mid] == mine && a < i / K))
+                                    lo = mid + 1;
+                                else
+                                    hi = mid;
+                            }
+                            r += lo;
+                        }
+                        if (r < K) s_top[r] = mine;
                     }
-                    int have = 0;
-                    for (int j = 0; j < CL * K; ++j) have += x_top[buf][j] != 0 ? 1 : 0;
-                    if (tid >= have && tid < K) s_top[tid] = 0ull;
                     __syncthreads();
                 }
             }
@@ -423,12 +487,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobPar
 
 template <typename T, bool TOP>
 cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
-    // few rows: a cluster a row, so that the row's columns spread over the SMs;
-    // a CTA keeps at least one chunk's worth of columns
+    // few rows: a cluster a row, so that the row's columns spread over the SMs
+    // (two CTAs an SM); a CTA keeps at least a chunk's worth of columns
     const int chunk = Elem<T>::kPer * kLpBatch * kLpThreads;
     const int sms = device_sms();
     int cl = 1;
-    while (cl < kLpMaxCluster && (int64_t)p.n_rows * cl < 2 * sms && (int64_t)cl * chunk < p.n_cols) cl *= 2;
+    while (cl < kLpMaxCluster && (int64_t)p.n_rows * 2 * cl <= 2 * sms && (int64_t)cl * chunk < p.n_cols) cl *= 2;
     const int64_t groups = (int64_t)2 * sms / cl > 0 ? (int64_t)2 * sms / cl : 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)cl, (unsigned)(p.n_rows < groups ? p.n_rows : groups));
