@@ -39,13 +39,19 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         return TF_ERR_WORKSPACE;
     const int group = n_q_heads / c.n_kv_heads;
     int max_rows = n_rows_total, splits = n_splits_max, split = split_keys;
+    bool ws = false;  // decode-shaped: the warp-specialized kernel
     if (segs_host) {
         rc = check_segs_host(segs_host, n_segs, n_rows_total, page_table_len, c.page_size, c.n_pages, page_table_host,
                              split_keys, n_splits_max, &max_rows, full != 0);
         if (rc != TF_OK) return rc;
         if (max_rows == 0) return TF_OK;
+        ws = (int64_t)max_rows * group <= 8 && decode_q8_supported(c.head_dim, n_segs) &&
+             (split == 0 || split % std::min(c.page_size, 64) == 0);
         if (split == 0)
-            split = choose_split(segs_host, n_segs, c.n_kv_heads, (int64_t)device_sms() * 2, 2, 256, n_splits_max);
+            split = ws ? choose_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 3, 256,
+                                      n_splits_max)
+                       : choose_split(segs_host, n_segs, c.n_kv_heads, (int64_t)device_sms() * 2, 2, 256,
+                                      n_splits_max);
         // as many partial slots as the longest stream takes: the merge's reads stay close together
         int longest = 1;
         for (int s = 0; s < n_segs; ++s)
@@ -58,34 +64,69 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     const PartBuffers b = part_buffers(workspace, n_rows_total, n_q_heads, c.head_dim, splits);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
-    AttnParams p{};
-    p.q = static_cast<const uint16_t *>(q);
-    p.n_rows_total = n_rows_total;
-    p.hq = n_q_heads;
-    p.hkv = c.n_kv_heads;
-    p.group = group;
-    p.k_codes = static_cast<const uint8_t *>(c.k_codes);
-    p.v_codes = static_cast<const uint8_t *>(c.v_codes);
-    p.k_scale = c.k_scale;
-    p.v_scale = c.v_scale;
-    p.kv_type = c.kv_type;
-    p.n_pages = c.n_pages;
-    p.log2_page = log2_exact(c.page_size);
-    p.pt_len = page_table_len;
-    p.page_table = page_table;
-    p.segs = segs;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.split_keys = split;
-    p.n_splits_max = splits;
-    p.n_qgroups = (int)n_qgroups;
-    p.full = full ? 1 : 0;
-    p.part_o = b.o;
-    p.part_m = b.m;
-    p.part_l = b.l;
-    p.part_flag = b.flag;
-    p.status = status;
-    const dim3 grid((unsigned)splits, (unsigned)(n_qgroups * c.n_kv_heads), (unsigned)n_segs);
-    if (launch_attn_partial(p, c.head_dim, false, false, grid, st) != cudaSuccess) return TF_ERR_CUDA;
+    const int lp = log2_exact(c.page_size);
+    const float scale_log2 = scale * 1.4426950408889634f;
+    cudaError_t e = cudaSuccess;
+    if (ws) {
+        WsParams w{};
+        w.q = static_cast<const uint16_t *>(q);
+        w.n_rows_total = n_rows_total;
+        w.hq = n_q_heads;
+        w.hkv = c.n_kv_heads;
+        w.group = group;
+        w.n_segs = n_segs;
+        w.segs = segs;
+        w.page_table = page_table;
+        w.n_pages = c.n_pages;
+        w.log2_page = lp;
+        w.pt_len = page_table_len;
+        w.k_scale = c.k_scale;
+        w.v_scale = c.v_scale;
+        w.scale_log2 = scale_log2;
+        w.split_keys = split;
+        w.n_splits_max = splits;
+        w.full = full ? 1 : 0;
+        w.part_o = b.o;
+        w.part_m = b.m;
+        w.part_l = b.l;
+        w.part_flag = b.flag;
+        w.status = status;
+        int64_t items = 0;
+        for (int s = 0; s < n_segs; ++s)
+            if (segs_host[s].n_rows > 0)
+                items += ((int64_t)segs_host[s].n_keys + split - 1) / split * c.n_kv_heads;
+        e = launch_decode_q8(w, c.head_dim, c.kv_type, c.k_codes, c.v_codes, items, st);
+    } else {
+        AttnParams p{};
+        p.q = static_cast<const uint16_t *>(q);
+        p.n_rows_total = n_rows_total;
+        p.hq = n_q_heads;
+        p.hkv = c.n_kv_heads;
+        p.group = group;
+        p.k_codes = static_cast<const uint8_t *>(c.k_codes);
+        p.v_codes = static_cast<const uint8_t *>(c.v_codes);
+        p.k_scale = c.k_scale;
+        p.v_scale = c.v_scale;
+        p.kv_type = c.kv_type;
+        p.n_pages = c.n_pages;
+        p.log2_page = lp;
+        p.pt_len = page_table_len;
+        p.page_table = page_table;
+        p.segs = segs;
+        p.scale_log2 = scale_log2;
+        p.split_keys = split;
+        p.n_splits_max = splits;
+        p.n_qgroups = (int)n_qgroups;
+        p.full = full ? 1 : 0;
+        p.part_o = b.o;
+        p.part_m = b.m;
+        p.part_l = b.l;
+        p.part_flag = b.flag;
+        p.status = status;
+        const dim3 grid((unsigned)splits, (unsigned)(n_qgroups * c.n_kv_heads), (unsigned)n_segs);
+        e = launch_attn_partial(p, c.head_dim, false, false, grid, st);
+    }
+    if (e != cudaSuccess) return TF_ERR_CUDA;
 
     MergeSegsParams m{};
     m.own = PartSet{b.o, b.m, b.l, b.flag, splits, split};
@@ -94,9 +135,9 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     m.max_rows = max_rows;
     m.n_rows_total = n_rows_total;
     m.hq = n_q_heads;
-    m.log2_page = p.log2_page;
+    m.log2_page = lp;
     m.pt_len = page_table_len;
-    m.full = p.full;
+    m.full = full ? 1 : 0;
     m.out = out;
     m.out_bf16 = out_dtype == TF_OUT_BF16;
     m.flags = flags;

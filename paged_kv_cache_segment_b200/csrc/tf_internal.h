@@ -107,6 +107,8 @@ struct WsParams {
     // ring
     const tf_ring_seg *rsegs;
     int64_t ring_slots_total;
+    // an 8-bit cache's scale bytes [pages][Hkv][P]
+    const uint8_t *k_scale, *v_scale;
     float scale_log2;
     int split_keys, n_splits_max;
     int full;  // every row sees all of its stream's keys (no causal count)
@@ -170,6 +172,10 @@ cudaError_t launch_argmax(const ArgmaxParams &p, bool vec, bool early, cudaStrea
 bool prompt_tc_supported(int head_dim, int group, int page_size);
 bool decode_ws_supported(int head_dim, int n_segs);
 cudaError_t launch_decode_ws(const WsParams &p, int head_dim, bool ring, const void *k, const void *v,
+                             int64_t n_items_bound, cudaStream_t st);
+bool decode_q8_supported(int head_dim, int n_segs);
+int decode_q8_grid(int head_dim, int kv_type);  // CTAs of a full launch on the current device
+cudaError_t launch_decode_q8(const WsParams &p, int head_dim, int kv_type, const void *k, const void *v,
                              int64_t n_items_bound, cudaStream_t st);
 cudaError_t launch_kv_append(const AppendParams &p, int head_dim, int n_segs, int max_rows, cudaStream_t st);
 cudaError_t launch_prompt_tc(const PromptTcParams &p, int head_dim, const void *k, const void *v, cudaStream_t st);

@@ -43,6 +43,38 @@ __device__ __forceinline__ void q8_to_f16(uint32_t w, uint32_t &p01, uint32_t &p
     }
 }
 
+// Two keys' code pairs as a transposing ldmatrix leaves them (bytes: key a
+// column d, key a column d + 1, key b column d, key b column d + 1) to the f16
+// pairs (key a, key b) of column d and of column d + 1.
+template <int TYPE>
+__device__ __forceinline__ void q8_to_f16_pairs(uint32_t w, uint32_t &d0, uint32_t &d1) {
+    if constexpr (TYPE == TF_KV_E4M3) {
+        q8_to_f16<TYPE>(__byte_perm(w, 0u, 0x3120), d0, d1);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d0) : "r"(a), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d1) : "r"(b), "r"(0x64806480u));
+    }
+}
+
+// Two floats -> packed f16x2 (round to nearest even); `lo` lands in bits 0..15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// D = A * B + D, f16 inputs, fp32 accumulators (m16n8k16, row.col).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t p) {
     __half2 h;
     *reinterpret_cast<uint32_t *>(&h) = p;

@@ -13,4 +13,9 @@ namespace tfp {
 bool make_tensor_map_bf16(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
                           const cuuint64_t *strides, const cuuint32_t *box);
 
+// A tiled map of bytes; swizzle 128 or 64 is the span of the pattern, which is
+// also the box's inner extent.
+bool make_tensor_map_u8(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                        const cuuint32_t *box, int swizzle);
+
 }  // namespace tfp
