@@ -118,4 +118,37 @@ inline int choose_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t sl
     return len > 0x40000000 ? 0x40000000 : (int)len;
 }
 
+
+// A split size for kernels of one CTA an SM with a fixed cost a CTA (start-up
+// and epilogue, some eight 64-key tiles' worth): the smallest whole number of
+// tiles that leaves one wave of CTAs (streams x kv-heads x query tiles x splits)
+// on the SMs, since a second wave pays the fixed cost again; one split a stream
+// where even that is more.
+inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows_per_tile, int n_sms, int least,
+                          int n_splits_max) {
+    int64_t longest = 1;
+    for (int s = 0; s < n_segs; ++s)
+        if (sh[s].n_rows > 0 && sh[s].n_keys > longest) longest = sh[s].n_keys;
+    auto ctas = [&](int64_t tiles) {
+        int64_t n = 0;
+        for (int s = 0; s < n_segs; ++s)
+            if (sh[s].n_rows > 0)
+                n += ((int64_t)sh[s].n_keys + tiles * 64 - 1) / (tiles * 64) *
+                     (((int64_t)sh[s].n_rows + rows_per_tile - 1) / rows_per_tile) * n_kv_heads;
+        return n;
+    };
+    const int64_t fit = (longest + n_splits_max - 1) / n_splits_max;
+    int64_t lo = (least > fit ? least : fit) + 63, hi = (longest + 63) / 64;
+    lo /= 64;
+    if (hi < lo) hi = lo;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (ctas(mid) <= n_sms)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo > (0x40000000 >> 6) ? 0x40000000 : (int)(lo * 64);
+}
+
 }  // namespace tfp

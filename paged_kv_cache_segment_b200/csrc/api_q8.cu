@@ -50,8 +50,8 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         if (split == 0)
             split = ws ? choose_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 3, 256,
                                       n_splits_max)
-                       : choose_split(segs_host, n_segs, c.n_kv_heads, (int64_t)device_sms() * 2, 2, 256,
-                                      n_splits_max);
+                       : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), 256,
+                                        n_splits_max);
         // as many partial slots as the longest stream takes: the merge's reads stay close together
         int longest = 1;
         for (int s = 0; s < n_segs; ++s)
@@ -96,6 +96,35 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
             if (segs_host[s].n_rows > 0)
                 items += ((int64_t)segs_host[s].n_keys + split - 1) / split * c.n_kv_heads;
         e = launch_decode_q8(w, c.head_dim, c.kv_type, c.k_codes, c.v_codes, items, st);
+    } else if (verify_q8_supported(c.head_dim, group, split)) {
+        // more queries a kv-head (a verify round, a block): the tensor-core kernel
+        Q8TcParams t{};
+        t.q = static_cast<const uint16_t *>(q);
+        t.k_codes = static_cast<const uint8_t *>(c.k_codes);
+        t.v_codes = static_cast<const uint8_t *>(c.v_codes);
+        t.k_scale = c.k_scale;
+        t.v_scale = c.v_scale;
+        t.page_table = page_table;
+        t.segs = segs;
+        t.n_rows_total = n_rows_total;
+        t.hq = n_q_heads;
+        t.hkv = c.n_kv_heads;
+        t.group = group;
+        t.n_pages = c.n_pages;
+        t.log2_page = lp;
+        t.pt_len = page_table_len;
+        t.scale_log2 = scale_log2;
+        t.split_keys = split;
+        t.n_splits = splits;
+        t.n_qt = (max_rows + 128 / group - 1) / (128 / group);
+        t.full = full ? 1 : 0;
+        t.part_o = b.o;
+        t.part_m = b.m;
+        t.part_l = b.l;
+        t.part_flag = b.flag;
+        t.status = status;
+        if ((int64_t)t.n_qt * splits > 0x7fffffff || c.n_kv_heads > 65535) return TF_ERR_UNSUPPORTED;
+        e = launch_verify_q8(t, c.head_dim, c.kv_type, n_segs, st);
     } else {
         AttnParams p{};
         p.q = static_cast<const uint16_t *>(q);

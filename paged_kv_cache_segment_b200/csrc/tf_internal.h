@@ -85,6 +85,23 @@ struct PromptTcParams {
     uint64_t wait_ns;
 };
 
+// Parameters of the tensor-core partial kernel over an 8-bit cache.
+struct Q8TcParams {
+    const uint16_t *q;  // bf16 [n_rows_total][hq][D]
+    const uint8_t *k_codes, *v_codes, *k_scale, *v_scale;
+    const int32_t *page_table;
+    const tf_seg *segs;
+    int n_rows_total, hq, hkv, group, n_pages, log2_page, pt_len;
+    float scale_log2;
+    int split_keys, n_splits, n_qt;  // n_qt: 128-query tiles of the longest stream's rows
+    int full;
+    float *part_o, *part_m, *part_l;
+    uint8_t *part_flag;
+    uint32_t *status;
+    int test_idle;  // the timeout test hook, as in PromptTcParams
+    uint64_t wait_ns;
+};
+
 // Parameters of the KV append (rows into their pages).
 struct AppendParams {
     const uint16_t *k_rows, *v_rows;  // bf16 [n_rows_total][hkv][D]
@@ -177,6 +194,8 @@ bool decode_q8_supported(int head_dim, int n_segs);
 int decode_q8_grid(int head_dim, int kv_type);  // CTAs of a full launch on the current device
 cudaError_t launch_decode_q8(const WsParams &p, int head_dim, int kv_type, const void *k, const void *v,
                              int64_t n_items_bound, cudaStream_t st);
+bool verify_q8_supported(int head_dim, int group, int split_keys);
+cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, int n_segs, cudaStream_t st);
 cudaError_t launch_kv_append(const AppendParams &p, int head_dim, int n_segs, int max_rows, cudaStream_t st);
 cudaError_t launch_prompt_tc(const PromptTcParams &p, int head_dim, const void *k, const void *v, cudaStream_t st);
 bool partial_tc_supported(int head_dim, int group, int page_size, int split_keys);

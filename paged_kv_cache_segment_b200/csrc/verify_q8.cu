@@ -1,0 +1,622 @@
+// verify_q8.cu - split-KV partials over an 8-bit cache for more than 8 queries
+// a kv-head (verify rounds, blocks) on the 5th-generation tensor cores: the
+// 8-bit counterpart of prompt_tc.cu's partial kernel, whose work split, barriers,
+// softmax roles and abort path it follows.
+//
+// One CTA computes 128 queries (128/G rows x the G q-heads of a kv-head) over a
+// split of the keys, 64 at a time.  Fourteen warps:
+//  - a load warp brings a tile's codes by bulk copies (a page's slots of a
+//    kv-head are contiguous) and its scale bytes (8-byte cp.async) into raw
+//    buffers;
+//  - four converter warps turn codes into f16 tiles in the tensor cores' swizzled
+//    layout (exact, one conversion instruction per two codes) and the scale bytes
+//    into two floats a key: 2^e of K, and e itself of V;
+//  - an MMA warp issues S = Q K^T and O += W V (both f16 with fp32 accumulators
+//    in tensor memory, Q and W as the tensor-memory operand);
+//  - eight softmax warps, two threads a query row, as in prompt_tc.cu.
+// The numerics are those of decode_q8.cu: Q's rows scaled by a power of two into
+// f16, K's scale multiplying the score, V's joining the weight, whose sum o
+// keeps a reference of its own (W = f16 hi + f16 lo, 22 bits of a weight).  So
+// the converters never multiply, and an element costs them about one
+// instruction: with bf16 tiles that carry the scales it would be four.
+//
+// What bounds it is the tensor pipe: at head dim 256 a tile's MMAs take about
+// 2,000 cycles (QK at N = 64 runs at half rate, W V goes twice), against some
+// 900 of softmax and 250 of conversion, and 0.7 us for the tile's 33 KB at an
+// SM's share of HBM.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "tf_common.cuh"
+#include "tf_internal.h"
+#include "tf_q8.cuh"
+#include "tf_sm100.cuh"
+
+namespace tfp {
+namespace {
+
+constexpr int kSoftmax = 256;                       // threads of the eight softmax warps
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kVqThreads = (kConvWarp + kConvWarps) * 32;
+constexpr int kTmemBar = 6;                         // named barriers: 1 softmax, 2-5 softmax pairs
+constexpr int kM = 128, kN = 64;                    // queries a CTA, keys a tile
+constexpr int kSlab = kN * 128;                     // 64 keys x 64 columns of f16
+constexpr int kStages = 2;                          // f16 K and V tiles
+constexpr int kFactors = 4;                         // tiles whose per-key factors are kept
+constexpr uint32_t kColS0 = 0, kColS1 = 64, kColQ = 128, kColO = 256;
+constexpr int kPids = 1024;                         // page ids held in shared memory
+
+template <int D>
+struct VqCfg {
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kTile = kSlabs * kSlab;    // an f16 tile
+    static constexpr int kRaw = kN * D;             // a tile of codes
+    static constexpr int kRawStages = D == 256 ? 2 : 4;
+    static constexpr int kRawStage = 2 * kRaw + 128;  // K, V, 64 + 64 scale bytes
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kStages * kTile;
+    static constexpr int kOffRaw = 2 * kStages * kTile;
+    static constexpr int kOffFactor = kOffRaw + kRawStages * kRawStage;  // float [kFactors][2][kN]
+    static constexpr int kOffPid = kOffFactor + kFactors * 2 * kN * 4;
+    static constexpr int kSmem = kOffPid + kPids * 4 + 1024;
+};
+
+// barrier slots
+constexpr int kBarQ = 0;                                 // Q in tensor memory
+constexpr int kBarRawFull = 1;                           // [4] codes and scale bytes landed
+constexpr int kBarRawFree = kBarRawFull + 4;             // [4] the converters have read them
+constexpr int kBarKFull = kBarRawFree + 4;               // [kStages] f16 tile written
+constexpr int kBarVFull = kBarKFull + kStages;
+constexpr int kBarKFree = kBarVFull + kStages;           // [kStages] the MMA that read it is done
+constexpr int kBarVFree = kBarKFree + kStages;
+constexpr int kBarS = kBarVFree + kStages;               // [2] QK done
+constexpr int kBarW = kBarS + 2;                         // [2] weights written
+constexpr int kBarO = kBarW + 2;                         // [2] W V done
+constexpr int kNumBars = kBarO + 2;
+
+// Instruction descriptor, kind::f16: f16 x f16 -> f32.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ bool vq_wait(uint32_t bar, uint32_t phase, volatile uint32_t *abort_flag, uint64_t lim) {
+    if (*abort_flag) return false;
+    if (mbar_wait(bar, phase, lim)) return true;
+    *abort_flag = 1;
+    return false;
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcParams p) {
+    using C = VqCfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t bars[kNumBars];
+    __shared__ uint32_t s_tmem, s_err, s_abort;
+    __shared__ float2 s_xmax[2][2][kM];     // [tile parity][column half][row]: maxima of score, of score + value scale
+    __shared__ float s_xl[2][kM];           // [column half][row]: final partial sums
+    __shared__ uint32_t s_x[2][2][kM];      // [exchange][column half][row]: row maxima of Q, findings
+    __shared__ uint32_t s_vnan[kFactors][2];  // value rows marked nonfinite, a bit a key
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t lim = p.wait_ns ? p.wait_ns : 2000000000ull;  // every bounded wait's limit
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char *base_ptr = smem_raw + (sbase - smem_u32(smem_raw));
+    auto sK = [&](int s) { return sbase + C::kOffK + s * C::kTile; };
+    auto sV = [&](int s) { return sbase + C::kOffV + s * C::kTile; };
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    float *factor = reinterpret_cast<float *>(base_ptr + C::kOffFactor);
+    volatile uint32_t *abort_flag = &s_abort;
+    bool sent_row = false;
+
+    // ---- the work item: a stream, a kv-head, a split of its keys, a tile of 128/G rows
+    const int G = p.group, RT = kM / p.group, g = (int)blockIdx.y;
+    const int P = 1 << p.log2_page, BR = P < kN ? P : kN, n_box = kN / BR;
+    const int split = (int)blockIdx.x / p.n_qt, qt = p.n_qt - 1 - (int)blockIdx.x % p.n_qt;
+    const tf_seg e = p.segs[blockIdx.z];
+    const int q_row = e.q_row, T = e.n_rows, N = e.n_keys, pt_base = e.pt_base, n_pg = e.n_pages;
+    {
+        const bool bad = q_row < 0 || T < 0 || (int64_t)q_row + T > p.n_rows_total ||
+                         N < (p.full ? (T > 0 ? 1 : 0) : T) || pt_base < 0 || n_pg < 0 ||
+                         (int64_t)pt_base + n_pg > p.pt_len;
+        uint32_t bit = 0;
+        if (bad)
+            bit = TF_DEV_BAD_SEG;
+        else if ((int64_t)N > ((int64_t)n_pg << p.log2_page))
+            bit = TF_DEV_PAST_PAGES;
+        else if (((int64_t)N + p.split_keys - 1) / p.split_keys > p.n_splits)
+            bit = TF_DEV_SPLITS;
+        if (bit) {
+            if (tid == 0) atomicOr(p.status, bit);
+            return;
+        }
+    }
+    const int64_t key_lo64 = (int64_t)split * p.split_keys;
+    if (qt * RT >= T || key_lo64 >= N) return;  // the merge knows how many partials a row has
+    const int key_lo = (int)key_lo64;
+    const int key_hi = (int)min((int64_t)N, key_lo64 + p.split_keys);
+    const int row0 = qt * RT, rows_here = min(RT, T - row0);
+    const int causal0 = p.full ? N : N - T + 1;  // row i sees keys [0, causal0 + i), with full all N
+    const int key_hi_eff = p.full ? key_hi : min(key_hi, causal0 + row0 + rows_here - 1);
+    const int full_hi = min(key_hi_eff, causal0 + (p.full ? 0 : row0));  // keys every row of the tile sees
+    const int n_tiles = key_hi_eff > key_lo ? (key_hi_eff - key_lo + kN - 1) / kN : 0;
+    if (n_tiles == 0) {
+        // no row of the tile sees a key of this split
+        for (int r = tid; r < rows_here * G; r += kVqThreads) {
+            const int64_t at = ((int64_t)(q_row + row0 + r / G) * p.hq + g * G + r % G) * p.n_splits + split;
+            p.part_m[at] = -INFINITY;
+            p.part_l[at] = 0.f;
+            p.part_flag[at] = 0;
+        }
+        return;
+    }
+
+    int *pids = reinterpret_cast<int *>(base_ptr + C::kOffPid);
+    const int pg_lo = key_lo >> p.log2_page;
+    {
+        const int n_pid = min((int)(((int64_t)key_hi_eff + P - 1) >> p.log2_page), n_pg) - pg_lo;
+        for (int i = tid; i < n_pid && i < kPids; i += kVqThreads) {
+            const int id = p.page_table[pt_base + pg_lo + i];
+            pids[i] = (id < 0 || id >= p.n_pages) ? -1 : id;
+        }
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i) {
+            uint32_t count = 1;
+            if (i >= kBarS && i < kBarS + 2) count = 2;
+            if (i == kBarQ || (i >= kBarW && i < kBarW + 2)) count = kSoftmax / 32;
+            if (i >= kBarRawFull && i < kBarRawFull + 4) count = 1 + 32;  // expect_tx, every lane's scale bytes
+            if ((i >= kBarRawFree && i < kBarRawFree + 4) || (i >= kBarKFull && i < kBarKFree)) count = kConvWarps;
+            mbar_init(bar(i), count);
+        }
+        fence_barrier_init();
+        s_err = 0;
+        s_abort = 0;
+    }
+    __syncthreads();
+    uint32_t tmem = 0;
+    auto take_tmem = [&]() {  // the softmax warps and the MMA warp
+        if (warp == 0) {
+            tmem_alloc(smem_u32(&s_tmem), 512);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        named_bar_sync(kTmemBar, kSoftmax + 32);
+        tc_fence_after();
+        tmem = s_tmem;
+    };
+    auto wwait = [&](uint32_t b, uint32_t phase) { return __all_sync(0xffffffffu, vq_wait(b, phase, abort_flag, lim)); };
+
+    if (warp == kLoadWarp) {
+        // ================= load warp: codes by bulk copies, one per page (or
+        // 64-key span of a larger page) of K and of V; scale bytes in 8-byte pieces
+        for (int t = 0; t < n_tiles && !p.test_idle; ++t) {
+            const int s = t % C::kRawStages, kt = key_lo + t * kN;
+            if (t >= C::kRawStages && !wwait(bar(kBarRawFree + s), (uint32_t)((t / C::kRawStages - 1) & 1))) break;
+            const uint32_t dst = sbase + C::kOffRaw + s * C::kRawStage, full = bar(kBarRawFull + s);
+            auto page_of = [&](int key) -> int {
+                const int idx = key >> p.log2_page;
+                if (idx >= n_pg) return -1;
+                const int id = idx - pg_lo < kPids ? pids[idx - pg_lo] : p.page_table[pt_base + idx];
+                return id < 0 || id >= p.n_pages ? -1 : id;
+            };
+            {  // lanes 0-7: K's scale bytes, 8-15: V's
+                const int key0 = kt + (lane & 7) * 8;
+                const int id = lane < 16 && key0 < key_hi_eff ? page_of(key0) : -1;
+                if (id >= 0) {
+                    const uint8_t *src = (lane < 8 ? p.k_scale : p.v_scale) +
+                                         (((int64_t)id * p.hkv + g) << p.log2_page) + (key0 & (P - 1));
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(
+                                     dst + 2 * C::kRaw + (lane < 8 ? 0 : kN) + (lane & 7) * 8),
+                                 "l"(src)
+                                 : "memory");
+                }
+            }
+            // lane i < n_box: K's box i, lane 16 + i: V's
+            const int x = lane & 15, key0 = kt + x * BR;
+            int id = -1;
+            if (x < n_box && key0 < key_hi_eff) {
+                id = page_of(key0);
+                if (id < 0) {
+                    s_err = 1;
+                    atomicOr(p.status, TF_DEV_BAD_PAGE);
+                }
+            }
+            const uint32_t live = __ballot_sync(0xffffffffu, id >= 0);
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(live) * (uint32_t)(BR * D));
+            __syncwarp();
+            if (id >= 0) {
+                const int64_t src = ((((int64_t)id * p.hkv + g) << p.log2_page) + (key0 & (P - 1))) * D;
+                bulk_load(dst + (lane < 16 ? 0 : C::kRaw) + x * BR * D, (lane < 16 ? p.k_codes : p.v_codes) + src,
+                          (uint32_t)(BR * D), full);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full) : "memory");
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // no scale byte is in flight when this CTA ends
+    } else if (warp >= kConvWarp) {
+        // ================= converter warps: a 16-byte chunk of a key's codes
+        // becomes two 16-byte chunks of f16.  Consecutive lanes take consecutive
+        // chunks; a chunk's two halves are stored in an order that alternates by
+        // 64-column slab, so that eight lanes hit eight bank groups.
+        const int ct = tid - kConvWarp * 32;
+        constexpr int kCpr = D / 16;  // chunks a key
+        for (int t = 0; t < n_tiles; ++t) {
+            const int s = t % C::kRawStages, f = t % kStages, kt = key_lo + t * kN;
+            if (!wwait(bar(kBarRawFull + s), (uint32_t)((t / C::kRawStages) & 1))) break;
+            const unsigned char *raw = base_ptr + C::kOffRaw + s * C::kRawStage;
+            const uint32_t fph = (uint32_t)((t / kStages - 1) & 1);
+            // K's tile is free once QK(t - stages) is done; by then softmax(t - kFactors) is too
+            if (t >= kStages && !wwait(bar(kBarKFree + f), fph)) break;
+            if (ct < kN) {
+                const uint32_t ek = raw[2 * C::kRaw + ct], ev = raw[2 * C::kRaw + kN + ct];
+                float *fk = factor + (t % kFactors) * 2 * kN;
+                fk[ct] = e8m0_f32(ek);
+                fk[kN + ct] = ev == kE8Nan ? -INFINITY : (float)((int)ev - kE8Bias);
+                const uint32_t nan = __ballot_sync(0xffffffffu, ev == kE8Nan);
+                if (lane == 0) s_vnan[t % kFactors][ct >> 5] = nan;
+            }
+            auto convert = [&](const unsigned char *src, unsigned char *dst, int rows) {
+#pragma unroll 4
+                for (int x = ct; x < kN * kCpr; x += kConvWarps * 32) {
+                    const int r = x / kCpr, c = x % kCpr;
+                    uint4 w = *reinterpret_cast<const uint4 *>(src + r * D + c * 16);
+                    if (r >= rows) w = make_uint4(0, 0, 0, 0);
+                    uint4 h[2];
+                    q8_to_f16<TYPE>(w.x, h[0].x, h[0].y);
+                    q8_to_f16<TYPE>(w.y, h[0].z, h[0].w);
+                    q8_to_f16<TYPE>(w.z, h[1].x, h[1].y);
+                    q8_to_f16<TYPE>(w.w, h[1].z, h[1].w);
+                    const int sl = c >> 2, at = 2 * (c & 3), odd = sl & 1;
+                    unsigned char *d = dst + sl * kSlab + r * 128;
+                    *reinterpret_cast<uint4 *>(d + (((at + odd) ^ (r & 7)) << 4)) = odd ? h[1] : h[0];
+                    *reinterpret_cast<uint4 *>(d + (((at + 1 - odd) ^ (r & 7)) << 4)) = odd ? h[0] : h[1];
+                }
+            };
+            const int rows = key_hi_eff - kt;  // keys past it: codes 0 (their scores are masked)
+            convert(raw, base_ptr + C::kOffK + f * C::kTile, rows);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarKFull + f));
+            if (t >= kStages && !wwait(bar(kBarVFree + f), fph)) break;
+            convert(raw + C::kRaw, base_ptr + C::kOffV + f * C::kTile, rows);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kBarVFull + f));
+                mbar_arrive(bar(kBarRawFree + s));
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ================= MMA warp: lane 0 issues every tcgen05.mma
+        take_tmem();
+        const uint32_t idesc_qk = idesc_f16(kM, kN, false), idesc_wv = idesc_f16(kM, D, true);
+        auto issue_qk = [&](int t) {
+            if (lane == 0) {
+                const int b = t & 1, s = t % kStages;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int sl = k >> 2, kk = k & 3;
+                    const uint64_t bd = umma_desc_sw128(sK(s) + sl * kSlab + kk * 32, 16, 1024);
+                    umma_ts(tmem + (b ? kColS1 : kColS0), tmem + kColQ + k * 8, bd, idesc_qk, k > 0 ? 1u : 0u);
+                }
+                umma_commit(bar(kBarS + b));
+                umma_commit(bar(kBarKFree + s));
+                mbar_arrive(bar(kBarS + b));  // hands on the converters' factors, acquired with the K tile
+            }
+            __syncwarp();
+        };
+        auto issue_wv = [&](int j) {
+            if (lane == 0) {
+                const int b = j & 1, s = j % kStages;
+                tc_fence_after();
+                const uint32_t sb = tmem + (b ? kColS1 : kColS0);
+#pragma unroll
+                for (int kk = 0; kk < kN / 16; ++kk) {
+                    const uint64_t bd = umma_desc_sw128(sV(s) + kk * 16 * 128, kSlab, 1024);
+                    umma_ts(tmem + kColO, sb + kk * 8, bd, idesc_wv, (j > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
+                }
+                umma_commit(bar(kBarO + b));
+                umma_commit(bar(kBarVFree + s));
+            }
+            __syncwarp();
+        };
+        auto ready = [&](uint32_t bb, uint32_t phase) { return __all_sync(0xffffffffu, mbar_test_wait(bb, phase)); };
+        if (wwait(bar(kBarQ), 0) && wwait(bar(kBarKFull), 0)) issue_qk(0);
+        for (int j = 0; j < n_tiles && !*abort_flag; ++j) {
+            // QK(j + 1) and W V(j) touch different S buffers: whichever is ready goes first
+            const int b = j & 1, s = j % kStages, j1 = j + 1;
+            bool need_qk = j1 < n_tiles, need_wv = true;
+            const uint64_t t_poll = global_ns();
+            while (need_qk || need_wv) {
+                bool moved = false;
+                if (need_qk && ready(bar(kBarKFull + j1 % kStages), (uint32_t)((j1 / kStages) & 1))) {
+                    issue_qk(j1);
+                    need_qk = false;
+                    moved = true;
+                }
+                if (need_wv && ready(bar(kBarW + b), (uint32_t)((j >> 1) & 1)) &&
+                    ready(bar(kBarVFull + s), (uint32_t)((j / kStages) & 1))) {
+                    issue_wv(j);
+                    need_wv = false;
+                    moved = true;
+                }
+                if (!moved) {
+                    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_ns() - t_poll > lim)) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    __nanosleep(32);
+                }
+            }
+        }
+    } else {
+        // ================= softmax warps: row qi of the tile, keys 32 h .. 32 h + 31 of each key tile
+        const int quad = warp & 3, h = warp >> 2, qi = quad * 32 + lane;
+        const int row_i = row0 + qi / G;
+        const bool valid_row = row_i < T;
+        const int lim_k = valid_row && !p.full ? min(key_hi_eff, causal0 + row_i) : key_hi_eff;
+        const uint32_t pair_bar = 2 + quad;
+        float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
+        uint32_t emax = 0, tail_bad = 0, lane_base = 0;
+        float fq;  // scale * log2(e) over the row's power of two
+
+        // Q into tensor memory as f16, this thread's half of its row; the row's
+        // largest magnitude goes to [2^14, 2^15); rows past the stream are zero
+        {
+            constexpr int kWH = D / 4;  // 32-bit words a half row
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + ((int64_t)(q_row + (valid_row ? row_i : 0)) * p.hq + g * G + qi % G) * D + h * (D / 2));
+            uint32_t w[kWH / 16][16];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int v = 0; v < kWH / 4; ++v) {
+                const uint4 x = valid_row ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+                w[v >> 2][4 * (v & 3)] = x.x;
+                w[v >> 2][4 * (v & 3) + 1] = x.y;
+                w[v >> 2][4 * (v & 3) + 2] = x.z;
+                w[v >> 2][4 * (v & 3) + 3] = x.w;
+            }
+#pragma unroll
+            for (int c = 0; c < kWH / 16; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    amax = max(amax, max(w[c][i] & 0x7fffu, (w[c][i] >> 16) & 0x7fffu));
+            s_x[0][h][qi] = amax;
+            named_bar_sync(pair_bar, 64);
+            amax = max(amax, s_x[0][h ^ 1][qi]);
+            const int ex = min(120, 14 + 127 - (int)(amax >> 7));
+            const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+            fq = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+            if (amax >= 0x7f80u) tail_bad = 1;  // a nonfinite query
+#pragma unroll
+            for (int c = 0; c < kWH / 16; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    w[c][i] = pack_f16x2(bf16_lo_to_f32(w[c][i]) * up, bf16_hi_to_f32(w[c][i]) * up);
+            take_tmem();
+            lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+#pragma unroll
+            for (int c = 0; c < kWH / 16; ++c) tmem_st16(lane_base + kColQ + h * kWH + c * 16, w[c]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarQ));
+        }
+
+        for (int j = 0; j < n_tiles; ++j) {
+            const int b = j & 1, kt = key_lo + j * kN;
+            const uint32_t colS = b ? kColS1 : kColS0;
+            const int kh = kt + 32 * h;
+            vq_wait(bar(kBarS + b), (uint32_t)((j >> 1) & 1), abort_flag, lim);
+            tc_fence_after();
+            float sv[32];
+            {
+                uint32_t r[32];
+                tmem_ld32(lane_base + colS + 32 * h, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sv[c] = __uint_as_float(r[c]);
+            }
+            // the scores in base 2, masked; their largest, and the largest of score + value exponent
+            const float4 *fk = reinterpret_cast<const float4 *>(factor + (j % kFactors) * 2 * kN + 32 * h);
+            const float4 *fv = reinterpret_cast<const float4 *>(factor + (j % kFactors) * 2 * kN + kN + 32 * h);
+            const uint32_t vnan = s_vnan[j % kFactors][h];
+            const bool masked = kt + kN > full_hi;
+            float mx = -INFINITY, my = -INFINITY, mn = INFINITY;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const float4 k4 = fk[q], v4 = fv[q];
+                const float kf[4] = {k4.x, k4.y, k4.z, k4.w}, vf[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 4 * q + i;
+                    float x = sv[c] * (kf[i] * fq);
+                    if (masked) {
+                        const bool vis = kh + c < lim_k;
+                        emax = max(emax, vis ? exp_bits(x) : 0u);
+                        x = vis ? x : -INFINITY;
+                    } else {
+                        mn = fminf(mn, x);  // NaN and +inf reach the row sum, -inf is caught here
+                    }
+                    sv[c] = x;
+                    mx = fmaxf(mx, x);
+                    my = fmaxf(my, x + vf[i]);
+                }
+            }
+            if (mn == -INFINITY) emax = 0x7f800000u;
+            if (vnan) {  // value rows marked nonfinite: flag the rows that see one
+#pragma unroll 1
+                for (uint32_t v = vnan; v; v &= v - 1)
+                    if (kh + __ffs(v) - 1 < lim_k) tail_bad = 1;
+            }
+            s_xmax[b][h][qi] = make_float2(mx, my);
+            named_bar_sync(pair_bar, 64);
+            {
+                const float2 o = s_xmax[b][h ^ 1][qi];
+                mx = fmaxf(mx, o.x);
+                my = fmaxf(my, o.y);
+            }
+            // lazy references: they move when a term would pass 2^8 above them
+            // (both halves see the same maxima, so they move together)
+            if (mx > m_ref + 8.f) {
+                l_run *= ex2(m_ref - mx);
+                m_ref = mx;
+            }
+            float alpha = 1.f;
+            if (my > r_ref + 8.f) {
+                alpha = ex2(r_ref - my);
+                r_ref = my;
+            }
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;
+            {
+                uint32_t hi[16], lo[16];
+                float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 v4 = fv[q];
+                    const float vf[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const int c = 4 * q + i;
+                        ls0 += ex2(sv[c] - mu);
+                        ls1 += ex2(sv[c + 1] - mu);
+                        const float w0 = ex2(sv[c] + vf[i] - ru), w1 = ex2(sv[c + 1] + vf[i + 1] - ru);
+                        hi[c / 2] = pack_f16x2(w0, w1);
+                        const float2 f = f16x2_to_f32(hi[c / 2]);
+                        lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
+                    }
+                }
+                l_run += ls0 + ls1;
+                tmem_st16(lane_base + colS + 32 + 16 * h, lo);
+                tmem_st16(lane_base + colS + 16 * h, hi);
+            }
+            // O holds the tiles before this one: rescale it once W V(j - 1) is done
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                vq_wait(bar(kBarO + ((j - 1) & 1)), (uint32_t)(((j - 1) >> 1) & 1), abort_flag, lim);
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t r[32];
+                    const uint32_t col = kColO + h * (D / 2) + c * 32;
+                    tmem_ld32(lane_base + col, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int w = 0; w < 32; ++w) r[w] = __float_as_uint(__uint_as_float(r[w]) * alpha);
+                    tmem_st32(lane_base + col, r);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarW + b));
+        }
+
+        // ---- epilogue: o in units of 2^m, each half stores its D/2 columns
+        vq_wait(bar(kBarO + ((n_tiles - 1) & 1)), (uint32_t)(((n_tiles - 1) >> 1) & 1), abort_flag, lim);
+        tc_fence_after();
+        const bool aborted = *abort_flag != 0;
+        s_xl[h][qi] = l_run;
+        s_x[1][h][qi] = (emax == 0x7f800000u ? 1u : 0u) | tail_bad;
+        named_bar_sync(pair_bar, 64);
+        const float l_sum = s_xl[0][qi] + s_xl[1][qi];
+        uint32_t bad = s_x[1][0][qi] | s_x[1][1][qi] | s_err | (aborted ? 1u : 0u) | (isfinite(l_sum) ? 0u : 1u);
+        const int64_t at = ((int64_t)(q_row + row_i) * p.hq + g * G + qi % G) * p.n_splits + split;
+        // 2^(r - m) in two steps: it may itself be past the floats where o is small
+        const float gf = r_ref == -INFINITY ? 0.f : ex2(0.5f * (r_ref - (m_ref == -INFINITY ? 0.f : m_ref)));
+        const int d0 = h * (D / 2);
+        const bool staged = rows_here * G >= 64;  // see prompt_tc.cu: many rows leave by bulk copies
+        uint32_t *stage = reinterpret_cast<uint32_t *>(base_ptr + C::kOffK) + qi * (D + 4) + d0;
+        uint32_t *gout = reinterpret_cast<uint32_t *>(p.part_o + at * D + d0);
+        const bool direct = !staged && valid_row && !aborted;
+        uint32_t obad = 0;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 64; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
+            tmem_wait_ld();
+            float o[32];
+#pragma unroll
+            for (int w = 0; w < 32; ++w) {
+                o[w] = __uint_as_float(r[w]) * gf * gf;
+                obad |= !isfinite(o[w]);
+            }
+            if ((staged && !aborted) || direct) {
+                float4 *d4 = reinterpret_cast<float4 *>((staged ? stage : gout) + cc * 32);
+#pragma unroll
+                for (int w = 0; w < 8; ++w) d4[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+            }
+        }
+        s_x[0][h][qi] = obad;
+        named_bar_sync(pair_bar, 64);
+        bad |= s_x[0][0][qi] | s_x[0][1][qi];
+        if (staged && valid_row && !aborted) {
+            fence_proxy_async_smem();
+            bulk_store(gout, smem_u32(stage), (uint32_t)(D / 2) * 4u);
+            bulk_commit();
+            sent_row = true;
+        }
+        if (valid_row && h == 0) {
+            p.part_m[at] = m_ref == -INFINITY ? -INFINITY : m_ref * kLn2;
+            p.part_l[at] = l_sum;
+            p.part_flag[at] = (uint8_t)(bad ? 1 : 0);
+        }
+    }
+    // everyone: report a timeout, give in-flight work a bounded chance to land,
+    // release tensor memory
+    __syncthreads();
+    if (s_abort) {
+        if (tid == 0) atomicOr(p.status, TF_DEV_TIMEOUT);
+        if (tid == 0)
+            for (int i = 0; i < kNumBars; ++i) {
+                mbar_wait(bar(i), 0u, 20000000ull);
+                mbar_wait(bar(i), 1u, 20000000ull);
+            }
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (sent_row) bulk_wait_read();
+}
+
+template <int D, int TYPE>
+cudaError_t launch_t(const Q8TcParams &p, int n_segs, cudaStream_t st) {
+    using C = VqCfg<D>;
+    auto kern = verify_q8_kernel<D, TYPE>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    Q8TcParams q = p;
+    if (const uint64_t runout = test_wait_runout_ns()) {
+        q.test_idle = 1;
+        q.wait_ns = runout;
+    }
+    const dim3 grid((unsigned)(p.n_qt * p.n_splits), (unsigned)p.hkv, (unsigned)n_segs);
+    kern<<<grid, kVqThreads, C::kSmem, st>>>(q);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool verify_q8_supported(int head_dim, int group, int split_keys) {
+    return (head_dim == 64 || head_dim == 128 || head_dim == 256) && group <= 128 && 128 % group == 0 &&
+           split_keys > 0 && split_keys % kN == 0;
+}
+
+cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, int n_segs, cudaStream_t st) {
+    const bool e = kv_type == TF_KV_E4M3;
+    switch (head_dim) {
+        case 64: return e ? launch_t<64, TF_KV_E4M3>(p, n_segs, st) : launch_t<64, TF_KV_INT8>(p, n_segs, st);
+        case 128: return e ? launch_t<128, TF_KV_E4M3>(p, n_segs, st) : launch_t<128, TF_KV_INT8>(p, n_segs, st);
+        case 256: return e ? launch_t<256, TF_KV_E4M3>(p, n_segs, st) : launch_t<256, TF_KV_INT8>(p, n_segs, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tfp
