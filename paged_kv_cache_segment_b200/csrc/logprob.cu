@@ -123,31 +123,6 @@ __device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uin
     for (int i = n + threadIdx.x; i < k; i += kLpThreads) top[i] = 0ull;
 }
 
-// Two floats as one 64-bit operand of the packed fp32 instructions.
-__device__ __forceinline__ uint64_t pk2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpk2(uint64_t x, float &a, float &b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // A masked column (-infinity) enters the sums as this finite value, whose term
 // is 0 and whose product with 0 is 0; x - m cannot overflow from it.  It also
 // stands in for logits below it, so a thread whose maximum is not far above it

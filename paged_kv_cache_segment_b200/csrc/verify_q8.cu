@@ -4,11 +4,11 @@
 // softmax roles and abort path it follows.
 //
 // One CTA computes 128 queries (128/G rows x the G q-heads of a kv-head) over a
-// split of the keys, 64 at a time.  Fourteen warps:
+// split of the keys, 64 at a time.  Eighteen warps:
 //  - a load warp brings a tile's codes by bulk copies (a page's slots of a
 //    kv-head are contiguous) and its scale bytes (8-byte cp.async) into raw
 //    buffers;
-//  - four converter warps turn codes into f16 tiles in the tensor cores' swizzled
+//  - eight converter warps turn codes into f16 tiles in the tensor cores' swizzled
 //    layout (exact, one conversion instruction per two codes) and the scale bytes
 //    into two floats a key: 2^e of K, and e itself of V;
 //  - an MMA warp issues S = Q K^T and O += W V (both f16 with fp32 accumulators
@@ -37,7 +37,7 @@ namespace tfp {
 namespace {
 
 constexpr int kSoftmax = 256;                       // threads of the eight softmax warps
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kConvWarp = 10, kConvWarps = 8;
 constexpr int kVqThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kTmemBar = 6;                         // named barriers: 1 softmax, 2-5 softmax pairs
 constexpr int kM = 128, kN = 64;                    // queries a CTA, keys a tile
@@ -53,20 +53,23 @@ struct VqCfg {
     static constexpr int kTile = kSlabs * kSlab;    // an f16 tile
     static constexpr int kRaw = kN * D;             // a tile of codes
     static constexpr int kRawStages = D == 256 ? 2 : 4;
-    static constexpr int kRawStage = 2 * kRaw + 128;  // K, V, 64 + 64 scale bytes
+    static constexpr int kRawK = kRaw + 128;        // with K's and V's 64 scale bytes
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kStages * kTile;
     static constexpr int kOffRaw = 2 * kStages * kTile;
-    static constexpr int kOffFactor = kOffRaw + kRawStages * kRawStage;  // float [kFactors][2][kN]
-    static constexpr int kOffPid = kOffFactor + kFactors * 2 * kN * 4;
+    static constexpr int kOffRawV = kOffRaw + kRawStages * kRawK;
+    static constexpr int kOffFactor = kOffRawV + kRawStages * kRaw;  // float [kFactors][3][kN]
+    static constexpr int kOffPid = kOffFactor + kFactors * 3 * kN * 4;
     static constexpr int kSmem = kOffPid + kPids * 4 + 1024;
 };
 
 // barrier slots
 constexpr int kBarQ = 0;                                 // Q in tensor memory
-constexpr int kBarRawFull = 1;                           // [4] codes and scale bytes landed
-constexpr int kBarRawFree = kBarRawFull + 4;             // [4] the converters have read them
-constexpr int kBarKFull = kBarRawFree + 4;               // [kStages] f16 tile written
+constexpr int kBarRawK = 1;                              // [4] K's codes and both scale bytes landed
+constexpr int kBarRawV = kBarRawK + 4;                   // [4] V's codes landed
+constexpr int kBarRawKFree = kBarRawV + 4;               // [4] the converters have read them
+constexpr int kBarRawVFree = kBarRawKFree + 4;
+constexpr int kBarKFull = kBarRawVFree + 4;              // [kStages] f16 tile written
 constexpr int kBarVFull = kBarKFull + kStages;
 constexpr int kBarKFree = kBarVFull + kStages;           // [kStages] the MMA that read it is done
 constexpr int kBarVFree = kBarKFree + kStages;
@@ -93,10 +96,12 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     extern __shared__ unsigned char smem_raw[];
     __shared__ __align__(8) uint64_t bars[kNumBars];
     __shared__ uint32_t s_tmem, s_err, s_abort;
-    __shared__ float2 s_xmax[2][2][kM];     // [tile parity][column half][row]: maxima of score, of score + value scale
+    __shared__ float s_xmax[2][2][kM];      // [tile parity][column half][row]: the largest score
+    __shared__ float s_ymax[2][kM];         // [column half][row]: the largest score + value exponent
     __shared__ float s_xl[2][kM];           // [column half][row]: final partial sums
     __shared__ uint32_t s_x[2][2][kM];      // [exchange][column half][row]: row maxima of Q, findings
     __shared__ uint32_t s_vnan[kFactors][2];  // value rows marked nonfinite, a bit a key
+    __shared__ uint32_t s_vmax[kFactors][2];  // the largest scale byte of the others
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = p.wait_ns ? p.wait_ns : 2000000000ull;  // every bounded wait's limit
@@ -166,8 +171,8 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             uint32_t count = 1;
             if (i >= kBarS && i < kBarS + 2) count = 2;
             if (i == kBarQ || (i >= kBarW && i < kBarW + 2)) count = kSoftmax / 32;
-            if (i >= kBarRawFull && i < kBarRawFull + 4) count = 1 + 32;  // expect_tx, every lane's scale bytes
-            if ((i >= kBarRawFree && i < kBarRawFree + 4) || (i >= kBarKFull && i < kBarKFree)) count = kConvWarps;
+            if (i >= kBarRawK && i < kBarRawV) count = 1 + 32;  // expect_tx, every lane's scale bytes
+            if (i >= kBarRawKFree && i < kBarKFree) count = kConvWarps;  // raw free, K and V tiles written
             mbar_init(bar(i), count);
         }
         fence_barrier_init();
@@ -190,33 +195,36 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 
     if (warp == kLoadWarp) {
         // ================= load warp: codes by bulk copies, one per page (or
-        // 64-key span of a larger page) of K and of V; scale bytes in 8-byte pieces
-        for (int t = 0; t < n_tiles && !p.test_idle; ++t) {
+        // 64-key span of a larger page); scale bytes, K's and V's, in 8-byte
+        // pieces with K's codes.  K goes a tile ahead of V, as it is converted.
+        auto page_of = [&](int key) -> int {
+            const int idx = key >> p.log2_page;
+            if (idx >= n_pg) return -1;
+            const int id = idx - pg_lo < kPids ? pids[idx - pg_lo] : p.page_table[pt_base + idx];
+            return id < 0 || id >= p.n_pages ? -1 : id;
+        };
+        auto issue = [&](int t, bool is_v) -> bool {
             const int s = t % C::kRawStages, kt = key_lo + t * kN;
-            if (t >= C::kRawStages && !wwait(bar(kBarRawFree + s), (uint32_t)((t / C::kRawStages - 1) & 1))) break;
-            const uint32_t dst = sbase + C::kOffRaw + s * C::kRawStage, full = bar(kBarRawFull + s);
-            auto page_of = [&](int key) -> int {
-                const int idx = key >> p.log2_page;
-                if (idx >= n_pg) return -1;
-                const int id = idx - pg_lo < kPids ? pids[idx - pg_lo] : p.page_table[pt_base + idx];
-                return id < 0 || id >= p.n_pages ? -1 : id;
-            };
-            {  // lanes 0-7: K's scale bytes, 8-15: V's
+            if (t >= C::kRawStages &&
+                !wwait(bar((is_v ? kBarRawVFree : kBarRawKFree) + s), (uint32_t)((t / C::kRawStages - 1) & 1)))
+                return false;
+            const uint32_t dst = sbase + (is_v ? C::kOffRawV + s * C::kRaw : C::kOffRaw + s * C::kRawK);
+            const uint32_t full = bar((is_v ? kBarRawV : kBarRawK) + s);
+            if (!is_v) {  // lanes 0-7: K's scale bytes, 8-15: V's
                 const int key0 = kt + (lane & 7) * 8;
                 const int id = lane < 16 && key0 < key_hi_eff ? page_of(key0) : -1;
                 if (id >= 0) {
                     const uint8_t *src = (lane < 8 ? p.k_scale : p.v_scale) +
                                          (((int64_t)id * p.hkv + g) << p.log2_page) + (key0 & (P - 1));
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(
-                                     dst + 2 * C::kRaw + (lane < 8 ? 0 : kN) + (lane & 7) * 8),
+                                     dst + C::kRaw + (lane < 8 ? 0 : kN) + (lane & 7) * 8),
                                  "l"(src)
                                  : "memory");
                 }
             }
-            // lane i < n_box: K's box i, lane 16 + i: V's
-            const int x = lane & 15, key0 = kt + x * BR;
+            const int key0 = kt + lane * BR;  // lane i < n_box: box i
             int id = -1;
-            if (x < n_box && key0 < key_hi_eff) {
+            if (lane < n_box && key0 < key_hi_eff) {
                 id = page_of(key0);
                 if (id < 0) {
                     s_err = 1;
@@ -228,65 +236,103 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             __syncwarp();
             if (id >= 0) {
                 const int64_t src = ((((int64_t)id * p.hkv + g) << p.log2_page) + (key0 & (P - 1))) * D;
-                bulk_load(dst + (lane < 16 ? 0 : C::kRaw) + x * BR * D, (lane < 16 ? p.k_codes : p.v_codes) + src,
-                          (uint32_t)(BR * D), full);
+                bulk_load(dst + lane * BR * D, (is_v ? p.v_codes : p.k_codes) + src, (uint32_t)(BR * D), full);
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full) : "memory");
+            if (!is_v) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(full) : "memory");
+            return true;
+        };
+        // (under the timeout test hook it issues nothing: the other warps' waits run out)
+        bool ok = !p.test_idle && issue(0, false);
+        for (int t = 0; t < n_tiles && ok; ++t) {
+            if (t + 1 < n_tiles) ok = issue(t + 1, false);
+            if (ok) ok = issue(t, true);
         }
         cp_async_commit();
         cp_async_wait<0>();  // no scale byte is in flight when this CTA ends
     } else if (warp >= kConvWarp) {
         // ================= converter warps: a 16-byte chunk of a key's codes
-        // becomes two 16-byte chunks of f16.  Consecutive lanes take consecutive
-        // chunks; a chunk's two halves are stored in an order that alternates by
-        // 64-column slab, so that eight lanes hit eight bank groups.
+        // becomes two 16-byte chunks of f16.  A thread keeps its column and its
+        // row modulo 8, so every address is a base and a constant step.  Of eight
+        // neighbouring lanes four take 64 codes of one key and four the next 64
+        // codes of the key after it: the loads then cover 128 bytes of banks, and
+        // the swizzle puts the two keys' stores on even and odd bank groups.
         const int ct = tid - kConvWarp * 32;
-        constexpr int kCpr = D / 16;  // chunks a key
-        for (int t = 0; t < n_tiles; ++t) {
-            const int s = t % C::kRawStages, f = t % kStages, kt = key_lo + t * kN;
-            if (!wwait(bar(kBarRawFull + s), (uint32_t)((t / C::kRawStages) & 1))) break;
-            const unsigned char *raw = base_ptr + C::kOffRaw + s * C::kRawStage;
-            const uint32_t fph = (uint32_t)((t / kStages - 1) & 1);
-            // K's tile is free once QK(t - stages) is done; by then softmax(t - kFactors) is too
-            if (t >= kStages && !wwait(bar(kBarKFree + f), fph)) break;
-            if (ct < kN) {
-                const uint32_t ek = raw[2 * C::kRaw + ct], ev = raw[2 * C::kRaw + kN + ct];
-                float *fk = factor + (t % kFactors) * 2 * kN;
-                fk[ct] = e8m0_f32(ek);
-                fk[kN + ct] = ev == kE8Nan ? -INFINITY : (float)((int)ev - kE8Bias);
-                const uint32_t nan = __ballot_sync(0xffffffffu, ev == kE8Nan);
-                if (lane == 0) s_vnan[t % kFactors][ct >> 5] = nan;
+        const int c4 = ct & 3, hi = (ct >> 2) & 1, rest = ct >> 3;
+        constexpr int kPairs = C::kSlabs > 1 ? C::kSlabs / 2 : 1;  // pairs of slabs
+        const int flip = C::kSlabs > 1 ? rest & 1 : 0;
+        const int sl = C::kSlabs > 1 ? 2 * ((rest >> 1) % kPairs) + (hi ^ flip) : 0;
+        const int r0 = 2 * (C::kSlabs > 1 ? (rest >> 1) / kPairs : rest) + hi;  // first row
+        constexpr int kStep = C::kSlabs > 1 ? 4 * kConvWarps / kPairs : 8 * kConvWarps;  // rows from one to the next
+        const uint32_t src0 = (uint32_t)(r0 * D + sl * 64 + c4 * 16);
+        const uint32_t dst0 = (uint32_t)(sl * kSlab + r0 * 128);
+        const uint32_t at0 = dst0 + (((2 * c4) ^ (r0 & 7)) << 4), at1 = dst0 + (((2 * c4 + 1) ^ (r0 & 7)) << 4);
+        auto convert = [&](const unsigned char *src, unsigned char *dst, int rows) {
+            uint4 w[kN / kStep];
+#pragma unroll
+            for (int i = 0; i < kN / kStep; ++i) {
+                w[i] = *reinterpret_cast<const uint4 *>(src + src0 + i * kStep * D);
+                if (r0 + i * kStep >= rows) w[i] = make_uint4(0, 0, 0, 0);
             }
-            auto convert = [&](const unsigned char *src, unsigned char *dst, int rows) {
-#pragma unroll 4
-                for (int x = ct; x < kN * kCpr; x += kConvWarps * 32) {
-                    const int r = x / kCpr, c = x % kCpr;
-                    uint4 w = *reinterpret_cast<const uint4 *>(src + r * D + c * 16);
-                    if (r >= rows) w = make_uint4(0, 0, 0, 0);
-                    uint4 h[2];
-                    q8_to_f16<TYPE>(w.x, h[0].x, h[0].y);
-                    q8_to_f16<TYPE>(w.y, h[0].z, h[0].w);
-                    q8_to_f16<TYPE>(w.z, h[1].x, h[1].y);
-                    q8_to_f16<TYPE>(w.w, h[1].z, h[1].w);
-                    const int sl = c >> 2, at = 2 * (c & 3), odd = sl & 1;
-                    unsigned char *d = dst + sl * kSlab + r * 128;
-                    *reinterpret_cast<uint4 *>(d + (((at + odd) ^ (r & 7)) << 4)) = odd ? h[1] : h[0];
-                    *reinterpret_cast<uint4 *>(d + (((at + 1 - odd) ^ (r & 7)) << 4)) = odd ? h[0] : h[1];
+#pragma unroll
+            for (int i = 0; i < kN / kStep; ++i) {
+                uint4 h0, h1;
+                q8_to_f16<TYPE>(w[i].x, h0.x, h0.y);
+                q8_to_f16<TYPE>(w[i].y, h0.z, h0.w);
+                q8_to_f16<TYPE>(w[i].z, h1.x, h1.y);
+                q8_to_f16<TYPE>(w[i].w, h1.z, h1.w);
+                *reinterpret_cast<uint4 *>(dst + at0 + i * kStep * 128) = h0;
+                *reinterpret_cast<uint4 *>(dst + at1 + i * kStep * 128) = h1;
+            }
+        };
+        auto convert_k = [&](int t) -> bool {
+            const int s = t % C::kRawStages, f = t % kStages;
+            if (!wwait(bar(kBarRawK + s), (uint32_t)((t / C::kRawStages) & 1))) return false;
+            // the tile is free once QK(t - stages) is done; by then softmax(t - kFactors) is too
+            if (t >= kStages && !wwait(bar(kBarKFree + f), (uint32_t)((t / kStages - 1) & 1))) return false;
+            const unsigned char *raw = base_ptr + C::kOffRaw + s * C::kRawK;
+            const int rows = key_hi_eff - (key_lo + t * kN);  // keys past it: codes 0 (their scores are masked)
+            if (ct < kN) {
+                const uint32_t ek = raw[C::kRaw + ct], ev = raw[C::kRaw + kN + ct];
+                const bool nan = ev == kE8Nan;
+                float *fk = factor + (t % kFactors) * 3 * kN;
+                fk[ct] = e8m0_f32(ek);
+                fk[kN + ct] = nan ? -INFINITY : (float)((int)ev - kE8Bias);
+                fk[2 * kN + ct] = nan || ct >= rows ? 0.f : e8m0_f32(ev);
+                const uint32_t nans = __ballot_sync(0xffffffffu, nan);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, nan || ct >= rows ? 0u : ev);
+                if (lane == 0) {
+                    s_vnan[t % kFactors][ct >> 5] = nans;
+                    s_vmax[t % kFactors][ct >> 5] = top;
                 }
-            };
-            const int rows = key_hi_eff - kt;  // keys past it: codes 0 (their scores are masked)
+            }
             convert(raw, base_ptr + C::kOffK + f * C::kTile, rows);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarKFull + f));
-            if (t >= kStages && !wwait(bar(kBarVFree + f), fph)) break;
-            convert(raw + C::kRaw, base_ptr + C::kOffV + f * C::kTile, rows);
+            if (lane == 0) {
+                mbar_arrive(bar(kBarKFull + f));
+                mbar_arrive(bar(kBarRawKFree + s));
+            }
+            return true;
+        };
+        auto convert_v = [&](int t) -> bool {
+            const int s = t % C::kRawStages, f = t % kStages;
+            if (!wwait(bar(kBarRawV + s), (uint32_t)((t / C::kRawStages) & 1))) return false;
+            if (t >= kStages && !wwait(bar(kBarVFree + f), (uint32_t)((t / kStages - 1) & 1))) return false;
+            convert(base_ptr + C::kOffRawV + s * C::kRaw, base_ptr + C::kOffV + f * C::kTile,
+                    key_hi_eff - (key_lo + t * kN));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(kBarVFull + f));
-                mbar_arrive(bar(kBarRawFree + s));
+                mbar_arrive(bar(kBarRawVFree + s));
             }
+            return true;
+        };
+        // K a tile ahead of V: QK(t + 1) is then ready to run while softmax(t) does
+        bool ok = convert_k(0);
+        for (int t = 0; t < n_tiles && ok; ++t) {
+            if (t + 1 < n_tiles) ok = convert_k(t + 1);
+            if (ok) ok = convert_v(t);
         }
     } else if (warp == kMmaWarp) {
         // ================= MMA warp: lane 0 issues every tcgen05.mma
@@ -421,75 +467,119 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
                 for (int c = 0; c < 32; ++c) sv[c] = __uint_as_float(r[c]);
             }
-            // the scores in base 2, masked; their largest, and the largest of score + value exponent
-            const float4 *fk = reinterpret_cast<const float4 *>(factor + (j % kFactors) * 2 * kN + 32 * h);
-            const float4 *fv = reinterpret_cast<const float4 *>(factor + (j % kFactors) * 2 * kN + kN + 32 * h);
-            const uint32_t vnan = s_vnan[j % kFactors][h];
-            const bool masked = kt + kN > full_hi;
-            float mx = -INFINITY, my = -INFINITY, mn = INFINITY;
+            // scores over fq (> 0: maxima commute with it) and their largest
+            const int fs = j % kFactors;
+            const float4 *fk = reinterpret_cast<const float4 *>(factor + fs * 3 * kN + 32 * h);
+            const float4 *fv = fk + kN / 4, *vs = fk + 2 * (kN / 4);
+            const uint32_t vnan = s_vnan[fs][h];
+            float mx = -INFINITY;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float4 k4 = fk[q], v4 = fv[q];
-                const float kf[4] = {k4.x, k4.y, k4.z, k4.w}, vf[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 4 * q + i;
-                    float x = sv[c] * (kf[i] * fq);
-                    if (masked) {
-                        const bool vis = kh + c < lim_k;
-                        emax = max(emax, vis ? exp_bits(x) : 0u);
-                        x = vis ? x : -INFINITY;
-                    } else {
-                        mn = fminf(mn, x);  // NaN and +inf reach the row sum, -inf is caught here
-                    }
-                    sv[c] = x;
-                    mx = fmaxf(mx, x);
-                    my = fmaxf(my, x + vf[i]);
-                }
+                const float4 k4 = fk[q];
+                unpk2(mul2(pk2(sv[4 * q], sv[4 * q + 1]), pk2(k4.x, k4.y)), sv[4 * q], sv[4 * q + 1]);
+                unpk2(mul2(pk2(sv[4 * q + 2], sv[4 * q + 3]), pk2(k4.z, k4.w)), sv[4 * q + 2], sv[4 * q + 3]);
             }
-            if (mn == -INFINITY) emax = 0x7f800000u;
+            if (kt + kN > full_hi) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const bool vis = kh + c < lim_k;
+                    emax = max(emax, vis ? exp_bits(sv[c]) : 0u);
+                    sv[c] = vis ? sv[c] : -INFINITY;
+                }
+            } else {
+                float mn = INFINITY;
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) mn = min3(mn, sv[c], sv[c + 1]);
+                if (mn == -INFINITY) emax = 0x7f800000u;  // (NaN and +inf reach the row sum)
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) mx = max3(mx, sv[c], sv[c + 1]);
+            mx *= fq;
             if (vnan) {  // value rows marked nonfinite: flag the rows that see one
 #pragma unroll 1
                 for (uint32_t v = vnan; v; v &= v - 1)
                     if (kh + __ffs(v) - 1 < lim_k) tail_bad = 1;
             }
-            s_xmax[b][h][qi] = make_float2(mx, my);
+            s_xmax[b][h][qi] = mx;
             named_bar_sync(pair_bar, 64);
-            {
-                const float2 o = s_xmax[b][h ^ 1][qi];
-                mx = fmaxf(mx, o.x);
-                my = fmaxf(my, o.y);
-            }
+            mx = fmaxf(mx, s_xmax[b][h ^ 1][qi]);
             // lazy references: they move when a term would pass 2^8 above them
             // (both halves see the same maxima, so they move together)
             if (mx > m_ref + 8.f) {
                 l_run *= ex2(m_ref - mx);
                 m_ref = mx;
             }
+            const uint64_t fq2 = pk2(fq, fq);
             float alpha = 1.f;
-            if (my > r_ref + 8.f) {
-                alpha = ex2(r_ref - my);
-                r_ref = my;
+            // score + value exponent is at most mx + vmax: its own maximum is
+            // looked for only when that bound is past the reference
+            const float vmax = (float)((int)max(s_vmax[fs][0], s_vmax[fs][1]) - kE8Bias);
+            if (__any_sync(0xffffffffu, mx + vmax > r_ref + 8.f)) {
+                float my = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 v4 = fv[q];
+                    float y0, y1, y2, y3;
+                    unpk2(fma2(pk2(sv[4 * q], sv[4 * q + 1]), fq2, pk2(v4.x, v4.y)), y0, y1);
+                    unpk2(fma2(pk2(sv[4 * q + 2], sv[4 * q + 3]), fq2, pk2(v4.z, v4.w)), y2, y3);
+                    my = max3(my, max3(y0, y1, y2), y3);
+                }
+                s_ymax[h][qi] = my;
+                named_bar_sync(pair_bar, 64);
+                my = fmaxf(my, s_ymax[h ^ 1][qi]);
+                if (my > r_ref + 8.f) {
+                    alpha = ex2(r_ref - my);
+                    r_ref = my;
+                }
             }
             const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;
             {
                 uint32_t hi[16], lo[16];
-                float ls0 = 0.f, ls1 = 0.f;
+                uint64_t ls2 = 0;  // two zeros
+                const uint64_t nmu2 = pk2(-mu, -mu);
+                auto split = [&](int c, float w0, float w1) {
+                    hi[c / 2] = pack_f16x2(w0, w1);
+                    const float2 f = f16x2_to_f32(hi[c / 2]);
+                    lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
+                };
+                if (__all_sync(0xffffffffu, vmax + mu - ru <= 90.f)) {
+                    // a weight is its probability times 2^(e + mu - ru): a probability
+                    // below the floats would give one below 2^-36
+                    const float rho = ex2(mu - ru);
+                    const uint64_t rho2 = pk2(rho, rho);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float4 v4 = fv[q];
-                    const float vf[4] = {v4.x, v4.y, v4.z, v4.w};
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 s4 = vs[q];
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const int c = 4 * q + i;
-                        ls0 += ex2(sv[c] - mu);
-                        ls1 += ex2(sv[c + 1] - mu);
-                        const float w0 = ex2(sv[c] + vf[i] - ru), w1 = ex2(sv[c + 1] + vf[i + 1] - ru);
-                        hi[c / 2] = pack_f16x2(w0, w1);
-                        const float2 f = f16x2_to_f32(hi[c / 2]);
-                        lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
+                        for (int i = 0; i < 4; i += 2) {
+                            const int c = 4 * q + i;
+                            float p0, p1, w0, w1;
+                            unpk2(fma2(pk2(sv[c], sv[c + 1]), fq2, nmu2), p0, p1);
+                            const uint64_t p2 = pk2(ex2(p0), ex2(p1));
+                            ls2 = add2(ls2, p2);
+                            unpk2(mul2(p2, mul2(i ? pk2(s4.z, s4.w) : pk2(s4.x, s4.y), rho2)), w0, w1);
+                            split(c, w0, w1);
+                        }
+                    }
+                } else {
+                    const uint64_t nru2 = pk2(-ru, -ru);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 v4 = fv[q];
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const int c = 4 * q + i;
+                            const uint64_t x2 = pk2(sv[c], sv[c + 1]);
+                            float p0, p1, w0, w1;
+                            unpk2(fma2(x2, fq2, nmu2), p0, p1);
+                            ls2 = add2(ls2, pk2(ex2(p0), ex2(p1)));
+                            unpk2(fma2(x2, fq2, add2(i ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y), nru2)), w0, w1);
+                            split(c, ex2(w0), ex2(w1));
+                        }
                     }
                 }
+                float ls0, ls1;
+                unpk2(ls2, ls0, ls1);
                 l_run += ls0 + ls1;
                 tmem_st16(lane_base + colS + 32 + 16 * h, lo);
                 tmem_st16(lane_base + colS + 16 * h, hi);
