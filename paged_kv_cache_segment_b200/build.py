@@ -1,4 +1,5 @@
-"""Build libtfpaged.so in this package directory with nvcc for sm_100a.
+"""Build libtfpaged.so in this package directory with nvcc for sm_100a, and
+_serve.so, the compiled argument marshalling of serving.py, with g++.
 
     python -m paged_kv_cache_segment_b200.build [--verbose-ptxas]
 
@@ -15,6 +16,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtfpaged.so")
+EXT = os.path.join(HERE, "_serve.so")
+EXT_SRC = os.path.join(CSRC, "serve_ext.cpp")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -32,10 +36,35 @@ def headers() -> list[str]:
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in sources() + headers())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    return any(os.path.getmtime(f) > t for f in sources() + headers() + [EXT_SRC])
+
+
+def compile_ext(obj: str) -> str:
+    """Compile serve_ext.cpp against this interpreter and torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ce
+
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    inc = [d for p in [*ce.include_paths(), sysconfig.get_paths()["include"], cuda_inc] for d in ("-isystem", p)]
+    subprocess.run([CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, "-c", EXT_SRC, "-o",
+                    obj], check=True)
+    return obj
+
+
+def link_ext(obj: str) -> str:
+    """Link _serve.so with libtfpaged.so beside it and with torch's libraries (loaded by `import torch`)."""
+    import torch
+
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    subprocess.run([CXX, "-shared", "-s", obj, "-o", EXT, "-L", HERE, "-l:libtfpaged.so", "-Wl,-rpath,$ORIGIN", "-L",
+                    torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
+    return EXT
 
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
@@ -59,8 +88,10 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        ext = ex.submit(compile_ext, os.path.join(objdir, "serve_ext.o"))
         objs = list(ex.map(compile_one, sources()))
     subprocess.run([NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", LIB], check=True)
+    link_ext(ext.result())
     return LIB
 
 

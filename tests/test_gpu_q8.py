@@ -408,3 +408,31 @@ def test_a_decode_step_over_the_8_bit_cache():
     am = torch.empty(4, dtype=torch.int32, device=DEV)
     tf.tf_argmax_rows(logits, am, fl8)
     assert (am.cpu().numpy() == r[3][:, 0]).all()
+
+
+def test_shapes_and_devices_the_binding_refuses():
+    b, sides, c = q8_batch("e4m3", 81, rows=[1, 1], keys=[40, 16], n_q_heads=8, n_kv_heads=2, head_dim=64, page_size=16)
+    st, pt, sg = status_word(), dev(b.page_table), dev(b.segs)
+    k = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="shapes disagree"):
+        tf.tf_kv_append_q8(k[:, :1].contiguous(), k[:, :1].contiguous(), c, pt, sg, status=st)
+    with pytest.raises(ValueError, match="contiguous"):
+        tf.tf_kv_append_q8(k.transpose(0, 1), k, c, pt, sg, status=st)
+    with pytest.raises(TypeError, match="dtype"):
+        tf.tf_kv_append_q8(k.float(), k.float(), c, pt, sg, status=st)
+    with pytest.raises(ValueError, match="differ in length"):
+        tf.tf_kv_append_q8(k, k, c, pt, sg, status=st, segs_host=b.segs[:1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        tf.tf_kv_append_q8(k, k.cpu(), c, pt, sg, status=st)
+    out, fl = torch.zeros((2, 8, 64), device=DEV), torch.zeros((2, 8), dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(tf.tf_paged_attn_q8_workspace_bytes(2, 8, 64, 2), dtype=torch.uint8, device=DEV)
+    kw = dict(scale=0.125, n_splits_max=2, workspace=ws, status=st)
+    with pytest.raises(ValueError, match="shapes disagree"):
+        tf.tf_paged_attn_q8(dev(b.q), c, pt, sg, out=out[:1], flags=fl, **kw)
+    with pytest.raises(tf.TfError, match="TF_ERR_WORKSPACE|workspace"):
+        tf.tf_paged_attn_q8(dev(b.q), c, pt, sg, out=out, flags=fl, **dict(kw, workspace=ws[:-1]))
+    # tables as lists and as int64 are converted; the same call still stands
+    tf.tf_paged_attn_q8(dev(b.q), c, pt, sg, out=out, flags=fl, segs_host=b.segs.tolist(),
+                        page_table_host=b.page_table.astype(np.int64), **kw)
+    ref, rf, vmax = reference(b, sides, "e4m3")
+    sv.check_attention(out.cpu().numpy(), fl.cpu().numpy(), ref, rf, vmax, False)
