@@ -8,21 +8,23 @@
 // once, where x * c - m * c would carry the rounding of m * c into every term.
 // Every thread keeps its own m, l and t; they are joined once a row.
 //
-// A CTA (512 threads) owns a row's columns, or 1/CL of them with a cluster of CL
-// CTAs a row when there are few rows.  It walks them in chunks that a thread
-// holds in registers (four 16-byte vectors), the next chunk's loads in flight
-// while the current one folds, across the row's end too, and without a barrier
-// inside the row.  Vectors are aligned to 16 bytes whatever the row's own
-// alignment: the grid of vectors starts up to 15 bytes before the row, and only
-// the vectors that cross its ends load by element.
+// A CTA owns a row's columns, or 1/CL of them with a cluster of CL CTAs a row
+// when there are few rows.  It walks them in chunks that a thread holds in
+// registers (four 16-byte vectors), the next chunk's loads in flight while the
+// current one folds, and without a barrier inside the row.  Vectors are aligned
+// to 16 bytes whatever the row's own alignment: the grid of vectors starts up to
+// 15 bytes before the row, and only the vectors that cross its ends load by
+// element.  Many rows take CTAs of 256 threads, four an SM, whose row ends (a few
+// barriers, a scan, a ranking) hide behind each other's streaming; short rows
+// take 64 threads, few rows 512 or 1,024.
 //
 // Top k: elements are ordered by a 64-bit key, the value's order-preserving image
 // above the complement of the column, so keys are distinct and ties go to the
 // lower column.  During the pass a thread keeps only its largest value.  The k-th
-// largest of the 128 largest values of groups of four threads is a threshold
-// that at least k elements reach, and few others do (some k + k^2 / 256 of random
-// rows): only the threads whose own maximum reaches it read their columns again,
-// from L2, and put the elements that do on a list in shared memory, which is
+// largest of the largest values of groups of four threads (or two) is a threshold
+// that at least k elements reach, and few others do: only the threads whose own
+// maximum reaches it have their columns read again, from L2 and by their whole
+// warp, and the elements that reach it go to a list in shared memory, which is
 // ranked by counting.  Should the list overflow (a thousand columns tied at the
 // threshold), the k largest keys are taken one at a time: every thread holds its
 // best remaining key, and after each block-wide maximum only the thread that held
@@ -43,14 +45,16 @@ namespace cg = cooperative_groups;
 namespace tfp {
 namespace {
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpBatch = 4;       // 16-byte vectors a thread holds of a chunk
+constexpr int kLpBatch = 4;     // 16-byte vectors a thread holds of a chunk
 constexpr int kLpMaxTop = 32;
-constexpr int kLpGroups = kLpThreads / 4;  // groups of four threads, each with its largest value
-constexpr int kLpList = 1024;              // candidates of a row's columns in a CTA
+constexpr int kLpList = 1024;   // candidates of a row's columns in a CTA
 constexpr int kLpMaxCluster = 8;
-// With fewer columns than would fill kLpMaxTop groups, the list holds them all.
+
+// Threads a group, each group with its largest value: 32 groups of 64 threads, 64
+// of 256, 128 of more, at least kLpMaxTop of them.  With fewer columns than would
+// fill that many groups the list holds them all (1,024-thread CTAs have more).
+template <int NT>
+constexpr int lp_group() { return NT == 64 ? 2 : (NT == 1024 ? 8 : 4); }
 static_assert(kLpMaxTop * 4 * 8 <= kLpList, "a row without k filled groups must fit the list");
 
 struct LogprobParams {
@@ -111,16 +115,17 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
 
 // Ranks the n distinct keys of `list` and puts the k largest, largest first,
 // into `top` (0 past the n-th): a warp a key, 32 of the others at a time.
+template <int NT>
 __device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uint64_t *top) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n; i += kLpWarps) {
+    for (int i = threadIdx.x >> 5; i < n; i += NT / 32) {
         const uint64_t mine = list[i];
         int rank = 0;
         for (int j = 0; j < n; j += 32)
             rank += __popc(__ballot_sync(0xffffffffu, j + lane < n && list[min(j + lane, n - 1)] > mine));
         if (lane == 0 && rank < k) top[rank] = mine;
     }
-    for (int i = n + threadIdx.x; i < k; i += kLpThreads) top[i] = 0ull;
+    for (int i = n + threadIdx.x; i < k; i += NT) top[i] = 0ull;
 }
 
 // A masked column (-infinity) enters the sums as this finite value, whose term
@@ -171,307 +176,314 @@ struct Elem<uint16_t> {
     }
 };
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 2) logprob_kernel(const LogprobParams p) {
+template <typename T, bool TOP, int NT>
+__global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel(const LogprobParams p) {
     using E = Elem<T>;
     constexpr int EPV = E::kPer;
+    constexpr int NW = NT / 32, GT = lp_group<NT>(), NG = NT / GT;
     cg::cluster_group cluster = cg::this_cluster();
     const int CL = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ Stat w_stat[kLpWarps];
-    __shared__ float s_group[TOP ? kLpGroups : 1], s_tau;
-    __shared__ uint64_t s_list[TOP ? kLpList : 1], s_top[kLpMaxTop], s_best[kLpWarps];
+    __shared__ Stat w_stat[NW];
+    __shared__ float s_group[TOP ? NG : 1], s_tau;
+    __shared__ uint64_t s_list[TOP ? kLpList : 1], s_top[kLpMaxTop], s_best[NW];
     __shared__ int s_n;
-    // rank 0's slots, filled by every CTA of the cluster, two buffers by row parity
-    __shared__ Stat x_stat[2][kLpMaxCluster];
-    __shared__ uint64_t x_top[2][TOP ? kLpMaxCluster * kLpMaxTop : 1];
+    // rank 0's slots, filled by every CTA of the cluster
+    __shared__ Stat x_stat[kLpMaxCluster];
+    __shared__ uint64_t x_top[TOP ? kLpMaxCluster * kLpMaxTop : 1];
+    // remote shared memory only once every CTA of the cluster runs: arrive here, wait before the first store
     if (CL > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    bool joined = CL == 1;
     const float c = p.scale * kLog2e;
     const int K = p.top_k;
 
-    // this CTA's vectors [v0, v1) of a row; vector v holds columns v * EPV - mis ...
-    struct Row {
-        const T *at;
-        int mis, v0, v1, n_chunks;
-    };
-    auto open = [&](int r) {
-        Row w;
-        w.at = static_cast<const T *>(p.logits) + (int64_t)r * p.ld;
-        w.mis = (int)((reinterpret_cast<uintptr_t>(w.at) & 15u) / sizeof(T));
-        const int nv = (w.mis + p.n_cols + EPV - 1) / EPV, per = (nv + CL - 1) / CL;
-        w.v0 = min(nv, rank * per);
-        w.v1 = min(nv, w.v0 + per);
-        w.n_chunks = max(1, (w.v1 - w.v0 + kLpBatch * kLpThreads - 1) / (kLpBatch * kLpThreads));
-        return w;
-    };
-    // vector v of a row; columns outside the row (and vectors past this CTA's) are masked
-    auto load_vec = [&](const Row &w, int v, uint32_t (&x)[4]) {
-        const int c0 = v * EPV - w.mis;
-        if (v < w.v1 && c0 >= 0 && c0 + EPV <= p.n_cols) {
-            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(w.at + c0));
+    // this CTA's vectors [v0, v1) of the row; vector v holds columns v * EPV - mis ...
+    const int64_t row = blockIdx.x / (unsigned)CL;
+    const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
+    const int mis = (int)((reinterpret_cast<uintptr_t>(at) & 15u) / sizeof(T));
+    const int nv = (mis + p.n_cols + EPV - 1) / EPV, per = (nv + CL - 1) / CL;
+    const int v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
+    const int n_chunks = max(1, (v1 - v0 + kLpBatch * NT - 1) / (kLpBatch * NT));
+    // columns outside the row (and vectors past this CTA's) are masked
+    auto load_vec = [&](int v, uint32_t (&x)[4]) {
+        const int c0 = v * EPV - mis;
+        if (v < v1 && c0 >= 0 && c0 + EPV <= p.n_cols) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + c0));
             x[0] = y.x;
             x[1] = y.y;
             x[2] = y.z;
             x[3] = y.w;
         } else {
             x[0] = x[1] = x[2] = x[3] = EPV == 4 ? 0xff800000u : 0xff80ff80u;
-            if (v < w.v1) {
+            if (v < v1) {
 #pragma unroll
                 for (int e = 0; e < EPV; ++e)
-                    if (c0 + e >= 0 && c0 + e < p.n_cols) E::put(x, e, E::load(w.at + c0 + e));
+                    if (c0 + e >= 0 && c0 + e < p.n_cols) E::put(x, e, E::load(at + c0 + e));
             }
         }
     };
-    auto load = [&](const Row &w, int chunk, uint32_t (&x)[kLpBatch][4]) {
+    auto load = [&](int chunk, uint32_t (&x)[kLpBatch][4]) {
+        const int v = v0 + chunk * kLpBatch * NT;  // the chunk's first vector
+        if (v * EPV - mis >= 0 && v + kLpBatch * NT <= v1 && (v + kLpBatch * NT) * EPV - mis <= p.n_cols) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(at + (v * EPV - mis)) + tid;  // all inside the row
 #pragma unroll
-        for (int k = 0; k < kLpBatch; ++k) load_vec(w, w.v0 + (chunk * kLpBatch + k) * kLpThreads + tid, x[k]);
+            for (int k = 0; k < kLpBatch; ++k) {
+                const uint4 y = __ldg(src + k * NT);
+                x[k][0] = y.x;
+                x[k][1] = y.y;
+                x[k][2] = y.z;
+                x[k][3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k) load_vec(v + k * NT + tid, x[k]);
+        }
     };
 
-    uint32_t cur[kLpBatch][4], nxt[kLpBatch][4];
-    int row = blockIdx.y, it = 0;
-    if (row >= p.n_rows) {
-        if (!joined) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        return;  // (the whole cluster: its CTAs share blockIdx.y)
+    Stat st{-INFINITY, 0.f, 0.f};
+    auto fold = [&](const uint32_t (&x)[kLpBatch][4]) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(x[k]));
+        if (mx > st.m) st.to(mx, c);
+        if (st.m > kLpCareful || st.m == -INFINITY) {
+            // (all masked so far: the reference is 0, every term 0 or a NaN)
+            const float ref = st.m == -INFINITY ? 0.f : -st.m;
+            const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
+            uint64_t l2 = pk2(st.l, 0.f), t2 = pk2(st.t, 0.f);
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < EPV / 2; ++e) {
+                    const uint64_t d2 = add2(E::pair(x[k], e), ref2);
+                    float y0, y1;
+                    unpk2(mul2(d2, c2), y0, y1);
+                    const uint64_t q2 = pk2(ex2(y0), ex2(y1));
+                    l2 = add2(l2, q2);
+                    t2 = fma2(q2, d2, t2);
+                }
+            float a, b;
+            unpk2(l2, a, b);
+            st.l = a + b;
+            unpk2(t2, a, b);
+            st.t = a + b;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    const float d = max_nan(E::get(x[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
+                    const float q = ex2(d * c);
+                    st.l += q;
+                    st.t = fmaf(q, d, st.t);
+                }
+        }
+    };
+    uint32_t cur[kLpBatch][4];
+    load(0, cur);
+    if constexpr (TOP) {
+        if (tid == 0) s_n = 0;
     }
-    Row w = open(row);
-    load(w, 0, cur);
-    for (; row < p.n_rows; row += gridDim.y, ++it) {
-        Stat st{-INFINITY, 0.f, 0.f};
-        const int next_row = row + (int)gridDim.y;
-        Row wn = w;
-        if constexpr (TOP) {
-            if (tid == 0) s_n = 0;
+    for (int ch = 0; ch < n_chunks; ch += 2) {
+        uint32_t nxt[kLpBatch][4];
+        if (ch + 1 < n_chunks) load(ch + 1, nxt);
+        fold(cur);
+        if (ch + 1 < n_chunks) {
+            if (ch + 2 < n_chunks) load(ch + 2, cur);
+            fold(nxt);
         }
-        for (int ch = 0; ch < w.n_chunks; ++ch) {
-            // the next chunk's loads, of this row or the next one
-            if (ch + 1 < w.n_chunks) {
-                load(w, ch + 1, nxt);
-            } else if (next_row < p.n_rows) {
-                wn = open(next_row);
-                load(wn, 0, nxt);
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(cur[k]));
-            if (mx > st.m) st.to(mx, c);
-            if (st.m > kLpCareful || st.m == -INFINITY) {
-                // (all masked so far: the reference is 0, every term 0 or a NaN)
-                const float ref = st.m == -INFINITY ? 0.f : -st.m;
-                const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
-                uint64_t l2 = pk2(st.l, 0.f), t2 = pk2(st.t, 0.f);
-#pragma unroll
-                for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                    for (int e = 0; e < EPV / 2; ++e) {
-                        const uint64_t d2 = add2(E::pair(cur[k], e), ref2);
-                        float y0, y1;
-                        unpk2(mul2(d2, c2), y0, y1);
-                        const uint64_t q2 = pk2(ex2(y0), ex2(y1));
-                        l2 = add2(l2, q2);
-                        t2 = fma2(q2, d2, t2);
-                    }
-                float a, b;
-                unpk2(l2, a, b);
-                st.l = a + b;
-                unpk2(t2, a, b);
-                st.t = a + b;
-            } else {
-#pragma unroll
-                for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                    for (int e = 0; e < EPV; ++e) {
-                        const float d = max_nan(E::get(cur[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
-                        const float q = ex2(d * c);
-                        st.l += q;
-                        st.t = fmaf(q, d, st.t);
-                    }
-            }
-            if (ch + 1 < w.n_chunks) {
-#pragma unroll
-                for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) cur[k][e] = nxt[k][e];
-            }
-        }
-        if constexpr (TOP) {
-            const float mine = st.m;  // this thread's largest logit
-            // ---- the threshold: the K-th largest of the groups' largest values
-            float gm = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-            if ((lane & 3) == 0) s_group[tid >> 2] = gm;
-            __syncthreads();
-            {
-                float v[kLpGroups / 32];
-#pragma unroll
-                for (int i = 0; i < kLpGroups / 32; ++i) v[i] = s_group[32 * i + lane];
-#pragma unroll
-                for (int j = 0; j < kLpGroups / kLpWarps; ++j) {
-                    const int at = warp * (kLpGroups / kLpWarps) + j;
-                    const float x = s_group[at];
-                    int rank = 0;
-#pragma unroll
-                    for (int i = 0; i < kLpGroups / 32; ++i)  // equal values rank by place
-                        rank += __popc(__ballot_sync(0xffffffffu, v[i] > x || (v[i] == x && 32 * i + lane < at)));
-                    if (lane == 0 && rank == K - 1) s_tau = x;
-                }
-            }
-            __syncthreads();
-            const float tau = s_tau;
-            // ---- the threads that reach it go over their columns again
-            auto scan = [&](auto &&f) {  // f(value, column) for every unmasked column of this thread
-                for (int v = w.v0 + tid; v < w.v1; v += kLpBatch * kLpThreads) {
-                    uint32_t x[kLpBatch][4];
-#pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k) load_vec(w, v + k * kLpThreads, x[k]);
-#pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k) {
-                        const int c0 = (v + k * kLpThreads) * EPV - w.mis;
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e) f(E::get(x[k], e), c0 + e);
-                    }
-                }
-            };
-            if (mine >= tau && mine > -INFINITY)
-                scan([&](float x, int col) {
-                    if (x >= tau && x > -INFINITY) {
-                        const int at = atomicAdd(&s_n, 1);
-                        if (at < kLpList) s_list[at] = key64(x, col);
-                    }
-                });
-            __syncthreads();
-            if (s_n > kLpList) {
-                // one at a time: the largest key below the last one taken
-                uint64_t best = 0;
-                auto look = [&](uint64_t below) {
-                    best = 0;
-                    scan([&](float x, int col) {
-                        const uint64_t y = key64(x, col);
-                        if (y < below && y > best) best = y;
-                    });
-                };
-                look(~0ull);
-                for (int q = 0; q < K; ++q) {
-                    uint64_t b = best;
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) {
-                        const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
-                        b = y > b ? y : b;
-                    }
-                    if (lane == 0) s_best[warp] = b;
-                    __syncthreads();
-#pragma unroll
-                    for (int i = 0; i < kLpWarps; ++i) b = s_best[i] > b ? s_best[i] : b;
-                    if (tid == 0) s_top[q] = b;
-                    if (b != 0 && b == best) look(b);
-                    __syncthreads();
-                }
-            } else {
-                rank_top(s_list, s_n, K, s_top);
-            }
-        }
-        // ---- the CTA's statistics and top k
+    }
+
+    // ---- the CTA's statistics
+    {
+        Stat all = st;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-            const Stat y{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.l, o),
-                         __shfl_xor_sync(0xffffffffu, st.t, o)};
-            st = join(st, y, c);
+            const Stat y{__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.l, o),
+                         __shfl_xor_sync(0xffffffffu, all.t, o)};
+            all = join(all, y, c);
         }
-        if (lane == 0) w_stat[warp] = st;
-        if (!joined) {  // remote shared memory only once every CTA of the cluster runs
-            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-            joined = true;
+        if (lane == 0) w_stat[warp] = all;
+    }
+    if constexpr (TOP) {
+        const float mine = st.m;  // this thread's largest logit
+        // ---- the threshold: the K-th largest of the groups' largest values
+        float gm = mine;
+#pragma unroll
+        for (int o = 1; o < GT; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+        if (tid % GT == 0) s_group[tid / GT] = gm;
+        __syncthreads();
+        {
+            float v[NG / 32];
+#pragma unroll
+            for (int i = 0; i < NG / 32; ++i) v[i] = s_group[32 * i + lane];
+#pragma unroll
+            for (int j = 0; j < NG / NW; ++j) {
+                const int g = warp * (NG / NW) + j;
+                const float x = s_group[g];
+                int r = 0;
+#pragma unroll
+                for (int i = 0; i < NG / 32; ++i)  // equal values rank by place
+                    r += __popc(__ballot_sync(0xffffffffu, v[i] > x || (v[i] == x && 32 * i + lane < g)));
+                if (lane == 0 && r == K - 1) s_tau = x;
+            }
         }
         __syncthreads();
-        Stat all = w_stat[0];
+        const float tau = s_tau;
+        // ---- the threads that reach it go over their columns again
+        // f(value, column) for the unmasked columns of a vector no smaller than `want`
+        auto each = [&](const uint32_t (&x)[4], int v, float want, auto &&f) {
+            const float most = E::most(x);
+            if (!(most >= want) || most == -INFINITY) return;
+            const int c0 = v * EPV - mis;
 #pragma unroll
-        for (int i = 1; i < kLpWarps; ++i) all = join(all, w_stat[i], c);
-        if (CL > 1) {
-            const int buf = it & 1;
-            if (tid == 0) *cluster.map_shared_rank(&x_stat[buf][rank], 0) = all;
-            if constexpr (TOP) {
-                if (tid < K) *cluster.map_shared_rank(&x_top[buf][rank * K + tid], 0) = s_top[tid];
+            for (int e = 0; e < EPV; ++e) {
+                const float y = E::get(x, e);
+                if (y >= want && y > -INFINITY) f(y, c0 + e);
             }
-            cluster.sync();
-            if (rank == 0) {
-                all = x_stat[buf][0];
-                for (int i = 1; i < CL; ++i) all = join(all, x_stat[buf][i], c);
-                if constexpr (TOP) {
-                    // a key's rank: its place in its own sorted list and, in each of the
-                    // others, how many are larger; empty places (0) come last
-                    for (int i = tid; i < CL * K; i += kLpThreads) {
-                        const uint64_t mine = x_top[buf][i];
-                        int r = i % K;
-                        for (int a = 0; a < CL; ++a) {
-                            if (a == i / K) continue;
-                            const uint64_t *list = x_top[buf] + a * K;
-                            int lo = 0, hi = K;  // list[0 .. lo) > mine
-                            while (lo < hi) {
-                                const int mid = (lo + hi) >> 1;
-                                // equal only when both are empty: by list, so that every place is taken once
-                                if (list[mid] > mine || (list[mid] == mine && a < i / K))
-                                    lo = mid + 1;
-                                else
-                                    hi = mid;
-                            }
-                            r += lo;
-                        }
-                        if (r < K) s_top[r] = mine;
+        };
+        // a warp looks through one such thread's vectors together, a vector a lane
+        for (uint32_t hits = __ballot_sync(0xffffffffu, mine >= tau && mine > -INFINITY); hits; hits &= hits - 1) {
+            const int first = v0 + warp * 32 + __ffs(hits) - 1;
+            for (int v = first + lane * NT; v - lane * NT < v1; v += 2 * 32 * NT) {
+                uint32_t x[2][4];
+                load_vec(v, x[0]);
+                load_vec(v + 32 * NT, x[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    each(x[k], v + k * 32 * NT, tau, [&](float y, int col) {
+                        const int i = atomicAdd(&s_n, 1);
+                        if (i < kLpList) s_list[i] = key64(y, col);
+                    });
+            }
+        }
+        __syncthreads();
+        if (s_n > kLpList) {
+            // one at a time: the largest key below the last one taken
+            uint64_t best = 0;
+            auto look = [&](uint64_t below) {
+                best = 0;
+                for (int v = v0 + tid; v < v1; v += kLpBatch * NT) {
+                    uint32_t x[kLpBatch][4];
+#pragma unroll
+                    for (int k = 0; k < kLpBatch; ++k) load_vec(v + k * NT, x[k]);
+#pragma unroll
+                    for (int k = 0; k < kLpBatch; ++k)
+                        each(x[k], v + k * NT, -INFINITY, [&](float y, int col) {
+                            const uint64_t key = key64(y, col);
+                            if (key < below && key > best) best = key;
+                        });
+                }
+            };
+            look(~0ull);
+            for (int q = 0; q < K; ++q) {
+                uint64_t b = best;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
+                    b = y > b ? y : b;
+                }
+                if (lane == 0) s_best[warp] = b;
+                __syncthreads();
+                for (int i = 0; i < NW; ++i) b = s_best[i] > b ? s_best[i] : b;
+                if (tid == 0) s_top[q] = b;
+                if (b != 0 && b == best) look(b);
+                __syncthreads();
+            }
+        } else {
+            rank_top<NT>(s_list, s_n, K, s_top);
+        }
+    }
+    __syncthreads();
+    Stat all{-INFINITY, 0.f, 0.f};
+    if (warp == 0) {
+        if (lane < NW) all = w_stat[lane];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const Stat y{__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.l, o),
+                         __shfl_xor_sync(0xffffffffu, all.t, o)};
+            all = join(all, y, c);
+        }
+    }
+    if (CL > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid == 0) *cluster.map_shared_rank(&x_stat[rank], 0) = all;
+        if constexpr (TOP) {
+            if (tid < K) *cluster.map_shared_rank(&x_top[rank * K + tid], 0) = s_top[tid];
+        }
+        cluster.sync();
+        if (rank != 0) return;
+        if (warp == 0) {
+            all = lane < CL ? x_stat[lane] : Stat{-INFINITY, 0.f, 0.f};
+#pragma unroll
+            for (int o = kLpMaxCluster / 2; o; o >>= 1) {
+                const Stat y{__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.l, o),
+                             __shfl_xor_sync(0xffffffffu, all.t, o)};
+                all = join(all, y, c);
+            }
+        }
+        if constexpr (TOP) {
+            // a key's rank: its place in its own sorted list and, in each of the
+            // others, how many are larger; empty places (0) come last
+            for (int i = tid; i < CL * K; i += NT) {
+                const uint64_t mine = x_top[i];
+                int r = i % K;
+                for (int a = 0; a < CL; ++a) {
+                    if (a == i / K) continue;
+                    const uint64_t *list = x_top + a * K;
+                    int lo = 0, hi = K;  // list[0 .. lo) before mine
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        // equal only when both are empty: by list, so that every place is taken once
+                        if (list[mid] > mine || (list[mid] == mine && a < i / K))
+                            lo = mid + 1;
+                        else
+                            hi = mid;
                     }
-                    __syncthreads();
+                    r += lo;
                 }
+                if (r < K) s_top[r] = mine;
             }
+            __syncthreads();
         }
-        if (rank == 0) {
-            const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
-            const float nan = __int_as_float(0x7fc00000);
-            const float log_l = logf(all.l);
-            if (tid == 0) {
-                if (p.entropy) p.entropy[row] = bad ? nan : log_l - p.scale * (all.t / all.l);
-                if (p.lse) p.lse[row] = bad ? nan : fmaf(p.scale, all.m, log_l);
-                p.flags[row] = bad ? 1 : 0;
-            }
-            for (int i = tid; i < p.n_tokens; i += kLpThreads) {
-                const int64_t at = (int64_t)row * p.n_tokens + i;
-                const int tok = p.tokens[at];
-                float lp = nan;
-                if (tok < 0 || tok >= p.n_cols)
-                    atomicOr(p.status, TF_DEV_BAD_TOKEN);
-                else if (!bad)
-                    lp = (E::load(w.at + tok) - all.m) * p.scale - log_l;
-                p.token_logprobs[at] = lp;
-            }
-            if constexpr (TOP) {
-                if (tid < K) {
-                    const uint64_t y = s_top[tid];
-                    const int64_t at = (int64_t)row * K + tid;
-                    p.top_ids[at] = (bad || y == 0) ? -1 : (int)~(uint32_t)y;
-                    p.top_logprobs[at] =
-                        bad ? nan : (y == 0 ? -INFINITY : (unkey32((uint32_t)(y >> 32)) - all.m) * p.scale - log_l);
-                }
-            }
+    }
+    // ---- warp 0 writes the row
+    if (warp != 0) return;
+    all.m = __shfl_sync(0xffffffffu, all.m, 0);
+    all.l = __shfl_sync(0xffffffffu, all.l, 0);
+    const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
+    const float nan = __int_as_float(0x7fc00000);
+    const float log_l = logf(all.l);
+    if (lane == 0) {
+        if (p.entropy) p.entropy[row] = bad ? nan : log_l - p.scale * (all.t / all.l);
+        if (p.lse) p.lse[row] = bad ? nan : fmaf(p.scale, all.m, log_l);
+        p.flags[row] = bad ? 1 : 0;
+    }
+    for (int i = lane; i < p.n_tokens; i += 32) {
+        const int64_t to = row * p.n_tokens + i;
+        const int tok = p.tokens[to];
+        float lp = nan;
+        if (tok < 0 || tok >= p.n_cols)
+            atomicOr(p.status, TF_DEV_BAD_TOKEN);
+        else if (!bad)
+            lp = (E::load(at + tok) - all.m) * p.scale - log_l;
+        p.token_logprobs[to] = lp;
+    }
+    if constexpr (TOP) {
+        if (lane < K) {
+            const uint64_t y = s_top[lane];
+            const int64_t to = row * K + lane;
+            p.top_ids[to] = (bad || y == 0) ? -1 : (int)~(uint32_t)y;
+            p.top_logprobs[to] =
+                bad ? nan : (y == 0 ? -INFINITY : (unkey32((uint32_t)(y >> 32)) - all.m) * p.scale - log_l);
         }
-        __syncthreads();  // the shared arrays serve the next row
-        w = wn;
-#pragma unroll
-        for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cur[k][e] = nxt[k][e];
     }
 }
 
-template <typename T, bool TOP>
-cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
-    // few rows: a cluster a row, so that the row's columns spread over the SMs
-    // (two CTAs an SM); a CTA keeps at least a chunk's worth of columns
-    const int chunk = Elem<T>::kPer * kLpBatch * kLpThreads;
-    const int sms = device_sms();
-    int cl = 1;
-    while (cl < kLpMaxCluster && (int64_t)p.n_rows * 2 * cl <= 2 * sms && (int64_t)cl * chunk < p.n_cols) cl *= 2;
-    const int64_t groups = (int64_t)2 * sms / cl > 0 ? (int64_t)2 * sms / cl : 1;
+template <typename T, bool TOP, int NT>
+cudaError_t launch_logprob_t(const LogprobParams &p, int cl, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)cl, (unsigned)(p.n_rows < groups ? p.n_rows : groups));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.gridDim = dim3((unsigned)p.n_rows * (unsigned)cl);
+    cfg.blockDim = dim3(NT);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -480,7 +492,22 @@ cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, TOP>, p);
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<T, TOP, NT>, p);
+}
+
+template <typename T, bool TOP>
+cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
+    const int sms = device_sms();
+    const int chunk = Elem<T>::kPer * kLpBatch;  // columns a thread holds
+    // short rows: one chunk of 64 threads or two, sixteen rows an SM at once
+    if (p.n_cols <= 2 * 64 * chunk && p.n_rows > sms) return launch_logprob_t<T, TOP, 64>(p, 1, st);
+    // many rows: four CTAs an SM
+    if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_logprob_t<T, TOP, 256>(p, 1, st);
+    if (p.n_rows > sms) return launch_logprob_t<T, TOP, 512>(p, 1, st);
+    // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads
+    int cl = 1;
+    while (cl < kLpMaxCluster && p.n_rows * 2 * cl <= sms && cl * 1024 * chunk < p.n_cols) cl *= 2;
+    return launch_logprob_t<T, TOP, 1024>(p, cl, st);
 }
 
 }  // namespace
