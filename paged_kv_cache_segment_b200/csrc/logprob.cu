@@ -8,27 +8,32 @@
 // once, where x * c - m * c would carry the rounding of m * c into every term.
 // Every thread keeps its own m, l and t; they are joined once a row.
 //
-// A CTA owns a row's columns, or 1/CL of them with a cluster of CL CTAs a row
-// when there are few rows.  It walks them in chunks that a thread holds in
-// registers (four 16-byte vectors), the next chunk's loads in flight while the
-// current one folds, and without a barrier inside the row.  Vectors are aligned
-// to 16 bytes whatever the row's own alignment: the grid of vectors starts up to
-// 15 bytes before the row, and only the vectors that cross its ends load by
-// element.  Many rows take CTAs of 256 threads, four an SM, whose row ends (a few
-// barriers, a scan, a ranking) hide behind each other's streaming; short rows
-// take 64 threads, few rows 512 or 1,024.
+// A row's columns are walked in chunks that a thread holds in registers (four
+// 16-byte vectors), the next chunk's loads in flight while the current one folds,
+// and without a barrier inside the row.  Vectors are aligned to 16 bytes whatever
+// the row's own alignment: the grid of vectors starts up to 15 bytes before the
+// row, and only the vectors that cross its ends load by element.
 //
 // Top k: elements are ordered by a 64-bit key, the value's order-preserving image
 // above the complement of the column, so keys are distinct and ties go to the
 // lower column.  During the pass a thread keeps only its largest value.  The k-th
-// largest of the largest values of groups of four threads (or two) is a threshold
-// that at least k elements reach, and few others do: only the threads whose own
-// maximum reaches it have their columns read again, from L2 and by their whole
-// warp, and the elements that reach it go to a list in shared memory, which is
-// ranked by counting.  Should the list overflow (a thousand columns tied at the
-// threshold), the k largest keys are taken one at a time: every thread holds its
-// best remaining key, and after each block-wide maximum only the thread that held
-// it looks for its next one.
+// largest of 32 groups' largest values is a threshold that at least k elements
+// reach, and few others do (some 32 ln(32 / (32 - k)) of random rows): only the
+// threads whose own maximum reaches it have their columns read again, from L2,
+// and the elements that reach it go to a list that is ranked by counting.  A list
+// that overflows means ties (a mask of the type's lowest value): then the
+// elements above the threshold are listed, and the columns equal to it in order
+// until there are k.  If even the former overflow (columns left to a few threads
+// only) the k largest keys are taken one at a time: slow, but never wrong.
+//
+// What follows a row's pass is latency: a threshold, a second look at L2, a
+// ranking, some 4 us for one warp or for many.  So one warp does it, beside the
+// streaming ones:
+//  - CTA mode: NT streaming threads leave their statistics in shared memory and
+//    go on to the next row while a finishing warp works on the last one (two
+//    buffers, four named barriers).  Persistent, four CTAs of 224 + 32 threads an
+//    SM; with few rows, 480 + 32 threads and a cluster of up to eight CTAs a row.
+//  - warp mode, for short rows: every warp streams and finishes rows of its own.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -45,16 +50,16 @@ namespace cg = cooperative_groups;
 namespace tfp {
 namespace {
 
-constexpr int kLpBatch = 4;     // 16-byte vectors a thread holds of a chunk
+constexpr int kLpBatch = 4;  // 16-byte vectors a thread holds of a chunk
 constexpr int kLpMaxTop = 32;
-constexpr int kLpList = 1024;   // candidates of a row's columns in a CTA
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpList = 1024;  // candidates of a row's columns in a CTA
 
-// Threads a group, each group with its largest value: 32 groups of 64 threads, 64
-// of 256, 128 of more, at least kLpMaxTop of them.  With fewer columns than would
+// Threads a group, each group with its largest value: 64 groups of 128 or 256
+// threads, 128 of more, at least kLpMaxTop of them.  With fewer columns than would
 // fill that many groups the list holds them all (1,024-thread CTAs have more).
 template <int NT>
-constexpr int lp_group() { return NT == 64 ? 2 : (NT == 1024 ? 8 : 4); }
+constexpr int lp_group() { return NT == 128 ? 2 : (NT == 1024 ? 8 : 4); }
 static_assert(kLpMaxTop * 4 * 8 <= kLpList, "a row without k filled groups must fit the list");
 
 struct LogprobParams {
@@ -113,21 +118,6 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
     return {M, a.l + b.l, a.t + b.t};
 }
 
-// Ranks the n distinct keys of `list` and puts the k largest, largest first,
-// into `top` (0 past the n-th): a warp a key, 32 of the others at a time.
-template <int NT>
-__device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uint64_t *top) {
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n; i += NT / 32) {
-        const uint64_t mine = list[i];
-        int rank = 0;
-        for (int j = 0; j < n; j += 32)
-            rank += __popc(__ballot_sync(0xffffffffu, j + lane < n && list[min(j + lane, n - 1)] > mine));
-        if (lane == 0 && rank < k) top[rank] = mine;
-    }
-    for (int i = n + threadIdx.x; i < k; i += NT) top[i] = 0ull;
-}
-
 // A masked column (-infinity) enters the sums as this finite value, whose term
 // is 0 and whose product with 0 is 0; x - m cannot overflow from it.  It also
 // stands in for logits below it, so a thread whose maximum is not far above it
@@ -176,6 +166,332 @@ struct Elem<uint16_t> {
     }
 };
 
+// One row's columns, or a CTA's share of them: vectors [v0, v1), vector v holding
+// columns v * kPer - mis and on; columns outside the row are masked.
+template <typename T>
+struct RowView {
+    static constexpr int kPer = Elem<T>::kPer;
+    const T *at;
+    int mis, v0, v1, n_cols;
+
+    __device__ __forceinline__ RowView(const LogprobParams &p, int64_t row, int rank, int cl) {
+        at = static_cast<const T *>(p.logits) + row * p.ld;
+        n_cols = p.n_cols;
+        mis = (int)((reinterpret_cast<uintptr_t>(at) & 15u) / sizeof(T));
+        const int nv = (mis + n_cols + kPer - 1) / kPer, per = (nv + cl - 1) / cl;
+        v0 = min(nv, rank * per);
+        v1 = min(nv, v0 + per);
+    }
+    __device__ __forceinline__ void vec(int v, uint32_t (&x)[4]) const {
+        const int c0 = v * kPer - mis;
+        if (v < v1 && c0 >= 0 && c0 + kPer <= n_cols) {
+            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + c0));
+            x[0] = y.x;
+            x[1] = y.y;
+            x[2] = y.z;
+            x[3] = y.w;
+        } else {
+            x[0] = x[1] = x[2] = x[3] = kPer == 4 ? 0xff800000u : 0xff80ff80u;
+            if (v < v1) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (c0 + e >= 0 && c0 + e < n_cols) Elem<T>::put(x, e, Elem<T>::load(at + c0 + e));
+            }
+        }
+    }
+    // chunk `c` of thread `tid` of `nt`
+    __device__ __forceinline__ void chunk(int c, int tid, int nt, uint32_t (&x)[kLpBatch][4]) const {
+        const int v = v0 + c * kLpBatch * nt;  // the chunk's first vector
+        if (v * kPer - mis >= 0 && v + kLpBatch * nt <= v1 && (v + kLpBatch * nt) * kPer - mis <= n_cols) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(at + (v * kPer - mis)) + tid;  // all inside the row
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k) {
+                const uint4 y = __ldg(src + k * nt);
+                x[k][0] = y.x;
+                x[k][1] = y.y;
+                x[k][2] = y.z;
+                x[k][3] = y.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k) vec(v + k * nt + tid, x[k]);
+        }
+    }
+    __device__ __forceinline__ int chunks(int nt) const {
+        return max(1, (v1 - v0 + kLpBatch * nt - 1) / (kLpBatch * nt));
+    }
+};
+
+// Folds a chunk into a thread's statistics; the chunk's largest value.
+template <typename T>
+__device__ __forceinline__ float fold(Stat &st, const uint32_t (&x)[kLpBatch][4], float c) {
+    using E = Elem<T>;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(x[k]));
+    if (mx > st.m) st.to(mx, c);
+    if (st.m > kLpCareful || st.m == -INFINITY) {
+        // (all masked so far: the reference is 0, every term 0 or a NaN)
+        const float ref = st.m == -INFINITY ? 0.f : -st.m;
+        const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
+        uint64_t l2 = pk2(st.l, 0.f), t2 = pk2(st.t, 0.f);
+#pragma unroll
+        for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+            for (int e = 0; e < E::kPer / 2; ++e) {
+                const uint64_t d2 = add2(E::pair(x[k], e), ref2);
+                float y0, y1;
+                unpk2(mul2(d2, c2), y0, y1);
+                const uint64_t q2 = pk2(ex2(y0), ex2(y1));
+                l2 = add2(l2, q2);
+                t2 = fma2(q2, d2, t2);
+            }
+        float a, b;
+        unpk2(l2, a, b);
+        st.l = a + b;
+        unpk2(t2, a, b);
+        st.t = a + b;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+            for (int e = 0; e < E::kPer; ++e) {
+                const float d = max_nan(E::get(x[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
+                const float q = ex2(d * c);
+                st.l += q;
+                st.t = fmaf(q, d, st.t);
+            }
+    }
+    return mx;
+}
+
+// Shared memory of a finishing warp.
+template <int NT, int LIST>
+struct FinishBuf {
+    uint64_t list[LIST], top[kLpMaxTop];
+    uint16_t hits[NT];
+    int n;
+};
+
+// One warp ends a row (or a CTA's share): lane's s[i] are the statistics of
+// streaming thread 32 i + lane of NT.  Returns the joined statistics; with TOP
+// the K largest keys are in b.top, largest first, 0 past the unmasked columns.
+template <typename T, bool TOP, int NT, int LIST>
+__device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT / 32], FinishBuf<NT, LIST> &b, int K,
+                                       float c) {
+    using E = Elem<T>;
+    constexpr int NI = NT / 32, EPV = E::kPer;
+    const int lane = threadIdx.x & 31;
+    float lm = s[0].m;  // the lane's largest
+#pragma unroll
+    for (int i = 1; i < NI; ++i) lm = fmaxf(lm, s[i].m);
+    float M = lm;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    Stat all{M, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        Stat y = s[i];
+        if (M != -INFINITY) y.to(M, c);
+        all.l += y.l;
+        all.t += y.t;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        all.l += __shfl_xor_sync(0xffffffffu, all.l, o);
+        all.t += __shfl_xor_sync(0xffffffffu, all.t, o);
+    }
+    if constexpr (TOP) {
+        // ---- the threshold: the K-th largest of the lanes' largest values (equal ones rank by lane)
+        int r = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float y = __shfl_sync(0xffffffffu, lm, j);
+            r += (y > lm || (y == lm && j < lane)) ? 1 : 0;
+        }
+        const float tau = __shfl_sync(0xffffffffu, lm, __ffs(__ballot_sync(0xffffffffu, r == K - 1)) - 1);
+        const int nk = (w.v1 - w.v0 + NT - 1) / NT;  // vectors a thread
+        // the streaming threads whose largest value is at least `want` (above it, if strict)
+        auto find = [&](float want, bool strict) -> int {
+            int n = 0;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float m = s[i].m;
+                const bool hit = (strict ? m > want : m >= want) && m > -INFINITY;
+                const uint32_t who = __ballot_sync(0xffffffffu, hit);
+                if (hit) b.hits[n + __popc(who & ((1u << lane) - 1u))] = (uint16_t)(32 * i + lane);
+                n += __popc(who);
+            }
+            if (lane == 0) b.n = 0;
+            __syncwarp();
+            return n;
+        };
+        // a vector's elements at least (above, if strict) `want`, to the list
+        auto take = [&](const uint32_t (&x)[4], int v, float want, bool strict) {
+            const float most = E::most(x);
+            if (!(strict ? most > want : most >= want) || most == -INFINITY) return;
+            const int c0 = v * EPV - w.mis;
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                const float y = E::get(x, e);
+                if ((strict ? y > want : y >= want) && y > -INFINITY) {
+                    const int at = atomicAdd(&b.n, 1);
+                    if (at < LIST) b.list[at] = key64(y, c0 + e);
+                }
+            }
+        };
+        // the hit threads' vectors, four a lane in flight; false if the list overflows
+        auto look = [&](int n_hits, float want, bool strict) -> bool {
+            const int total = n_hits * nk;
+            for (int base = 0; base < total; base += 4 * 32) {
+                uint32_t x[4][4];
+                int v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int idx = base + 32 * k + lane, h = idx / nk;
+                    v[k] = idx < total ? w.v0 + b.hits[h] + (idx - h * nk) * NT : w.v1;
+                    w.vec(v[k], x[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) take(x[k], v[k], want, strict);
+                __syncwarp();
+                const int n = b.n;
+                __syncwarp();
+                if (n > LIST) return false;
+            }
+            return true;
+        };
+        bool ok = look(find(tau, false), tau, false);
+        if (!ok && tau > -INFINITY) {
+            // ties: what is above the threshold, then the first columns equal to it
+            ok = look(find(tau, true), tau, true);
+            int n = b.n;
+            for (int v = w.v0; ok && n < K && v < w.v1; v += 32) {
+                uint32_t x[4];
+                w.vec(v + lane, x);
+                const int c0 = (v + lane) * EPV - w.mis;
+                int mine = 0;
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) mine += E::get(x, e) == tau ? 1 : 0;
+                int before = mine;  // equal columns in this and the lower lanes
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, before, o);
+                    if (lane >= o) before += y;
+                }
+                const int found = __shfl_sync(0xffffffffu, before, 31);
+                before -= mine;
+#pragma unroll
+                for (int e = 0; e < EPV; ++e)
+                    if (E::get(x, e) == tau) {
+                        if (n + before < K) b.list[n + before] = key64(tau, c0 + e);
+                        ++before;
+                    }
+                n = min(K, n + found);
+            }
+            __syncwarp();
+            if (lane == 0 && ok) b.n = n;
+            __syncwarp();
+        }
+        if (ok) {
+            // ---- rank by counting: a key a lane
+            const int n = b.n;
+            for (int i = lane; i < ((n + 31) & ~31); i += 32) {
+                const uint64_t mine = i < n ? b.list[i] : ~0ull;
+                int rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) rank += b.list[j] > mine ? 1 : 0;
+                if (i < n && rank < K) b.top[rank] = mine;
+            }
+            for (int i = n + lane; i < K; i += 32) b.top[i] = 0ull;
+        } else {
+            // ---- one at a time: the largest key below the last one taken, a lane's share each
+            uint64_t last = ~0ull, best = 0;
+            bool stale = true;
+            for (int q = 0; q < K; ++q) {
+                if (stale) {
+                    best = 0;
+                    for (int v = w.v0 + lane; v < w.v1; v += 32 * kLpBatch) {
+                        uint32_t x[kLpBatch][4];
+#pragma unroll
+                        for (int k = 0; k < kLpBatch; ++k) w.vec(v + 32 * k, x[k]);
+#pragma unroll
+                        for (int k = 0; k < kLpBatch; ++k)
+#pragma unroll
+                            for (int e = 0; e < EPV; ++e) {
+                                const uint64_t y = key64(E::get(x[k], e), (v + 32 * k) * EPV - w.mis + e);
+                                if (y < last && y > best) best = y;
+                            }
+                    }
+                }
+                __syncwarp();
+                uint64_t top = best;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) {
+                    const uint64_t y = __shfl_xor_sync(0xffffffffu, top, o);
+                    top = y > top ? y : top;
+                }
+                if (lane == 0) b.top[q] = top;
+                last = top;
+                stale = top != 0 && top == best;
+            }
+        }
+        __syncwarp();
+    }
+    return all;
+}
+
+// One warp writes a row's outputs.
+template <typename T, bool TOP>
+__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const Stat &all, const uint64_t *top) {
+    const int lane = threadIdx.x & 31, K = p.top_k;
+    const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
+    const float nan = __int_as_float(0x7fc00000);
+    const float log_l = logf(all.l);
+    if (lane == 0) {
+        if (p.entropy) p.entropy[row] = bad ? nan : log_l - p.scale * (all.t / all.l);
+        if (p.lse) p.lse[row] = bad ? nan : fmaf(p.scale, all.m, log_l);
+        p.flags[row] = bad ? 1 : 0;
+    }
+    const T *at = static_cast<const T *>(p.logits) + row * p.ld;
+    for (int i = lane; i < p.n_tokens; i += 32) {
+        const int64_t to = row * p.n_tokens + i;
+        const int tok = p.tokens[to];
+        float lp = nan;
+        if (tok < 0 || tok >= p.n_cols)
+            atomicOr(p.status, TF_DEV_BAD_TOKEN);
+        else if (!bad)
+            lp = (Elem<T>::load(at + tok) - all.m) * p.scale - log_l;
+        p.token_logprobs[to] = lp;
+    }
+    if constexpr (TOP) {
+        if (lane < K) {
+            const uint64_t y = top[lane];
+            const int64_t to = row * K + lane;
+            p.top_ids[to] = (bad || y == 0) ? -1 : (int)~(uint32_t)y;
+            p.top_logprobs[to] =
+                bad ? nan : (y == 0 ? -INFINITY : (unkey32((uint32_t)(y >> 32)) - all.m) * p.scale - log_l);
+        }
+    }
+}
+
+// ---- CTA mode: a CTA a row, or a cluster of CL
+// Ranks the n distinct keys of `list` and puts the k largest, largest first,
+// into `top` (0 past the n-th): a warp a key, 32 of the others at a time.
+template <int NT>
+__device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uint64_t *top) {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < n; i += NT / 32) {
+        const uint64_t mine = list[i];
+        int rank = 0;
+        for (int j = 0; j < n; j += 32)
+            rank += __popc(__ballot_sync(0xffffffffu, j + lane < n && list[min(j + lane, n - 1)] > mine));
+        if (lane == 0 && rank < k) top[rank] = mine;
+    }
+    for (int i = n + threadIdx.x; i < k; i += NT) top[i] = 0ull;
+}
+
 template <typename T, bool TOP, int NT>
 __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel(const LogprobParams p) {
     using E = Elem<T>;
@@ -196,100 +512,32 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
     const float c = p.scale * kLog2e;
     const int K = p.top_k;
 
-    // this CTA's vectors [v0, v1) of the row; vector v holds columns v * EPV - mis ...
     const int64_t row = blockIdx.x / (unsigned)CL;
-    const T *const at = static_cast<const T *>(p.logits) + row * p.ld;
-    const int mis = (int)((reinterpret_cast<uintptr_t>(at) & 15u) / sizeof(T));
-    const int nv = (mis + p.n_cols + EPV - 1) / EPV, per = (nv + CL - 1) / CL;
-    const int v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
-    const int n_chunks = max(1, (v1 - v0 + kLpBatch * NT - 1) / (kLpBatch * NT));
-    // columns outside the row (and vectors past this CTA's) are masked
-    auto load_vec = [&](int v, uint32_t (&x)[4]) {
-        const int c0 = v * EPV - mis;
-        if (v < v1 && c0 >= 0 && c0 + EPV <= p.n_cols) {
-            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at + c0));
-            x[0] = y.x;
-            x[1] = y.y;
-            x[2] = y.z;
-            x[3] = y.w;
-        } else {
-            x[0] = x[1] = x[2] = x[3] = EPV == 4 ? 0xff800000u : 0xff80ff80u;
-            if (v < v1) {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e)
-                    if (c0 + e >= 0 && c0 + e < p.n_cols) E::put(x, e, E::load(at + c0 + e));
-            }
-        }
-    };
-    auto load = [&](int chunk, uint32_t (&x)[kLpBatch][4]) {
-        const int v = v0 + chunk * kLpBatch * NT;  // the chunk's first vector
-        if (v * EPV - mis >= 0 && v + kLpBatch * NT <= v1 && (v + kLpBatch * NT) * EPV - mis <= p.n_cols) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(at + (v * EPV - mis)) + tid;  // all inside the row
-#pragma unroll
-            for (int k = 0; k < kLpBatch; ++k) {
-                const uint4 y = __ldg(src + k * NT);
-                x[k][0] = y.x;
-                x[k][1] = y.y;
-                x[k][2] = y.z;
-                x[k][3] = y.w;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kLpBatch; ++k) load_vec(v + k * NT + tid, x[k]);
-        }
-    };
-
+    const RowView<T> w(p, row, rank, CL);
+    const int n_chunks = w.chunks(NT);
     Stat st{-INFINITY, 0.f, 0.f};
-    auto fold = [&](const uint32_t (&x)[kLpBatch][4]) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(x[k]));
-        if (mx > st.m) st.to(mx, c);
-        if (st.m > kLpCareful || st.m == -INFINITY) {
-            // (all masked so far: the reference is 0, every term 0 or a NaN)
-            const float ref = st.m == -INFINITY ? 0.f : -st.m;
-            const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
-            uint64_t l2 = pk2(st.l, 0.f), t2 = pk2(st.t, 0.f);
-#pragma unroll
-            for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                for (int e = 0; e < EPV / 2; ++e) {
-                    const uint64_t d2 = add2(E::pair(x[k], e), ref2);
-                    float y0, y1;
-                    unpk2(mul2(d2, c2), y0, y1);
-                    const uint64_t q2 = pk2(ex2(y0), ex2(y1));
-                    l2 = add2(l2, q2);
-                    t2 = fma2(q2, d2, t2);
-                }
-            float a, b;
-            unpk2(l2, a, b);
-            st.l = a + b;
-            unpk2(t2, a, b);
-            st.t = a + b;
-        } else {
-#pragma unroll
-            for (int k = 0; k < kLpBatch; ++k)
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    const float d = max_nan(E::get(x[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
-                    const float q = ex2(d * c);
-                    st.l += q;
-                    st.t = fmaf(q, d, st.t);
-                }
-        }
-    };
     uint32_t cur[kLpBatch][4];
-    load(0, cur);
+    w.chunk(0, tid, NT, cur);
     if constexpr (TOP) {
         if (tid == 0) s_n = 0;
     }
+    // the thread's chunk with its largest value, the largest of its other chunks
+    int best_ch = 0;
+    float second = -INFINITY;
+    auto step = [&](const uint32_t (&x)[kLpBatch][4], int ch) {
+        const float before = st.m, mx = fold<T>(st, x, c);
+        if constexpr (TOP) {
+            second = fmaxf(second, fminf(before, mx));
+            best_ch = mx > before ? ch : best_ch;
+        }
+    };
     for (int ch = 0; ch < n_chunks; ch += 2) {
         uint32_t nxt[kLpBatch][4];
-        if (ch + 1 < n_chunks) load(ch + 1, nxt);
-        fold(cur);
+        if (ch + 1 < n_chunks) w.chunk(ch + 1, tid, NT, nxt);
+        step(cur, ch);
         if (ch + 1 < n_chunks) {
-            if (ch + 2 < n_chunks) load(ch + 2, cur);
-            fold(nxt);
+            if (ch + 2 < n_chunks) w.chunk(ch + 2, tid, NT, cur);
+            step(nxt, ch + 1);
         }
     }
 
@@ -334,26 +582,41 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
         auto each = [&](const uint32_t (&x)[4], int v, float want, auto &&f) {
             const float most = E::most(x);
             if (!(most >= want) || most == -INFINITY) return;
-            const int c0 = v * EPV - mis;
+            const int c0 = v * EPV - w.mis;
 #pragma unroll
             for (int e = 0; e < EPV; ++e) {
                 const float y = E::get(x, e);
                 if (y >= want && y > -INFINITY) f(y, c0 + e);
             }
         };
-        // a warp looks through one such thread's vectors together, a vector a lane
-        for (uint32_t hits = __ballot_sync(0xffffffffu, mine >= tau && mine > -INFINITY); hits; hits &= hits - 1) {
-            const int first = v0 + warp * 32 + __ffs(hits) - 1;
-            for (int v = first + lane * NT; v - lane * NT < v1; v += 2 * 32 * NT) {
+        auto push = [&](float y, int col) {
+            const int i = atomicAdd(&s_n, 1);
+            if (i < kLpList) s_list[i] = key64(y, col);
+        };
+        const bool hit = mine >= tau && mine > -INFINITY;
+        // most have one chunk that reaches it: its vectors, eight threads' at a time
+        uint32_t one = __ballot_sync(0xffffffffu, hit && second < tau);
+        while (one) {
+            int from = -1;  // lane 4 i + k: vector k of the i-th such thread
+            for (int i = 0; i < 32 / kLpBatch && one; ++i, one &= one - 1)
+                if (lane / kLpBatch == i) from = __ffs(one) - 1;
+            const int ch = __shfl_sync(0xffffffffu, best_ch, from < 0 ? 0 : from);
+            if (from >= 0) {
+                const int v = w.v0 + (ch * kLpBatch + lane % kLpBatch) * NT + warp * 32 + from;
+                uint32_t x[4];
+                w.vec(v, x);
+                each(x, v, tau, push);
+            }
+        }
+        // the others' vectors, a vector a lane
+        for (uint32_t all = __ballot_sync(0xffffffffu, hit && !(second < tau)); all; all &= all - 1) {
+            const int first = w.v0 + warp * 32 + __ffs(all) - 1;
+            for (int v = first + lane * NT; v - lane * NT < w.v1; v += 2 * 32 * NT) {
                 uint32_t x[2][4];
-                load_vec(v, x[0]);
-                load_vec(v + 32 * NT, x[1]);
+                w.vec(v, x[0]);
+                w.vec(v + 32 * NT, x[1]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    each(x[k], v + k * 32 * NT, tau, [&](float y, int col) {
-                        const int i = atomicAdd(&s_n, 1);
-                        if (i < kLpList) s_list[i] = key64(y, col);
-                    });
+                for (int k = 0; k < 2; ++k) each(x[k], v + k * 32 * NT, tau, push);
             }
         }
         __syncthreads();
@@ -362,10 +625,10 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
             uint64_t best = 0;
             auto look = [&](uint64_t below) {
                 best = 0;
-                for (int v = v0 + tid; v < v1; v += kLpBatch * NT) {
+                for (int v = w.v0 + tid; v < w.v1; v += kLpBatch * NT) {
                     uint32_t x[kLpBatch][4];
 #pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k) load_vec(v + k * NT, x[k]);
+                    for (int k = 0; k < kLpBatch; ++k) w.vec(v + k * NT, x[k]);
 #pragma unroll
                     for (int k = 0; k < kLpBatch; ++k)
                         each(x[k], v + k * NT, -INFINITY, [&](float y, int col) {
@@ -450,37 +713,39 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
     if (warp != 0) return;
     all.m = __shfl_sync(0xffffffffu, all.m, 0);
     all.l = __shfl_sync(0xffffffffu, all.l, 0);
-    const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
-    const float nan = __int_as_float(0x7fc00000);
-    const float log_l = logf(all.l);
-    if (lane == 0) {
-        if (p.entropy) p.entropy[row] = bad ? nan : log_l - p.scale * (all.t / all.l);
-        if (p.lse) p.lse[row] = bad ? nan : fmaf(p.scale, all.m, log_l);
-        p.flags[row] = bad ? 1 : 0;
-    }
-    for (int i = lane; i < p.n_tokens; i += 32) {
-        const int64_t to = row * p.n_tokens + i;
-        const int tok = p.tokens[to];
-        float lp = nan;
-        if (tok < 0 || tok >= p.n_cols)
-            atomicOr(p.status, TF_DEV_BAD_TOKEN);
-        else if (!bad)
-            lp = (E::load(at + tok) - all.m) * p.scale - log_l;
-        p.token_logprobs[to] = lp;
-    }
-    if constexpr (TOP) {
-        if (lane < K) {
-            const uint64_t y = s_top[lane];
-            const int64_t to = row * K + lane;
-            p.top_ids[to] = (bad || y == 0) ? -1 : (int)~(uint32_t)y;
-            p.top_logprobs[to] =
-                bad ? nan : (y == 0 ? -INFINITY : (unkey32((uint32_t)(y >> 32)) - all.m) * p.scale - log_l);
+    write_row<T, TOP>(p, row, all, s_top);
+}
+
+// ---- warp mode: a warp a row
+constexpr int kLpWarpRows = 8;   // warps a CTA
+constexpr int kLpWarpList = 256;
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const LogprobParams p) {
+    __shared__ FinishBuf<32, TOP ? kLpWarpList : 1> s_fin[kLpWarpRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const float c = p.scale * kLog2e;
+    const int64_t row = (int64_t)blockIdx.x * kLpWarpRows + warp;
+    if (row >= p.n_rows) return;
+    const RowView<T> w(p, row, 0, 1);
+    Stat s[1] = {{-INFINITY, 0.f, 0.f}};
+    uint32_t a[kLpBatch][4], b[kLpBatch][4];
+    const int n_chunks = w.chunks(32);
+    w.chunk(0, lane, 32, a);
+    for (int ch = 0; ch < n_chunks; ch += 2) {
+        if (ch + 1 < n_chunks) w.chunk(ch + 1, lane, 32, b);
+        fold<T>(s[0], a, c);
+        if (ch + 1 < n_chunks) {
+            if (ch + 2 < n_chunks) w.chunk(ch + 2, lane, 32, a);
+            fold<T>(s[0], b, c);
         }
     }
+    const Stat all = finish<T, TOP>(w, s, s_fin[warp], p.top_k, c);
+    write_row<T, TOP>(p, row, all, s_fin[warp].top);
 }
 
 template <typename T, bool TOP, int NT>
-cudaError_t launch_logprob_t(const LogprobParams &p, int cl, cudaStream_t st) {
+cudaError_t launch_cta(const LogprobParams &p, int cl, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)p.n_rows * (unsigned)cl);
     cfg.blockDim = dim3(NT);
@@ -499,15 +764,20 @@ template <typename T, bool TOP>
 cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     const int sms = device_sms();
     const int chunk = Elem<T>::kPer * kLpBatch;  // columns a thread holds
-    // short rows: one chunk of 64 threads or two, sixteen rows an SM at once
-    if (p.n_cols <= 2 * 64 * chunk && p.n_rows > sms) return launch_logprob_t<T, TOP, 64>(p, 1, st);
-    // many rows: four CTAs an SM
-    if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_logprob_t<T, TOP, 256>(p, 1, st);
-    if (p.n_rows > sms) return launch_logprob_t<T, TOP, 512>(p, 1, st);
+    // short rows (up to four chunks of a warp): a warp a row
+    if (p.n_cols <= 4 * 32 * chunk && p.n_rows > 4 * sms) {
+        const int64_t grid = ((int64_t)p.n_rows + kLpWarpRows - 1) / kLpWarpRows;
+        logprob_warp_kernel<T, TOP><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
+        return cudaGetLastError();
+    }
+    // many rows: eight or four CTAs an SM
+    if (p.n_rows > 4 * sms && p.n_cols <= 2 * 1024 * chunk) return launch_cta<T, TOP, 128>(p, 1, st);
+    if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_cta<T, TOP, 256>(p, 1, st);
+    if (p.n_rows > sms) return launch_cta<T, TOP, 512>(p, 1, st);
     // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads
     int cl = 1;
     while (cl < kLpMaxCluster && p.n_rows * 2 * cl <= sms && cl * 1024 * chunk < p.n_cols) cl *= 2;
-    return launch_logprob_t<T, TOP, 1024>(p, cl, st);
+    return launch_cta<T, TOP, 1024>(p, cl, st);
 }
 
 }  // namespace
