@@ -48,10 +48,8 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         ws = (int64_t)max_rows * group <= 8 && decode_q8_supported(c.head_dim, n_segs) &&
              (split == 0 || split % std::min(c.page_size, 64) == 0);
         if (split == 0)
-            split = ws ? choose_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 3, 256,
-                                      n_splits_max)
-                       : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), 256,
-                                        n_splits_max);
+            split = one_wave_split(segs_host, n_segs, c.n_kv_heads, ws ? 1 << 30 : std::max(1, 128 / group),
+                                   ws ? decode_q8_grid(c.head_dim, c.kv_type) : device_sms(), 256, n_splits_max);
         // as many partial slots as the longest stream takes: the merge's reads stay close together
         int longest = 1;
         for (int s = 0; s < n_segs; ++s)

@@ -28,6 +28,7 @@
 //  - The references move only when a term would pass 2^8 above them, so a tile
 //    takes one vote instead of two butterfly maxima.
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -314,9 +315,12 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
             float o[D / 16][4];
 #pragma unroll
             for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
-            // m: reference of the scores; r: reference of score + value scale (both in base 2)
-            float m0 = -INFINITY, m1 = -INFINITY, r0 = -INFINITY, r1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-            uint32_t e0 = 0, e1 = 0, tb0 = 0, tb1 = 0, badp = 0;
+            // m: reference of the scores; r: reference of score + value scale (both in
+            // base 2; -FLT_MAX before the first key, so nothing is special-cased)
+            float m0 = -FLT_MAX, m1 = -FLT_MAX, r0 = -FLT_MAX, r1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
+            float n0 = INFINITY, n1 = INFINITY;  // the smallest scores (-inf: an overflow, flagged)
+            uint32_t e0 = 0, e1 = 0, tb0 = 0, tb1 = 0, badp = 0, vtop = 0;
+            const uint64_t f2 = pk2(fa, fb_);
             const int kb = warp * 16;
             bool aborted = !q_ok;
 
@@ -357,36 +361,68 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                         mma_f16(s5, a[0], a[1], a[2], a[3], qb[c + 1][0], qb[c + 1][1]);
                     }
                     // ---- scores and value exponents of keys kb + gq and kb + gq + 8
-                    const unsigned char *sc = base_ptr + st * C::kStageBytes + C::kOffScale;
-                    const int ra = kb + gq, rb = ra + 8, ka = j0 + ra, kbk = j0 + rb;
-                    const uint32_t eka = sc[ra], ekb = sc[rb], eva = sc[C::TK + ra], evb = sc[C::TK + rb];
-                    const float ska = e8m0_f32(eka), skb = e8m0_f32(ekb);
-                    const bool va0 = ra < rows && ka < lim_a, va1 = ra < rows && ka < lim_b;
-                    const bool vb0 = rb < rows && kbk < lim_a, vb1 = rb < rows && kbk < lim_b;
-                    float x0 = (s4[0] + s5[0]) * (ska * fa), x1 = (s4[1] + s5[1]) * (ska * fb_);
-                    float x2 = (s4[2] + s5[2]) * (skb * fa), x3 = (s4[3] + s5[3]) * (skb * fb_);
-                    e0 = max(e0, max(va0 ? exp_bits(x0) : 0u, vb0 ? exp_bits(x2) : 0u));
-                    e1 = max(e1, max(va1 ? exp_bits(x1) : 0u, vb1 ? exp_bits(x3) : 0u));
-                    // a value row marked nonfinite flags the queries that see it and weighs nothing
-                    if (eva == kE8Nan) {
-                        tb0 |= va0;
-                        tb1 |= va1;
+                    const unsigned char *sc = base_ptr + st * C::kStageBytes + C::kOffScale + kb + gq;
+                    const uint32_t eka = sc[0], ekb = sc[8], eva = sc[C::TK], evb = sc[C::TK + 8];
+                    // (a marked row's scale is inf here: inf * 0, its codes' sum, is NaN)
+                    const float ska = __uint_as_float(eka << 23), skb = __uint_as_float(ekb << 23);
+                    uint64_t xa = mul2(add2(pk2(s4[0], s4[1]), pk2(s5[0], s5[1])), mul2(pk2(ska, ska), f2));
+                    uint64_t xb = mul2(add2(pk2(s4[2], s4[3]), pk2(s5[2], s5[3])), mul2(pk2(skb, skb), f2));
+                    float fva = (float)((int)eva - kE8Bias), fvb = (float)((int)evb - kE8Bias);
+                    if (kb + 16 <= rows && j0 + kb + 16 <= it.full_hi) {
+                        // every query sees these keys: NaN and +inf reach l, -inf is caught
+                        // here, a marked value row at the end
+                        float x0, x1, x2, x3;
+                        unpk2(xa, x0, x1);
+                        unpk2(xb, x2, x3);
+                        n0 = min3(n0, x0, x2);
+                        n1 = min3(n1, x1, x3);
+                        vtop = max(vtop, max(eva, evb));
+                    } else {
+                        const int ra = kb + gq, rb = ra + 8, ka = j0 + ra, kbk = j0 + rb;
+                        const bool va0 = ra < rows && ka < lim_a, va1 = ra < rows && ka < lim_b;
+                        const bool vb0 = rb < rows && kbk < lim_a, vb1 = rb < rows && kbk < lim_b;
+                        float x0, x1, x2, x3;
+                        unpk2(xa, x0, x1);
+                        unpk2(xb, x2, x3);
+                        e0 = max(e0, max(va0 ? exp_bits(x0) : 0u, vb0 ? exp_bits(x2) : 0u));
+                        e1 = max(e1, max(va1 ? exp_bits(x1) : 0u, vb1 ? exp_bits(x3) : 0u));
+                        // a value row marked nonfinite flags the queries that see it and weighs nothing
+                        if (eva == kE8Nan) {
+                            tb0 |= va0;
+                            tb1 |= va1;
+                            fva = -INFINITY;
+                        }
+                        if (evb == kE8Nan) {
+                            tb0 |= vb0;
+                            tb1 |= vb1;
+                            fvb = -INFINITY;
+                        }
+                        xa = pk2(va0 ? x0 : -INFINITY, va1 ? x1 : -INFINITY);
+                        xb = pk2(vb0 ? x2 : -INFINITY, vb1 ? x3 : -INFINITY);
                     }
-                    if (evb == kE8Nan) {
-                        tb0 |= vb0;
-                        tb1 |= vb1;
-                    }
-                    x0 = va0 ? x0 : -INFINITY;
-                    x1 = va1 ? x1 : -INFINITY;
-                    x2 = vb0 ? x2 : -INFINITY;
-                    x3 = vb1 ? x3 : -INFINITY;
-                    const float fva = eva == kE8Nan ? -INFINITY : (float)((int)eva - kE8Bias);
-                    const float fvb = evb == kE8Nan ? -INFINITY : (float)((int)evb - kE8Bias);
-                    const float y0 = x0 + fva, y1 = x1 + fva, y2 = x2 + fvb, y3 = x3 + fvb;
-                    // ---- the references move when a term would pass 2^8 above them
-                    const bool up = fmaxf(x0, x2) > m0 + 8.f || fmaxf(x1, x3) > m1 + 8.f ||
-                                    fmaxf(y0, y2) > r0 + 8.f || fmaxf(y1, y3) > r1 + 8.f;
-                    if (__any_sync(0xffffffffu, up)) {
+                    const uint64_t ya = add2(xa, pk2(fva, fva)), yb = add2(xb, pk2(fvb, fvb));
+                    // ---- exponents over the references, which move when one would pass 2^8
+                    uint64_t da, db, ga, gb;
+                    float d0, d1, d2, d3, g0, g1, g2, g3;
+                    auto over = [&]() {
+                        const uint64_t nm = pk2(-m0, -m1), nr = pk2(-r0, -r1);
+                        da = add2(xa, nm);
+                        db = add2(xb, nm);
+                        ga = add2(ya, nr);
+                        gb = add2(yb, nr);
+                        unpk2(da, d0, d1);
+                        unpk2(db, d2, d3);
+                        unpk2(ga, g0, g1);
+                        unpk2(gb, g2, g3);
+                    };
+                    over();
+                    const float most = max3(max3(d0, d1, d2), max3(d3, g0, g1), fmaxf(g2, g3));
+                    if (__any_sync(0xffffffffu, most > 8.f)) {
+                        float x0, x1, x2, x3, y0, y1, y2, y3;
+                        unpk2(xa, x0, x1);
+                        unpk2(xb, x2, x3);
+                        unpk2(ya, y0, y1);
+                        unpk2(yb, y2, y3);
                         float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3), b0 = fmaxf(y0, y2), b1 = fmaxf(y1, y3);
 #pragma unroll
                         for (int s = 4; s < 32; s <<= 1) {
@@ -395,29 +431,26 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                             b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, s));
                             b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, s));
                         }
-                        // (a reference at -inf has nothing to rescale: factor 0 of 0)
-                        auto move = [](float &ref, float to) -> float {
-                            const float n = fmaxf(ref, to);
-                            const float f = n == -INFINITY ? 1.f : ex2(ref - n);
+                        auto move = [](float &ref, float to) -> float {  // the factor of what was summed so far
+                            const float n = fmaxf(ref, to), f = ex2(ref - n);
                             ref = n;
                             return f;
                         };
                         l0 *= move(m0, a0);
                         l1 *= move(m1, a1);
-                        const float g0 = move(r0, b0), g1 = move(r1, b1);
+                        const float h0 = move(r0, b0), h1 = move(r1, b1);
 #pragma unroll
                         for (int u = 0; u < D / 16; ++u) {
-                            o[u][0] *= g0;
-                            o[u][1] *= g1;
-                            o[u][2] *= g0;
-                            o[u][3] *= g1;
+                            o[u][0] *= h0;
+                            o[u][1] *= h1;
+                            o[u][2] *= h0;
+                            o[u][3] *= h1;
                         }
+                        over();
                     }
-                    const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
-                    const float ru0 = r0 == -INFINITY ? 0.f : r0, ru1 = r1 == -INFINITY ? 0.f : r1;
-                    l0 += ex2(x0 - mu0) + ex2(x2 - mu0);
-                    l1 += ex2(x1 - mu1) + ex2(x3 - mu1);
-                    const float w0 = ex2(y0 - ru0), w1 = ex2(y1 - ru1), w2 = ex2(y2 - ru0), w3 = ex2(y3 - ru1);
+                    l0 += ex2(d0) + ex2(d2);
+                    l1 += ex2(d1) + ex2(d3);
+                    const float w0 = ex2(g0), w1 = ex2(g1), w2 = ex2(g2), w3 = ex2(g3);
                     // W^T fragments: (keys 2t4.., query gq) from (key gq.., queries 2t4..), hi and lo
                     const uint32_t h01 = pack_f16x2(w0, w1), h23 = pack_f16x2(w2, w3);
                     const float2 f01 = f16x2_to_f32(h01), f23 = f16x2_to_f32(h23);
@@ -455,6 +488,8 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
             }
 
             // ---- combine the four warps (tree through shared memory) and write
+            tb0 |= (n0 == -INFINITY || vtop == kE8Nan) ? 1u : 0u;
+            tb1 |= (n1 == -INFINITY || vtop == kE8Nan) ? 1u : 0u;
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, s);
@@ -491,9 +526,9 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                 f1 |= comb_f[slot][qb_];
                 // weights of this warp's and the slot's sums at the larger reference
                 auto pair = [](float &ref, float other, float &mine, float &theirs) {
-                    const float n = fmaxf(ref, other), u = n == -INFINITY ? 0.f : n;
-                    mine = ex2(ref - u);
-                    theirs = ex2(other - u);
+                    const float n = fmaxf(ref, other);
+                    mine = ex2(ref - n);
+                    theirs = ex2(other - n);
                     ref = n;
                 };
                 float a, b;
@@ -526,8 +561,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                 take(0);
                 // o in units of 2^m, as the merge wants it (in two steps: 2^(r - m)
                 // itself may be past the floats where o is small)
-                const float g0 = r0 == -INFINITY ? 0.f : ex2(0.5f * (r0 - (m0 == -INFINITY ? 0.f : m0)));
-                const float g1 = r1 == -INFINITY ? 0.f : ex2(0.5f * (r1 - (m1 == -INFINITY ? 0.f : m1)));
+                const float g0 = ex2(0.5f * (r0 - m0)), g1 = ex2(0.5f * (r1 - m1));
                 bool nf0 = !isfinite(l0), nf1 = !isfinite(l1);
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u) {
@@ -555,7 +589,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                     for (int u = 0; u < D / 16; ++u)
                         *reinterpret_cast<float2 *>(dst + 16 * u) = make_float2(o[u][c], o[u][c + 2]);
                     if (gq == 0) {
-                        p.part_m[at] = m == -INFINITY ? -INFINITY : m * kLn2;
+                        p.part_m[at] = m == -FLT_MAX ? -INFINITY : m * kLn2;
                         p.part_l[at] = l;
                         p.part_flag[at] = (uint8_t)(f ? 1 : 0);
                     }

@@ -10,9 +10,13 @@
 // One warp owns a (row, head) and 128 of its columns (float4 a lane; two warps
 // at head dim 256), and loads up to eight partials' rows in one round: the
 // kernel is a few microseconds of latency (its data, written just before, sits
-// in L2), so what counts is how few round trips a warp makes.  It launches as a
-// programmatic dependent of the partial kernel and reads the tables, which that
-// kernel never writes, before it waits for the partials.
+// in L2), so what counts is how few round trips a warp makes.  Where a row may
+// have more than two rounds of partials, a block of eight warps shares a (row,
+// head), each warp (pair) every fourth or eighth round, and joins them in shared
+// memory (one stream of 32,000 keys in 63 splits: see the log of the figures in
+// api_q8.cu).  It launches as a programmatic dependent of the partial kernel and
+// reads the tables, which that kernel never writes, before it waits for the
+// partials.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -38,13 +42,15 @@ __device__ __forceinline__ int seg_parts(const tf_seg &e, const PartSet &s, cons
     return n <= s.n_splits ? (int)n : 0;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) merge_segs_kernel(const MergeSegsParams p) {
-    constexpr int SL = D > 128 ? D / 128 : 1;  // warps a (row, head)
+template <int D, bool BF16, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 256 : 128) merge_segs_kernel(const MergeSegsParams p) {
+    constexpr int SL = D > 128 ? D / 128 : 1;  // warps across a (row, head)'s columns
     constexpr int DW = D / SL;                 // columns a warp
     constexpr int CH = 8;                      // partials in flight
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sl = warp % SL;
-    const int64_t u = (int64_t)blockIdx.x * (4 / SL) + warp / SL;  // row of the stream x head
+    constexpr int WAYS = WIDE ? 8 / SL : 1;    // warps along its partials
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sl = warp % SL, way = WIDE ? warp / SL : 0;
+    // row of the stream x head
+    const int64_t u = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (4 / SL) + warp / SL;
     const tf_seg e = p.segs[blockIdx.y];
     const int i = (int)(u / p.hq), h = (int)(u - (int64_t)i * p.hq);
     if (i >= e.n_rows || e.q_row < 0 || (int64_t)e.q_row + i >= p.n_rows_total) {  // all warps of a unit leave
@@ -76,7 +82,7 @@ __global__ void __launch_bounds__(128) merge_segs_kernel(const MergeSegsParams p
     float M = -INFINITY, L = 0.f;
     uint32_t f = bad ? 1u : 0u;
     const int total = bad ? 0 : n_pre + n_own;
-    for (int c0 = 0; c0 < total; c0 += CH) {
+    for (int c0 = way * CH; c0 < total; c0 += WAYS * CH) {
         float4 v[CH];
         float mc = -INFINITY, lc = 0.f;
 #pragma unroll
@@ -133,6 +139,37 @@ __global__ void __launch_bounds__(128) merge_segs_kernel(const MergeSegsParams p
         L += __shfl_xor_sync(0xffffffffu, L, x);
         f |= __shfl_xor_sync(0xffffffffu, f, x);
     }
+    if constexpr (WIDE) {
+        // the ways meet in the first one's warps
+        __shared__ float4 s_acc[8][32];
+        __shared__ float s_m[8], s_l[8];
+        __shared__ uint32_t s_f[8];
+        s_acc[warp][lane] = acc;
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_l[warp] = L;
+            s_f[warp] = f;
+        }
+        __syncthreads();
+        if (way != 0) return;
+        float Mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < WAYS; ++k) Mx = fmaxf(Mx, s_m[k * SL + sl]);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < WAYS; ++k) {
+            const int x = k * SL + sl;
+            const float w = s_m[x] == -INFINITY ? 0.f : ex2((s_m[x] - Mx) * kLog2e);
+            const float4 a = s_acc[x][lane];
+            acc.x += w * a.x;
+            acc.y += w * a.y;
+            acc.z += w * a.z;
+            acc.w += w * a.w;
+            L += w * s_l[x];
+            f |= s_f[x];
+        }
+    }
     acc.x /= L;
     acc.y /= L;
     acc.z /= L;
@@ -143,9 +180,9 @@ __global__ void __launch_bounds__(128) merge_segs_kernel(const MergeSegsParams p
     if constexpr (SL > 1) {  // the other half's columns
         __shared__ uint32_t s_nf[4];
         if (lane == 0) s_nf[warp] = nfw;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / SL), "r"(32 * SL) : "memory");
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (WIDE ? 0 : warp / SL)), "r"(32 * SL) : "memory");
 #pragma unroll
-        for (int k = 0; k < SL; ++k) nfw |= s_nf[(warp / SL) * SL + k];
+        for (int k = 0; k < SL; ++k) nfw |= s_nf[(WIDE ? 0 : warp / SL) * SL + k];
     }
     f |= nfw;
     if (f) {
@@ -164,19 +201,26 @@ __global__ void __launch_bounds__(128) merge_segs_kernel(const MergeSegsParams p
     if (lane == 0 && sl == 0) p.flags[unit] = (uint8_t)(f ? 1 : 0);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIDE>
 cudaError_t launch_t(const MergeSegsParams &p, cudaStream_t st) {
-    constexpr int units = D > 128 ? 4 / (D / 128) : 4;
+    constexpr int units = WIDE ? 1 : (D > 128 ? 4 / (D / 128) : 4);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(((int64_t)p.max_rows * p.hq + units - 1) / units), (unsigned)p.n_segs);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(WIDE ? 256 : 128);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_segs_kernel<D, BF16>, p);
+    return cudaLaunchKernelEx(&cfg, merge_segs_kernel<D, BF16, WIDE>, p);
+}
+
+template <int D>
+cudaError_t launch_d(const MergeSegsParams &p, cudaStream_t st) {
+    const bool wide = p.own.n_splits + (p.n_prefixes > 0 ? p.prefix.n_splits : 0) > 16;
+    if (p.out_bf16) return wide ? launch_t<D, true, true>(p, st) : launch_t<D, true, false>(p, st);
+    return wide ? launch_t<D, false, true>(p, st) : launch_t<D, false, false>(p, st);
 }
 
 }  // namespace
@@ -184,9 +228,9 @@ cudaError_t launch_t(const MergeSegsParams &p, cudaStream_t st) {
 cudaError_t launch_merge_segs(const MergeSegsParams &p, int head_dim, cudaStream_t st) {
     if (p.n_segs == 0 || p.max_rows == 0) return cudaSuccess;
     switch (head_dim) {
-        case 64: return p.out_bf16 ? launch_t<64, true>(p, st) : launch_t<64, false>(p, st);
-        case 128: return p.out_bf16 ? launch_t<128, true>(p, st) : launch_t<128, false>(p, st);
-        case 256: return p.out_bf16 ? launch_t<256, true>(p, st) : launch_t<256, false>(p, st);
+        case 64: return launch_d<64>(p, st);
+        case 128: return launch_d<128>(p, st);
+        case 256: return launch_d<256>(p, st);
         default: return cudaErrorInvalidValue;
     }
 }
