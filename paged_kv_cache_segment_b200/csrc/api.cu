@@ -90,7 +90,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
                                const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host,
                                const int32_t *page_table_host, float scale, int32_t split_keys,
                                int32_t n_splits_max, float *part_o, float *part_m, float *part_l,
-                               uint8_t *part_flag, uint32_t *status, tf_stream_t stream) {
+                               uint8_t *part_flag, uint32_t *status, tf_stream_t stream, bool beside) {
     if (n_rows_total < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_pages < 0 || page_table_len < 0 || n_segs < 0 ||
         split_keys < 0 || n_splits_max <= 0 || !std::isfinite(scale))
         return TF_ERR_ARG;
@@ -144,6 +144,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
         w.split_keys = split_keys;
         w.n_splits_max = n_splits_max;
         w.full = full ? 1 : 0;
+        w.beside = beside ? 1 : 0;
         w.part_o = part_o;
         w.part_m = part_m;
         w.part_l = part_l;
@@ -175,6 +176,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
             t.n_splits_max = n_splits_max;
             t.n_qt = (int)n_qt;
             t.full = full ? 1 : 0;
+            t.beside = beside ? 1 : 0;
             t.part_o = part_o;
             t.part_m = part_m;
             t.part_l = part_l;

@@ -99,25 +99,13 @@ inline int device_sms() {
     return n;
 }
 
-// A split size for a host table: enough items (streams x kv-heads x splits) to
-// give each of `slots` resident CTAs about `per_slot` of them, in whole 64-key
-// tiles, at least `least` keys, at most n_splits_max splits a stream.
-inline int choose_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t slots, int per_slot, int least,
-                        int n_splits_max) {
-    int64_t keys = 0, longest = 1;
-    for (int s = 0; s < n_segs; ++s) {
-        if (sh[s].n_rows == 0) continue;
-        keys += sh[s].n_keys;
-        if (sh[s].n_keys > longest) longest = sh[s].n_keys;
-    }
-    int64_t len = keys * n_kv_heads / (slots * per_slot);
-    if (len < least) len = least;
-    const int64_t fit = (longest + n_splits_max - 1) / n_splits_max;
-    if (len < fit) len = fit;
-    len = (len + 63) / 64 * 64;
-    return len > 0x40000000 ? 0x40000000 : (int)len;
+// The most keys of a stream with rows (at least 1).
+inline int longest_keys(const tf_seg *sh, int n_segs) {
+    int n = 1;
+    for (int s = 0; s < n_segs; ++s)
+        if (sh[s].n_rows > 0 && sh[s].n_keys > n) n = sh[s].n_keys;
+    return n;
 }
-
 
 // A split size for kernels of one CTA an SM with a fixed cost a CTA (start-up
 // and epilogue, some eight 64-key tiles' worth): the smallest whole number of
@@ -126,9 +114,7 @@ inline int choose_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t sl
 // where even that is more.
 inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows_per_tile, int n_sms, int least,
                           int n_splits_max) {
-    int64_t longest = 1;
-    for (int s = 0; s < n_segs; ++s)
-        if (sh[s].n_rows > 0 && sh[s].n_keys > longest) longest = sh[s].n_keys;
+    const int64_t longest = longest_keys(sh, n_segs);
     auto ctas = [&](int64_t tiles) {
         int64_t n = 0;
         for (int s = 0; s < n_segs; ++s)
@@ -149,6 +135,25 @@ inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows
             lo = mid + 1;
     }
     return lo > (0x40000000 >> 6) ? 0x40000000 : (int)(lo * 64);
+}
+
+// A split size for the persistent decode kernels (`slots` CTAs taking items one
+// after another): one wave of items when that is balanced, that is when its
+// longest item is near the slots' average load; otherwise half of that load, up
+// to `most` keys, since the items of a CTA follow one another without a new start.
+inline int decode_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t slots, int most, int n_splits_max) {
+    const int one = one_wave_split(sh, n_segs, n_kv_heads, 1 << 30, (int)slots, 256, n_splits_max);
+    int64_t tiles = 0;
+    for (int s = 0; s < n_segs; ++s)
+        if (sh[s].n_rows > 0) tiles += ((int64_t)sh[s].n_keys + 63) / 64 * n_kv_heads;
+    const int64_t load = tiles / slots;  // tiles a CTA
+    if (one / 64 <= load + load / 3 + 2) return one;
+    const int64_t fit = ((int64_t)longest_keys(sh, n_segs) + n_splits_max - 1) / n_splits_max;
+    int64_t len = load / 2 * 64;
+    if (len > most) len = most;
+    if (len < 256) len = 256;
+    if (len < fit) len = (fit + 63) / 64 * 64;
+    return (int)len;
 }
 
 }  // namespace tfp

@@ -57,14 +57,13 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         const tf_status rc = check_segs_host(host, n, n_rows_total, page_table_len, page_size, n_pages,
                                              page_table_host, split_keys, splits, &rows, full);
         if (rc != TF_OK || rows == 0) return rc;
-        const int64_t q_tiles = full ? ((int64_t)rows * group + 127) / 128 : 1;
+        // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave; the decode kernel
+        // with the CTA an SM that it has beside the other
         if (split == 0)
-            split = choose_split(host, n, n_kv_heads, (int64_t)device_sms() * 2 / std::min<int64_t>(q_tiles, 64) + 1,
-                                 full ? 1 : 2, 256, splits);
-        int longest = 1;
-        for (int s = 0; s < n; ++s)
-            if (host[s].n_rows > 0) longest = std::max(longest, (int)host[s].n_keys);
-        splits = (int)(((int64_t)longest + split - 1) / split);
+            split = (int64_t)rows * group > 8
+                        ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), 128, splits)
+                        : decode_split(host, n, n_kv_heads, device_sms(), 1024, splits);
+        splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
         return TF_OK;
     };
     if (segs_host) {
@@ -101,7 +100,7 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
     const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                         n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
                                         page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
-                                        status, stream);
+                                        status, stream, n_prefixes > 0 && pre_rows > 0);
     if (rc != TF_OK) return rc;
 
     MergeSegsParams m{};

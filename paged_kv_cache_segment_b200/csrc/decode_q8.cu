@@ -55,10 +55,10 @@ struct Q8Cfg {
     // codes of K, codes of V, scale bytes of K and of V, to a multiple of 1,024
     static constexpr int kOffScale = 2 * kTileBytes;
     static constexpr int kStageBytes = kOffScale + 1024;
-    static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 3 : 6);
+    static constexpr int kStages = D == 256 ? 2 : (D == 128 ? 3 : 4);
     static constexpr int kNQ = 2;
     static constexpr int kPrefixMax = 256;
-    static constexpr int kMinBlocks = D == 256 ? 2 : 3;
+    static constexpr int kMinBlocks = D == 256 ? 2 : (D == 128 ? 3 : 4);
     static constexpr int kQBytes = kWsQ * D * 2;
     static constexpr int kCombStride = D + 4;  // floats a query row of the combine buffer
     static constexpr int kCombBytes = (NC / 2) * kWsQ * kCombStride * 4;
@@ -582,8 +582,25 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                 auto write = [&](int qq, float m, float l, uint32_t f, int c) {
                     if (qq >= q_item) return;
                     const int i = qq / p.group, hl = qq - i * p.group;
-                    const int64_t at =
-                        ((int64_t)(it.q_row + i) * p.hq + it.g * p.group + hl) * p.n_splits_max + it.c;
+                    const int64_t unit = (int64_t)(it.q_row + i) * p.hq + it.g * p.group + hl;
+                    if (p.out) {  // one split a stream: the row itself
+                        const bool bad = f || !(l > 0.f);
+                        const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+                        for (int u = 0; u < D / 16; ++u) {
+                            const float y = o[u][c] / l, z = o[u][c + 2] / l;
+                            const int64_t to = unit * D + 16 * u + 2 * gq;
+                            if (p.out_bf16)
+                                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + to) =
+                                    bad ? 0x7fc07fc0u : pack_bf16x2(y, z);
+                            else
+                                *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to) =
+                                    bad ? make_float2(nan, nan) : make_float2(y, z);
+                        }
+                        if (gq == 0) p.out_flags[unit] = (uint8_t)(bad ? 1 : 0);
+                        return;
+                    }
+                    const int64_t at = unit * p.n_splits_max + it.c;
                     float *dst = p.part_o + at * D + 2 * gq;
 #pragma unroll
                     for (int u = 0; u < D / 16; ++u)

@@ -8,10 +8,10 @@
 // and none needs a marker; only rows the table names are written.
 //
 // One warp owns a (row, head) and 128 of its columns (float4 a lane; two warps
-// at head dim 256), and loads up to eight partials' rows in one round: the
+// at head dim 256), and loads up to sixteen partials' rows in one round: the
 // kernel is a few microseconds of latency (its data, written just before, sits
 // in L2), so what counts is how few round trips a warp makes.  Where a row may
-// have more than two rounds of partials, a block of eight warps shares a (row,
+// have more partials than that, a block of eight warps shares a (row,
 // head), each warp (pair) every fourth or eighth round, and joins them in shared
 // memory (one stream of 32,000 keys in 63 splits: see the log of the figures in
 // api_q8.cu).  It launches as a programmatic dependent of the partial kernel and
@@ -46,7 +46,7 @@ template <int D, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 256 : 128) merge_segs_kernel(const MergeSegsParams p) {
     constexpr int SL = D > 128 ? D / 128 : 1;  // warps across a (row, head)'s columns
     constexpr int DW = D / SL;                 // columns a warp
-    constexpr int CH = 8;                      // partials in flight
+    constexpr int CH = WIDE ? 8 : 16;          // partials in flight
     constexpr int WAYS = WIDE ? 8 / SL : 1;    // warps along its partials
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sl = warp % SL, way = WIDE ? warp / SL : 0;
     // row of the stream x head

@@ -130,6 +130,10 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     volatile uint32_t *abort_flag = &s_abort;
     bool sent_row = false;  // this thread sent a staged row with a bulk copy
+    // beside another partial kernel (PromptTcParams::beside): this grid ends after that one
+    auto leave = [&]() {
+        if (PARTIAL && p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
 
     const int G = p.group, RT = kQM / p.group;  // rows a tile
     // partials: kv-head blockIdx.y; a prompt chunk: the launch order (block
@@ -155,11 +159,13 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
             const tf_tree_seg e = p.tsegs[blockIdx.z];
             if (!tree_seg_ok(e, p.n_rows_total, p.n_parents, p.ring_slots_total)) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
+                leave();
                 return;
             }
             const TreeSplits ts = tree_splits(e, p.split_keys);
             if (ts.n_sp > p.n_splits_max) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_SPLITS);
+                leave();
                 return;
             }
             q_row = e.q_row;
@@ -189,21 +195,27 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
                              pt_base < 0 || n_pg < 0 || (int64_t)pt_base + n_pg > p.pt_len;
             if (bad) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
+                leave();
                 return;
             }
             if ((int64_t)N > ((int64_t)n_pg << p.log2_page)) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_PAST_PAGES);
+                leave();
                 return;
             }
             n_sp = (N + p.split_keys - 1) / p.split_keys;
             if (n_sp > p.n_splits_max) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_SPLITS);
+                leave();
                 return;
             }
             key_lo = split * p.split_keys;
             key_hi_split = min(N, key_lo + p.split_keys);
         }
-        if (qt * RT >= T) return;
+        if (qt * RT >= T) {
+            leave();
+            return;
+        }
         if (split >= n_sp) {
             // a partial slot past the stream's count: an empty partial, o untouched
             for (int r = tid; r < min(RT, T - qt * RT) * G; r += kPTThreads) {
@@ -212,6 +224,7 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
                 p.part_l[at] = 0.f;
                 p.part_flag[at] = 0;
             }
+            leave();
             return;
         }
     } else {
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
             for (int d = 0; d < D; d += 4)
                 *reinterpret_cast<float4 *>(p.part_o + at * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        leave();
         return;
     }
 
@@ -743,6 +757,7 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
     // a thread that sent a staged row stays until the copy has read it from
     // shared memory; the grid's completion makes its writes visible
     if (sent_row) bulk_wait_read();
+    leave();
 }
 
 // ---------------------------------------------------------------------------
@@ -782,7 +797,7 @@ static cudaError_t launch_tc_t(const PromptTcParams &p, const void *k, const voi
         q.test_idle = 1;
         q.wait_ns = runout;
     }
-    if (PARTIAL) {
+    if (PARTIAL && !p.beside) {
         kern<<<grid, kPTThreads, C::kSmemBytes, st>>>(mk, mv, q);
         return cudaGetLastError();
     }
@@ -790,7 +805,8 @@ static cudaError_t launch_tc_t(const PromptTcParams &p, const void *k, const voi
     // library's previous chunk, or another of its attention calls) finishes:
     // it reads q, the pools and the page table, which none of them writes, so
     // the next chunk's tiles fill the SMs the previous chunk's last wave
-    // leaves idle.
+    // leaves idle.  (So may partials beside another partial kernel, whose outputs
+    // they neither read nor write.)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kPTThreads);

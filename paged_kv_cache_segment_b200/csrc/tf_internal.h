@@ -70,6 +70,10 @@ struct PromptTcParams {
     const tf_seg *segs;
     int pt_len, split_keys, n_splits_max, n_qt;
     int full;  // every row sees all of its stream's keys (no causal count)
+    // partials that run beside the partial kernel launched before this one: as
+    // its programmatic dependent, waiting for that grid only at the end, so that
+    // what depends on this launch depends on both
+    int beside;
     float *part_o, *part_m, *part_l;
     uint8_t *part_flag;
     uint32_t *status;
@@ -126,6 +130,14 @@ struct WsParams {
     int64_t ring_slots_total;
     // an 8-bit cache's scale bytes [pages][Hkv][P]
     const uint8_t *k_scale, *v_scale;
+    // run beside the partial kernel launched before this one (see
+    // PromptTcParams::beside), with a CTA an item: an SM holds one of these beside
+    // one of that kernel's and two once that is gone, so the hardware deals them out
+    int beside;
+    // an 8-bit cache, one split a stream: the final rows instead of partials
+    void *out;
+    int out_bf16;
+    uint8_t *out_flags;
     float scale_log2;
     int split_keys, n_splits_max;
     int full;  // every row sees all of its stream's keys (no causal count)
@@ -152,13 +164,15 @@ struct ArgmaxParams {
 uint64_t test_wait_runout_ns();
 
 // Split-KV partials of tf_paged_attn_decode / tf_paged_attn_block, arguments
-// checked (csrc/api.cu).
+// checked (csrc/api.cu).  `beside`: the launch before it on the stream is another
+// call of this function, whose outputs it neither reads nor writes; the
+// kernel may then run beside it (PromptTcParams::beside, WsParams::beside).
 tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                          const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
                          const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
                          const tf_seg *segs_host, const int32_t *page_table_host, float scale, int32_t split_keys,
                          int32_t n_splits_max, float *part_o, float *part_m, float *part_l, uint8_t *part_flag,
-                         uint32_t *status, tf_stream_t stream);
+                         uint32_t *status, tf_stream_t stream, bool beside = false);
 
 // Partials of one kind for the merge of tf_paged_attn_q8 and
 // tf_paged_attn_shared: arrays [n_rows_total][hq][n_splits](*D), of which a row
