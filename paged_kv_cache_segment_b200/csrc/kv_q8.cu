@@ -8,7 +8,7 @@
 // owns a (row, kv-head): every lane moves one 16-byte chunk of bf16 of K and
 // one of V and the 8-byte runs of codes they become, so each side is whole
 // contiguous runs of D (codes) or 2 D (bf16) bytes and both tensors' loads are
-// in flight at once.  The row's largest magnitude is an integer maximum of the
+// in flight at once; with enough rows a group takes four.  The row's largest magnitude is an integer maximum of the
 // bf16 magnitude patterns over the group (its order is the values' order, and
 // the all-ones exponent of a NaN or an infinity tops every finite pattern).
 #include <climits>
@@ -48,87 +48,137 @@ __device__ __forceinline__ bool kv_q8_seg(const KvQ8Params &p, bool rows_used, t
     return bit == 0;
 }
 
-template <int D, int TYPE>
+// Unit (row, kv-head) `k` of this group's U: its row and head, or live = false.
+struct Unit {
+    int i, g;
+    bool live;
+};
+template <int L, int U>
+__device__ __forceinline__ Unit unit_of(const KvQ8Params &p, int n_rows, int k) {
+    constexpr uint32_t kGroups = kQ8Threads / L;
+    const uint32_t u = (blockIdx.x * U + k) * kGroups + threadIdx.x / L, n = (uint32_t)n_rows * (uint32_t)p.hkv;
+    Unit x;
+    x.live = u < n;
+    x.i = x.live ? (int)(u / (uint32_t)p.hkv) : 0;
+    x.g = x.live ? (int)(u - (uint32_t)x.i * (uint32_t)p.hkv) : 0;
+    return x;
+}
+
+template <int D, int TYPE, int U>
 __global__ void __launch_bounds__(kQ8Threads) kv_append_q8_kernel(const KvQ8Params p) {
     constexpr int L = D / 8;  // lanes of a group
     tf_seg e;
     if (!kv_q8_seg(p, true, e)) return;
     const int lane = threadIdx.x % L;
-    const int64_t n_units = (int64_t)e.n_rows * p.hkv;
-    const int64_t u = (int64_t)blockIdx.x * (kQ8Threads / L) + threadIdx.x / L;  // (row, kv-head) of this group
-    const bool live = u < n_units;
-    const int i = live ? (int)(u / p.hkv) : 0, g = live ? (int)(u - (int64_t)i * p.hkv) : 0;
-    const int j = e.n_keys - e.n_rows + i;
-    int page = -1;
-    if (live) page = p.page_table[e.pt_base + (j >> p.log2_page)];
-    const bool ok = live && page >= 0 && page < p.n_pages;
-    if (live && !ok && lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
-    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (ok) {
-        const int64_t src = ((int64_t)(e.q_row + i) * p.hkv + g) * D + lane * 8;
-        x[0] = __ldg(reinterpret_cast<const uint4 *>(p.k_rows + src));
-        x[1] = __ldg(reinterpret_cast<const uint4 *>(p.v_rows + src));
+    // every unit's rows and page ids first
+    uint4 x[U][2];
+    int page[U];
+    Unit w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        w[k] = unit_of<L, U>(p, e.n_rows, k);
+        x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+        page[k] = -1;
+        if (w[k].live) {
+            const int64_t src = ((int64_t)(e.q_row + w[k].i) * p.hkv + w[k].g) * D + lane * 8;
+            x[k][0] = __ldg(reinterpret_cast<const uint4 *>(p.k_rows + src));
+            x[k][1] = __ldg(reinterpret_cast<const uint4 *>(p.v_rows + src));
+            page[k] = p.page_table[e.pt_base + ((e.n_keys - e.n_rows + w[k].i) >> p.log2_page)];
+        }
     }
-    const int64_t slot = (((int64_t)page * p.hkv + g) << p.log2_page) | (j & ((1 << p.log2_page) - 1));
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
-        uint32_t amax = 0;
+    for (int k = 0; k < U; ++k) {
+        const bool ok = w[k].live && page[k] >= 0 && page[k] < p.n_pages;
+        if (w[k].live && !ok && lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
+        const int j = e.n_keys - e.n_rows + w[k].i;
+        const int64_t slot = (((int64_t)page[k] * p.hkv + w[k].g) << p.log2_page) | (j & ((1 << p.log2_page) - 1));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t v[4] = {x[k][t].x, x[k][t].y, x[k][t].z, x[k][t].w};
+            uint32_t amax = 0;
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const bool nf = amax >= 0x7f80u;
-        const int k2 = q8_exponent<TYPE>(amax);
-        const float s = __uint_as_float((uint32_t)(kE8Bias - k2) << 23);  // 2^-k2, exact
-        uint2 c;
-        c.x = q8_encode4<TYPE>(bf16_lo_to_f32(w[0]) * s, bf16_hi_to_f32(w[0]) * s, bf16_lo_to_f32(w[1]) * s,
-                               bf16_hi_to_f32(w[1]) * s);
-        c.y = q8_encode4<TYPE>(bf16_lo_to_f32(w[2]) * s, bf16_hi_to_f32(w[2]) * s, bf16_lo_to_f32(w[3]) * s,
-                               bf16_hi_to_f32(w[3]) * s);
-        if (nf) c = make_uint2(0u, 0u);
-        if (ok) {
-            reinterpret_cast<uint2 *>((t ? p.v_codes : p.k_codes) + slot * D)[lane] = c;
-            if (lane == 0) (t ? p.v_scale : p.k_scale)[slot] = (uint8_t)(nf ? kE8Nan : (uint32_t)(k2 + kE8Bias));
+            for (int q = 0; q < 4; ++q) amax = max(amax, max(v[q] & 0x7fffu, (v[q] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const bool nf = amax >= 0x7f80u;
+            const int k2 = q8_exponent<TYPE>(amax);
+            const float s = __uint_as_float((uint32_t)(kE8Bias - k2) << 23);  // 2^-k2, exact
+            uint2 c;
+            c.x = q8_encode4<TYPE>(bf16_lo_to_f32(v[0]), bf16_hi_to_f32(v[0]), bf16_lo_to_f32(v[1]),
+                                   bf16_hi_to_f32(v[1]), s);
+            c.y = q8_encode4<TYPE>(bf16_lo_to_f32(v[2]), bf16_hi_to_f32(v[2]), bf16_lo_to_f32(v[3]),
+                                   bf16_hi_to_f32(v[3]), s);
+            if (nf) c = make_uint2(0u, 0u);
+            if (ok) {
+                reinterpret_cast<uint2 *>((t ? p.v_codes : p.k_codes) + slot * D)[lane] = c;
+                if (lane == 0) (t ? p.v_scale : p.k_scale)[slot] = (uint8_t)(nf ? kE8Nan : (uint32_t)(k2 + kE8Bias));
+            }
         }
     }
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, int U>
 __global__ void __launch_bounds__(kQ8Threads) kv_read_q8_kernel(const KvQ8Params p) {
     constexpr int L = D / 8;
     tf_seg e;
     if (!kv_q8_seg(p, false, e)) return;
     const int lane = threadIdx.x % L;
-    const int64_t u = (int64_t)blockIdx.x * (kQ8Threads / L) + threadIdx.x / L;
-    if (u >= (int64_t)e.n_rows * p.hkv) return;
-    const int i = (int)(u / p.hkv), g = (int)(u - (int64_t)i * p.hkv);
-    const int j = e.n_keys - e.n_rows + i, at = e.pt_base + (j >> p.log2_page);
-    const int page = p.page_table[at], to = p.dst_page_table[at];
-    if (page < 0 || page >= p.n_pages || to < 0 || to >= p.n_pages_dst) {
-        if (lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
-        return;
+    Unit w[U];
+    int page[U], to[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        w[k] = unit_of<L, U>(p, e.n_rows, k);
+        page[k] = to[k] = -1;
+        if (w[k].live) {
+            const int at = e.pt_base + ((e.n_keys - e.n_rows + w[k].i) >> p.log2_page);
+            page[k] = p.page_table[at];
+            to[k] = p.dst_page_table[at];
+        }
     }
-    const int in_page = j & ((1 << p.log2_page) - 1);
-    const int64_t src = (((int64_t)page * p.hkv + g) << p.log2_page) | in_page;
-    const int64_t dst = (((int64_t)to * p.hkv + g) << p.log2_page) | in_page;
-    const uint2 ck = __ldg(reinterpret_cast<const uint2 *>(p.k_codes + src * D) + lane);
-    const uint2 cv = __ldg(reinterpret_cast<const uint2 *>(p.v_codes + src * D) + lane);
-    const float sk = e8m0_f32(__ldg(p.k_scale + src)), sv = e8m0_f32(__ldg(p.v_scale + src));
-    reinterpret_cast<uint4 *>(p.k_pool + dst * D)[lane] = q8_to_bf16x8<TYPE>(ck, sk);
-    reinterpret_cast<uint4 *>(p.v_pool + dst * D)[lane] = q8_to_bf16x8<TYPE>(cv, sv);
+    uint2 ck[U], cv[U];
+    uint32_t ek[U], ev[U];
+    int64_t dst[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const bool bad = page[k] < 0 || page[k] >= p.n_pages || to[k] < 0 || to[k] >= p.n_pages_dst;
+        if (w[k].live && bad && lane == 0) atomicOr(p.status, TF_DEV_BAD_PAGE);
+        w[k].live = w[k].live && !bad;
+        const int in_page = (e.n_keys - e.n_rows + w[k].i) & ((1 << p.log2_page) - 1);
+        const int64_t src = (((int64_t)page[k] * p.hkv + w[k].g) << p.log2_page) | in_page;
+        dst[k] = (((int64_t)to[k] * p.hkv + w[k].g) << p.log2_page) | in_page;
+        if (w[k].live) {
+            ck[k] = __ldg(reinterpret_cast<const uint2 *>(p.k_codes + src * D) + lane);
+            cv[k] = __ldg(reinterpret_cast<const uint2 *>(p.v_codes + src * D) + lane);
+            ek[k] = __ldg(p.k_scale + src);
+            ev[k] = __ldg(p.v_scale + src);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (!w[k].live) continue;
+        reinterpret_cast<uint4 *>(p.k_pool + dst[k] * D)[lane] = q8_to_bf16x8<TYPE>(ck[k], e8m0_f32(ek[k]));
+        reinterpret_cast<uint4 *>(p.v_pool + dst[k] * D)[lane] = q8_to_bf16x8<TYPE>(cv[k], e8m0_f32(ev[k]));
+    }
+}
+
+template <int D, int TYPE, int U>
+cudaError_t launch_kv_q8_u(const KvQ8Params &p, bool read, int n_segs, int64_t units, cudaStream_t st) {
+    constexpr int kGroups = kQ8Threads / (D / 8) * U;
+    const dim3 grid((unsigned)((units + kGroups - 1) / kGroups), (unsigned)n_segs);
+    if (read)
+        kv_read_q8_kernel<D, TYPE, U><<<grid, kQ8Threads, 0, st>>>(p);
+    else
+        kv_append_q8_kernel<D, TYPE, U><<<grid, kQ8Threads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <int D, int TYPE>
 cudaError_t launch_kv_q8(const KvQ8Params &p, bool read, int n_segs, int max_rows, cudaStream_t st) {
-    constexpr int kGroups = kQ8Threads / (D / 8);
     const int64_t units = (int64_t)max_rows * p.hkv;
-    const dim3 grid((unsigned)((units + kGroups - 1) / kGroups), (unsigned)n_segs);
-    if (read)
-        kv_read_q8_kernel<D, TYPE><<<grid, kQ8Threads, 0, st>>>(p);
-    else
-        kv_append_q8_kernel<D, TYPE><<<grid, kQ8Threads, 0, st>>>(p);
-    return cudaGetLastError();
+    // several units a thread, their loads in flight together, once that still fills the GPU
+    const int64_t wave = (int64_t)device_sms() * (2048 / (D / 8));  // units of one a group on every SM
+    if (units * n_segs >= 4 * wave) return launch_kv_q8_u<D, TYPE, 4>(p, read, n_segs, units, st);
+    return launch_kv_q8_u<D, TYPE, 1>(p, read, n_segs, units, st);
 }
 
 template <int TYPE>
@@ -185,7 +235,7 @@ tf_status tf_kv_append_q8(const void *k_rows, const void *v_rows, int32_t n_rows
         if (rc != TF_OK) return rc;
         if (max_rows == 0) return TF_OK;
     }
-    if ((int64_t)max_rows * c.n_kv_heads > ((int64_t)1 << 33)) return TF_ERR_UNSUPPORTED;
+    if ((int64_t)max_rows * c.n_kv_heads > ((int64_t)1 << 30)) return TF_ERR_UNSUPPORTED;
     KvQ8Params p = cache_params(c);
     p.k_rows = static_cast<const uint16_t *>(k_rows);
     p.v_rows = static_cast<const uint16_t *>(v_rows);
@@ -226,8 +276,7 @@ tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *page_table
         }
     }
     if (max_rows == 0) return TF_OK;
-    if (max_rows > INT_MAX) max_rows = INT_MAX;
-    if (max_rows * c.n_kv_heads > ((int64_t)1 << 33)) return TF_ERR_UNSUPPORTED;
+    if (max_rows * c.n_kv_heads > ((int64_t)1 << 30)) return TF_ERR_UNSUPPORTED;
     KvQ8Params p = cache_params(c);
     p.k_pool = static_cast<uint16_t *>(k_pool);
     p.v_pool = static_cast<uint16_t *>(v_pool);

@@ -107,10 +107,10 @@ __device__ __forceinline__ int q8_exponent(uint32_t amax) {
     return k > kE8MinExp ? k : kE8MinExp;
 }
 
-// Four values already scaled into the code range, to codes (nearest, ties to
-// even; lowest byte first).
+// Four values times s (a power of two that brings them into the code range), to
+// codes (nearest, ties to even; lowest byte first).
 template <int TYPE>
-__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float d, float s) {
     if constexpr (TYPE == TF_KV_E4M3) {
         uint32_t r;
         asm("{\n\t.reg .b16 lo, hi;\n\t"
@@ -118,11 +118,14 @@ __device__ __forceinline__ uint32_t q8_encode4(float a, float b, float c, float 
             "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
             "mov.b32 %0, {lo, hi};\n\t}"
             : "=r"(r)
-            : "f"(a), "f"(b), "f"(c), "f"(d));
+            : "f"(a * s), "f"(b * s), "f"(c * s), "f"(d * s));
         return r;
     } else {
-        const uint32_t x = (uint32_t)__float2int_rn(a), y = (uint32_t)__float2int_rn(b);
-        const uint32_t z = (uint32_t)__float2int_rn(c), w = (uint32_t)__float2int_rn(d);
+        // a * s is exact; adding 1.5 * 2^23 rounds it to an integer, whose low
+        // byte is the sum's
+        const float big = 12582912.f;
+        const uint32_t x = __float_as_uint(fmaf(a, s, big)), y = __float_as_uint(fmaf(b, s, big));
+        const uint32_t z = __float_as_uint(fmaf(c, s, big)), w = __float_as_uint(fmaf(d, s, big));
         return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
     }
 }
