@@ -32,6 +32,12 @@
 extern "C" {
 #endif
 
+/*
+ * A launch whose bounded wait gave up (TF_DEV_TIMEOUT in the status word) leaves
+ * the rows of tf_paged_attn_q8 and tf_paged_attn_shared flagged NaN, as does any
+ * later call while the caller has not cleared that bit.
+ */
+
 /* A given token lies outside [0, n_cols) (tf_logprob_rows). */
 #define TF_DEV_BAD_TOKEN 0x20u
 
@@ -45,7 +51,9 @@ enum { TF_KV_E4M3 = 1, TF_KV_INT8 = 2 };
  * code * 2^(e - 127), the code an e4m3 number or a signed byte.  Bytes 27 to
  * 249 are scales; 255 marks a row that held a NaN or an infinity (its codes
  * are 0): a query that sees it is flagged.  A value is exact in bf16, so
- * attention over the cache and over its read-back are the same attention.
+ * attention over the cache and over its read-back are the same attention.  (An
+ * e4m3 NaN code under another scale byte, which no append writes, flags the
+ * queries that see it and may flag other rows of its stream.)
  *
  *  k_codes, v_codes  u8 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned
  *  k_scale, v_scale  u8 [n_pages][n_kv_heads][page_size], 16-byte aligned
@@ -72,6 +80,7 @@ typedef struct {
  * for bit; an element is off by at most 2^-4 of itself (e4m3, above 2^(k-6)) or
  * by 2^(k-1) (int8).  A row holding a NaN or an infinity is stored as codes 0
  * and scale byte 255.  (A magnitude that rounds to 2^128 reads as infinity.)
+ * Streams must not share the slots they write.
  */
 TFS_API tf_status tf_kv_append_q8(const void *k_rows, const void *v_rows, int32_t n_rows_total,
                                   const tf_q8_cache *cache_host, const int32_t *page_table, int32_t page_table_len,
@@ -107,10 +116,18 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  * tf_paged_attn_block) and tf_attn_merge compute, with K and V the values the
  * codes stand for.  Scores, softmax statistics and sums are held in fp32.
  *
+ *  scale       > 0
  *  split_keys  keys a partial covers: 0 lets the library choose (from the host
  *              table when one is given, else ceil(n_keys / n_splits_max)
  *              rounded up to the page size, stream by stream); else >= 16
  *  n_splits_max  the most partials a stream may take; it sizes the workspace
+ *
+ * A captured call keeps the row counts of the host table it was captured with
+ * and, with split_keys = 0, its longest stream's partials: a replay whose device
+ * table asks for more partials reports TF_DEV_SPLITS and flags the stream's
+ * rows.  With a given split_keys a stream may grow to n_splits_max * split_keys
+ * keys.
+ *
  *  workspace   device scratch of at least tf_paged_attn_q8_workspace_bytes(...)
  *              bytes, 16-byte aligned; needs no initialisation
  *  out         f32 or bf16 (out_dtype TF_OUT_F32 / TF_OUT_BF16, rounded once)
@@ -146,8 +163,10 @@ TFS_API size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_
  *              overlap; a row no entry names has no prefix; n_rows = 0 is
  *              ignored, otherwise n_keys >= 1
  *  prefixes_host, segs_host  optional host copies, validated
+ *  scale       > 0
  *  split_keys  keys a partial covers: 0 lets the library choose for the
- *              prefixes and for the streams; else >= 16, for both
+ *              prefixes and for the streams (captured calls: as for
+ *              tf_paged_attn_q8); else >= 16, for both
  *  n_prefix_splits, n_splits_max  the most partials a prefix and a stream may
  *              take; they size the workspace
  *  workspace   at least tf_paged_attn_shared_workspace_bytes(...) bytes,

@@ -25,7 +25,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
                            int32_t split_keys, int32_t n_splits_max, void *workspace, size_t workspace_bytes,
                            void *out, int32_t out_dtype, uint8_t *flags, uint32_t *status, tf_stream_t stream) {
     if (!cache_host || n_rows_total < 0 || n_q_heads <= 0 || page_table_len < 0 || n_segs < 0 || split_keys < 0 ||
-        n_splits_max <= 0 || !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
+        n_splits_max <= 0 || !(scale > 0.f) || !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
         return TF_ERR_ARG;
     const tf_q8_cache c = *cache_host;
     tf_status rc = check_q8_shape(c);
@@ -54,8 +54,9 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
                                       n_splits_max)
                        : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), 256,
                                         n_splits_max);
-        // as many partial slots as the longest stream takes: the merge's reads stay close together
-        splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);
+        // a chosen split gets the partial slots its longest stream takes; a given one all n_splits_max, so that a
+        // captured call may be replayed over streams that have grown
+        if (split_keys == 0) splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);
     }
     const int64_t n_qgroups = ((int64_t)max_rows * group + 63) / 64;
     if (n_qgroups * c.n_kv_heads > 65535 || (int64_t)max_rows * n_q_heads > ((int64_t)1 << 31))
@@ -175,6 +176,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     m.out = out;
     m.out_bf16 = out_dtype == TF_OUT_BF16;
     m.flags = flags;
+    m.status = status;
     return cuda_status(launch_merge_segs(m, c.head_dim, st));
 }
 

@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
+#include <vector>
 #include <cuda_runtime.h>
 
 #include "api_common.h"
@@ -33,7 +35,7 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
                                void *out, int32_t out_dtype, uint8_t *flags, uint32_t *status, tf_stream_t stream) {
     if (n_rows_total < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_pages < 0 || page_table_len < 0 ||
         n_prefixes < 0 || n_segs < 0 || split_keys < 0 || n_prefix_splits <= 0 || n_splits_max <= 0 ||
-        !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
+        !(scale > 0.f) || !std::isfinite(scale) || (out_dtype != TF_OUT_F32 && out_dtype != TF_OUT_BF16))
         return TF_ERR_ARG;
     const int lp = log2_exact(page_size);
     if (n_q_heads % n_kv_heads != 0 || !head_dim_ok(head_dim) || lp < 3 || lp > 10 ||
@@ -59,11 +61,12 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         if (rc != TF_OK || rows == 0) return rc;
         // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave; the decode kernel
         // with the CTA an SM that it has beside the other
-        if (split == 0)
+        if (split == 0) {
             split = (int64_t)rows * group > 8
                         ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), 128, splits)
                         : decode_split(host, n, n_kv_heads, device_sms(), 1024, splits);
-        splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
+            splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
+        }
         return TF_OK;
     };
     if (segs_host) {
@@ -74,12 +77,15 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         const tf_status rc = plan(prefixes_host, n_prefixes, true, pre_rows, pre_splits, pre_split);
         if (rc != TF_OK) return rc;
         // a row belongs to one prefix
-        for (int a = 0; a < n_prefixes; ++a)
-            for (int b = 0; b < a; ++b) {
-                const tf_seg x = prefixes_host[a], y = prefixes_host[b];
-                if (x.n_rows > 0 && y.n_rows > 0 && x.q_row < y.q_row + y.n_rows && y.q_row < x.q_row + x.n_rows)
-                    return TF_ERR_ARG;
-            }
+        if (n_prefixes > 1) {
+            std::vector<std::pair<int, int>> runs;  // [first row, past the last)
+            for (int a = 0; a < n_prefixes; ++a)
+                if (prefixes_host[a].n_rows > 0)
+                    runs.emplace_back(prefixes_host[a].q_row, prefixes_host[a].q_row + prefixes_host[a].n_rows);
+            std::sort(runs.begin(), runs.end());
+            for (size_t a = 1; a < runs.size(); ++a)
+                if (runs[a].first < runs[a - 1].second) return TF_ERR_ARG;
+        }
     }
     if (max_rows == 0) return TF_OK;
     // what either partial launch would refuse, before the first one
@@ -118,6 +124,7 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
     m.out = out;
     m.out_bf16 = out_dtype == TF_OUT_BF16;
     m.flags = flags;
+    m.status = status;
     return cuda_status(launch_merge_segs(m, head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -86,7 +86,8 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
-template <int D, int TYPE>
+// DIRECT: one split a stream, so an item's rows are final and go to p.out.
+template <int D, int TYPE, bool DIRECT>
 __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const WsParams p) {
@@ -137,6 +138,18 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
     const int total = s_total, n_full = s_full;
     const int bid = (int)blockIdx.x, grid = (int)gridDim.x;
 
+    // final rows that no item writes: NaN, flagged
+    auto flag_rows = [&](int q_row, int rows, int h0, int heads, int from, int step) {
+        for (int x = from; x < rows * heads * D; x += step) {
+            const int q = x / D, i = q / heads;
+            const int64_t unit = (int64_t)(q_row + i) * p.hq + h0 + (q - i * heads);
+            if (p.out_bf16)
+                static_cast<uint16_t *>(p.out)[unit * D + x % D] = 0x7fc0;
+            else
+                static_cast<float *>(p.out)[unit * D + x % D] = __int_as_float(0x7fc00000);
+            if (x % D == 0) p.out_flags[unit] = 1;
+        }
+    };
     if (warp == C::NC) {
         // ---- producer warp: the items in order, a tile a stage; page ids come
         // a window of 32 at a time, the next item's before this one's tiles
@@ -260,6 +273,15 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                 atomicOr(p.status, TF_DEV_TIMEOUT);
                 s_abort = 1;
             }
+        }
+        if constexpr (DIRECT) {
+            for (int s = bid; s < p.n_segs; s += grid)
+                if (prefix[s + 1] == prefix[s]) {  // an entry found bad (or with no rows)
+                    const tf_seg e = p.segs[s];
+                    const int lo = max(e.q_row, 0);
+                    const int64_t hi = min((int64_t)e.q_row + e.n_rows, (int64_t)p.n_rows_total);
+                    if (hi > lo) flag_rows(lo, (int)(hi - lo), 0, p.hq, lane, 32);
+                }
         }
         cp_async_commit();
         cp_async_wait<0>();  // no scale byte is in flight when this CTA ends
@@ -583,7 +605,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                     if (qq >= q_item) return;
                     const int i = qq / p.group, hl = qq - i * p.group;
                     const int64_t unit = (int64_t)(it.q_row + i) * p.hq + it.g * p.group + hl;
-                    if (p.out) {  // one split a stream: the row itself
+                    if constexpr (DIRECT) {
                         const bool bad = f || !(l > 0.f);
                         const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
@@ -598,17 +620,17 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                                     bad ? make_float2(nan, nan) : make_float2(y, z);
                         }
                         if (gq == 0) p.out_flags[unit] = (uint8_t)(bad ? 1 : 0);
-                        return;
-                    }
-                    const int64_t at = unit * p.n_splits_max + it.c;
-                    float *dst = p.part_o + at * D + 2 * gq;
+                    } else {
+                        const int64_t at = unit * p.n_splits_max + it.c;
+                        float *dst = p.part_o + at * D + 2 * gq;
 #pragma unroll
-                    for (int u = 0; u < D / 16; ++u)
-                        *reinterpret_cast<float2 *>(dst + 16 * u) = make_float2(o[u][c], o[u][c + 2]);
-                    if (gq == 0) {
-                        p.part_m[at] = m == -FLT_MAX ? -INFINITY : m * kLn2;
-                        p.part_l[at] = l;
-                        p.part_flag[at] = (uint8_t)(f ? 1 : 0);
+                        for (int u = 0; u < D / 16; ++u)
+                            *reinterpret_cast<float2 *>(dst + 16 * u) = make_float2(o[u][c], o[u][c + 2]);
+                        if (gq == 0) {
+                            p.part_m[at] = m == -FLT_MAX ? -INFINITY : m * kLn2;
+                            p.part_l[at] = l;
+                            p.part_flag[at] = (uint8_t)(f ? 1 : 0);
+                        }
                     }
                 };
                 write(qa, m0, l0, f0, 0);
@@ -620,6 +642,11 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
     // ---- a CTA that gave up leaves only when its copies have landed (each
     // barrier gets a bounded wait for the phase it is in)
     __syncthreads();
+    if (DIRECT && s_abort)  // its rows are final, and some of them unwritten
+        for (int k = 0, L = ws_snake(0, bid, grid); L < total; L = ws_snake(++k, bid, grid)) {
+            const WsItem it = ws_resolve<false>(p, prefix, prefix_full, tail_order, n_full, L);
+            flag_rows(it.q_row, it.n_rows, it.g * p.group, p.group, tid, C::kThreads);
+        }
     if (s_abort && tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_wait(smem_u32(&full_bar[i]), 0u, 20000000ull);
@@ -634,7 +661,7 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
 
 // CTAs of a full launch on the current device: its SMs times the CTAs an SM
 // holds, looked up once a device.
-template <int D, int TYPE>
+template <int D, int TYPE, bool DIRECT>
 int grid_cap() {
     constexpr int kMaxDevices = 64;
     static std::atomic<int> cap[kMaxDevices];  // 0: not looked up yet
@@ -644,9 +671,9 @@ int grid_cap() {
     if (known > 0) return known;
     int n = 148, per_sm = 1;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
-    if (cudaFuncSetAttribute(decode_q8_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_q8_kernel<D, TYPE, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Q8Cfg<D>::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_q8_kernel<D, TYPE>, Q8Cfg<D>::kThreads,
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_q8_kernel<D, TYPE, DIRECT>, Q8Cfg<D>::kThreads,
                                                       Q8Cfg<D>::kSmem) != cudaSuccess ||
         per_sm < 1)
         per_sm = 1;
@@ -654,7 +681,7 @@ int grid_cap() {
     return n * per_sm;
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool DIRECT>
 cudaError_t launch_t(const WsParams &p, const void *k, const void *v, int64_t n_items_bound, cudaStream_t st) {
     using C = Q8Cfg<D>;
     CUtensorMap mk, mv;
@@ -664,10 +691,10 @@ cudaError_t launch_t(const WsParams &p, const void *k, const void *v, int64_t n_
     const cuuint32_t box[4] = {(cuuint32_t)C::kRow, (cuuint32_t)BR, 1, 1};
     if (!make_tensor_map_u8(&mk, k, 4, dims, strides, box, C::kRow)) return cudaErrorInvalidValue;
     if (!make_tensor_map_u8(&mv, v, 4, dims, strides, box, C::kRow)) return cudaErrorInvalidValue;
-    auto kern = decode_q8_kernel<D, TYPE>;
+    auto kern = decode_q8_kernel<D, TYPE, DIRECT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    int64_t grid = grid_cap<D, TYPE>();
+    int64_t grid = grid_cap<D, TYPE, DIRECT>();
     if (n_items_bound < grid) grid = n_items_bound < 1 ? 1 : n_items_bound;
     WsParams q = p;
     if (const uint64_t runout = test_wait_runout_ns()) {
@@ -687,22 +714,28 @@ bool decode_q8_supported(int head_dim, int n_segs) {
 int decode_q8_grid(int head_dim, int kv_type) {
     const bool e = kv_type == TF_KV_E4M3;
     switch (head_dim) {
-        case 64: return e ? grid_cap<64, TF_KV_E4M3>() : grid_cap<64, TF_KV_INT8>();
-        case 128: return e ? grid_cap<128, TF_KV_E4M3>() : grid_cap<128, TF_KV_INT8>();
-        default: return e ? grid_cap<256, TF_KV_E4M3>() : grid_cap<256, TF_KV_INT8>();
+        case 64: return e ? grid_cap<64, TF_KV_E4M3, false>() : grid_cap<64, TF_KV_INT8, false>();
+        case 128: return e ? grid_cap<128, TF_KV_E4M3, false>() : grid_cap<128, TF_KV_INT8, false>();
+        default: return e ? grid_cap<256, TF_KV_E4M3, false>() : grid_cap<256, TF_KV_INT8, false>();
     }
+}
+
+template <int D, int TYPE>
+static cudaError_t launch_d(const WsParams &p, const void *k, const void *v, int64_t n_items_bound, cudaStream_t st) {
+    return p.out ? launch_t<D, TYPE, true>(p, k, v, n_items_bound, st)
+                 : launch_t<D, TYPE, false>(p, k, v, n_items_bound, st);
 }
 
 cudaError_t launch_decode_q8(const WsParams &p, int head_dim, int kv_type, const void *k, const void *v,
                              int64_t n_items_bound, cudaStream_t st) {
     const bool e = kv_type == TF_KV_E4M3;
     switch (head_dim) {
-        case 64: return e ? launch_t<64, TF_KV_E4M3>(p, k, v, n_items_bound, st)
-                          : launch_t<64, TF_KV_INT8>(p, k, v, n_items_bound, st);
-        case 128: return e ? launch_t<128, TF_KV_E4M3>(p, k, v, n_items_bound, st)
-                           : launch_t<128, TF_KV_INT8>(p, k, v, n_items_bound, st);
-        case 256: return e ? launch_t<256, TF_KV_E4M3>(p, k, v, n_items_bound, st)
-                           : launch_t<256, TF_KV_INT8>(p, k, v, n_items_bound, st);
+        case 64: return e ? launch_d<64, TF_KV_E4M3>(p, k, v, n_items_bound, st)
+                          : launch_d<64, TF_KV_INT8>(p, k, v, n_items_bound, st);
+        case 128: return e ? launch_d<128, TF_KV_E4M3>(p, k, v, n_items_bound, st)
+                           : launch_d<128, TF_KV_INT8>(p, k, v, n_items_bound, st);
+        case 256: return e ? launch_d<256, TF_KV_E4M3>(p, k, v, n_items_bound, st)
+                           : launch_d<256, TF_KV_INT8>(p, k, v, n_items_bound, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -75,6 +75,8 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) merge_segs_kernel(const Merg
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a partial kernel whose wait ran out left partials unwritten
+    bad |= (*p.status & TF_DEV_TIMEOUT) != 0;
     const int64_t unit = (int64_t)row * p.hq + h;
     const int d0 = sl * DW + lane * 4;
     const bool col = lane * 4 < DW;

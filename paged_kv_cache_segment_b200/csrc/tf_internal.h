@@ -192,6 +192,7 @@ struct MergeSegsParams {
     void *out;
     int out_bf16;
     uint8_t *flags;
+    const uint32_t *status;
 };
 cudaError_t launch_merge_segs(const MergeSegsParams &p, int head_dim, cudaStream_t st);
 

@@ -1,0 +1,191 @@
+"""Edges of the serving calls on the GPU: waits that run out, more streams than
+the decode kernels take, caches and logits past 32-bit offsets, calls on two
+streams at once, workspaces of the smallest size."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_segment_b200 as tf
+from paged_kv_cache_segment_b200 import binding
+from paged_kv_cache_segment_b200 import workloads as wl
+
+import _serving as sv
+from _gpu import DEV, dev, status_word
+from test_gpu_q8 import attn, cache_of, q8_batch, reference
+from test_gpu_shared import batch, shared
+from test_gpu_shared import reference as shared_reference
+
+pytestmark = pytest.mark.gpu
+
+
+def with_hook(fn):
+    tf.tf_wait_limit_test(True)
+    try:
+        return fn()
+    finally:
+        tf.tf_wait_limit_test(False)
+
+
+@pytest.mark.parametrize("rows,keys,hq,hkv,d", [([1, 1], [700, 1500], 32, 8, 128),  # decode, partials and merge
+                                                ([1, 1, 1], [60, 100, 7], 8, 2, 64),  # decode, one split: no merge
+                                                ([5, 14], [900, 2100], 16, 2, 256)])  # the tensor-core kernel
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_q8_wait_runs_out_flags_every_row_then_recovers(rows, keys, hq, hkv, d, dt):
+    b, sides, c = q8_batch("e4m3", 3, rows=rows, keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32)
+    out, flags, st = with_hook(lambda: attn(c, b, "e4m3", out_dtype=dt))
+    assert st & binding.TF_DEV_TIMEOUT
+    assert (flags == 1).all() and np.isnan(out).all()
+    out, flags, st = attn(c, b, "e4m3", out_dtype=dt)
+    assert st == 0
+    ref, fl, vmax = reference(b, sides, "e4m3")
+    sv.check_attention(out, flags, ref, fl, vmax, dt == torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d", [(1, 32, 8, 128), (4, 16, 2, 256)])
+def test_shared_wait_runs_out_flags_every_row_then_recovers(rows, hq, hkv, d):
+    groups = [0, 0, 0]
+    b, prefixes, segs = batch(4, [500], groups, [rows] * 3, [20, 130, 300], hq, hkv, d, 32)
+    out, flags, st = with_hook(lambda: shared(b, prefixes, segs))
+    assert st & binding.TF_DEV_TIMEOUT
+    assert (flags == 1).all() and np.isnan(out).all()
+    out, flags, st = shared(b, prefixes, segs)
+    assert st == 0
+    ref, fl, vmax = shared_reference(b, prefixes, segs, groups)
+    sv.check_attention(out, flags, ref, fl, vmax, False)
+
+
+def test_three_hundred_streams():
+    rng = np.random.default_rng(0)
+    n = 300  # past the decode kernels' tables
+    keys = [int(k) for k in rng.integers(1, 90, n)]
+    b, sides, c = q8_batch("int8", 5, rows=[1] * n, keys=keys, n_q_heads=4, n_kv_heads=2, head_dim=64, page_size=16)
+    ref, fl, vmax = reference(b, sides, "int8")
+    out, flags, st = attn(c, b, "int8")
+    assert st == 0
+    sv.check_attention(out, flags, ref, fl, vmax, False)
+    groups = [s % 2 for s in sorted(range(n), key=lambda s: s % 2)]
+    b, prefixes, segs = batch(6, [70, 33], groups, [1] * n, keys, 4, 2, 64, 16)
+    ref, fl, vmax = shared_reference(b, prefixes, segs, groups)
+    out, flags, st = shared(b, prefixes, segs)
+    assert st == 0
+    sv.check_attention(out, flags, ref, fl, vmax, False)
+
+
+@pytest.mark.parametrize("rows", [1, 12])
+def test_a_cache_past_32_bit_offsets(rows):
+    """70,000 pages of 64 x 2 x 256 codes (2.3e9 of them) with a stream in the last pages: written, read back, attended."""
+    n_pages, hkv, psz, d, hq, n = 70000, 2, 64, 256, 4, 150
+    c = tf.Q8Cache(*(torch.empty((n_pages, hkv, psz, d), dtype=torch.int8, device=DEV) for _ in "kv"),
+                   *(torch.empty((n_pages, hkv, psz), dtype=torch.uint8, device=DEV) for _ in "kv"))
+    pt = np.array([n_pages - 1, 35000, n_pages - 2], np.int32)
+    fill = np.array([[0, n, n, 0, 3]], np.int32)
+    segs = np.array([[0, rows, n, 0, 3]], np.int32)
+    rng = np.random.default_rng(1)
+    kr, vr = wl.normal_bf16(rng, (n, hkv, d)), wl.normal_bf16(rng, (n, hkv, d))
+    st = status_word()
+    tf.tf_kv_append_q8(dev(kr), dev(vr), c, dev(pt), dev(fill), status=st, segs_host=fill, page_table_host=pt)
+    vals = [sv.values(*sv.quantise(x, "int8"), "int8") for x in (kr, vr)]
+    small = [torch.zeros((3, hkv, psz, d), dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    tf.tf_kv_read_q8(c, dev(pt), dev(fill), small[0], small[1], dev(np.arange(3, dtype=np.int32)), status=st)
+    for got, want in zip(small, vals):
+        rows_of = got.double().cpu().numpy().transpose(0, 2, 1, 3).reshape(-1, hkv, d)[:n]
+        assert (rows_of == want).all()
+    q = wl.normal_bf16(rng, (rows, hq, d))
+    out, fl = torch.empty((rows, hq, d), device=DEV), torch.empty((rows, hq), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(rows, hq, d, 4), dtype=torch.uint8, device=DEV)
+    for host in (segs, None):
+        tf.tf_paged_attn_q8(dev(q), c, dev(pt), dev(segs), scale=1 / 16, n_splits_max=4, workspace=ws, out=out, flags=fl,
+                            status=st, segs_host=host)
+        ref, rf = sv.attend(sv.bf16(q), vals[0], vals[1], [n - rows + i + 1 for i in range(rows)], 1 / 16)
+        sv.check_attention(out.cpu().numpy(), fl.cpu().numpy(), ref, rf, np.abs(vals[1]).max(), False)
+    assert int(st.item()) == 0
+
+
+def test_logits_past_32_bit_offsets():
+    rows, cols = 17000, 128000  # 2.2e9 elements; the last row is checked
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x[:-1].zero_()
+    rng = np.random.default_rng(2)
+    x[-1] = torch.from_numpy(rng.normal(0, 3, cols).astype(np.float32)).to(DEV)
+    tok = torch.zeros((rows, 1), dtype=torch.int32, device=DEV)
+    tok[-1] = 77
+    tl, fl, st = torch.empty((rows, 1), device=DEV), torch.empty(rows, dtype=torch.uint8, device=DEV), status_word()
+    ids, tops = torch.empty((rows, 3), dtype=torch.int32, device=DEV), torch.empty((rows, 3), device=DEV)
+    tf.tf_logprob_rows(x, tok, token_logprobs=tl, top_ids=ids, top_logprobs=tops, flags=fl, status=st)
+    want = sv.logprobs(x[-1:].double().cpu().numpy(), 1.0, np.array([[77]]), 3)
+    assert (ids[-1].cpu().numpy() == want[3][0]).all() and abs(tl[-1].item() - want[0][0, 0]) < 1e-4
+    # a row of equal columns: the first ones, each log(1 / n)
+    assert (ids[:-1] == torch.arange(3, device=DEV)).all()
+    assert (tl[:-1] + np.log(cols)).abs().max().item() < 1e-4 and int(fl.sum()) == 0
+
+
+def test_two_streams_at_once_with_their_own_workspaces():
+    jobs = []
+    for seed, kind in ((7, "e4m3"), (8, "int8")):
+        b, sides, c = q8_batch(kind, seed, rows=[1] * 8, keys=[900] * 8, n_q_heads=32, n_kv_heads=8, head_dim=128,
+                               page_size=32)
+        n, hq, d = b.q.shape
+        jobs.append(dict(args=(dev(b.q), c, dev(b.page_table), dev(b.segs)), host=b.segs, scale=b.scale,
+                         ws=torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 8), dtype=torch.uint8, device=DEV),
+                         out=torch.zeros((n, hq, d), device=DEV), fl=torch.zeros((n, hq), dtype=torch.uint8, device=DEV),
+                         st=status_word(), stream=torch.cuda.Stream(), ref=reference(b, sides, kind)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            tf.tf_paged_attn_q8(*j["args"], scale=j["scale"], n_splits_max=8, workspace=j["ws"], out=j["out"],
+                                flags=j["fl"], status=j["st"], segs_host=j["host"], stream=j["stream"])
+    torch.cuda.synchronize()
+    for j in jobs:
+        ref, fl, vmax = j["ref"]
+        sv.check_attention(j["out"].cpu().numpy(), j["fl"].cpu().numpy(), ref, fl, vmax, False)
+
+
+def test_a_captured_step_follows_streams_that_grow():
+    """With a given split the same captured call serves longer streams: only device memory changes."""
+    b, sides, c = q8_batch("e4m3", 9, rows=[1, 1], keys=[900, 300], n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=32)
+    n, hq, d = b.q.shape
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 8), dtype=torch.uint8, device=DEV)
+    out, fl, st = torch.zeros((n, hq, d), device=DEV), torch.zeros((n, hq), dtype=torch.uint8, device=DEV), status_word()
+    short = b.segs.copy()
+    short[:, 2] = [100, 5]
+    sg = dev(short)
+    args = (dev(b.q), c, dev(b.page_table), sg)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tf.tf_paged_attn_q8(*args, scale=b.scale, split_keys=128, n_splits_max=8, workspace=ws, out=out, flags=fl,
+                            status=st, segs_host=short)
+    for keys in ([100, 5], [128, 129], [900, 300]):
+        s = b.segs.copy()
+        s[:, 2] = keys
+        sg.copy_(dev(s))
+        g.replay()
+        torch.cuda.synchronize()
+        ref, rf, vmax = reference(b, sides, "e4m3", segs=s)
+        assert int(st.item()) == 0
+        sv.check_attention(out.cpu().numpy(), fl.cpu().numpy(), ref, rf, vmax, False, str(keys))
+
+
+@pytest.mark.parametrize("keys", [[100, 5], [1200, 300]])
+def test_a_replay_past_its_partials_is_flagged(keys):
+    """A chosen split holds the streams it was captured with: one that outgrows its partials is reported and flagged,
+    with one split (no merge) and with several."""
+    b, sides, c = q8_batch("e4m3", 10, rows=[1, 1], keys=[3000, 300], n_q_heads=8, n_kv_heads=2, head_dim=128,
+                           page_size=32)
+    n, hq, d = b.q.shape
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 64), dtype=torch.uint8, device=DEV)
+    out, fl, st = torch.zeros((n, hq, d), device=DEV), torch.zeros((n, hq), dtype=torch.uint8, device=DEV), status_word()
+    s = b.segs.copy()
+    s[:, 2] = keys
+    sg = dev(s)
+    args = (dev(b.q), c, dev(b.page_table), sg)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tf.tf_paged_attn_q8(*args, scale=b.scale, n_splits_max=64, workspace=ws, out=out, flags=fl, status=st, segs_host=s)
+    s[0, 2] = 3000
+    sg.copy_(dev(s))
+    g.replay()
+    torch.cuda.synchronize()
+    ref, rf, vmax = reference(b, sides, "e4m3", segs=s)
+    assert int(st.item()) == binding.TF_DEV_SPLITS
+    assert np.isnan(out[0].cpu().numpy()).all() and (fl[0] == 1).all()
+    sv.check_attention(out[1:].cpu().numpy(), fl[1:].cpu().numpy(), ref[1:], rf[1:], vmax, False)
