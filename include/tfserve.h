@@ -51,7 +51,7 @@ enum { TF_KV_E4M3 = 1, TF_KV_INT8 = 2 };
  * code * 2^(e - 127), the code an e4m3 number or a signed byte.  Bytes 27 to
  * 249 are scales; 255 marks a row that held a NaN or an infinity (its codes
  * are 0): a query that sees it is flagged.  A value is exact in bf16, so
- * attention over the cache and over its read-back are the same attention.  (An
+ * attention over the cache and over its read-back are one attention.  (An
  * e4m3 NaN code under another scale byte, which no append writes, flags the
  * queries that see it and may flag other rows of its stream.)
  *
@@ -122,15 +122,17 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  *              rounded up to the page size, stream by stream); else >= 16
  *  n_splits_max  the most partials a stream may take; it sizes the workspace
  *
- * A captured call keeps the row counts of the host table it was captured with
- * and, with split_keys = 0, its longest stream's partials: a replay whose device
- * table asks for more partials reports TF_DEV_SPLITS and flags the stream's
- * rows.  With a given split_keys a stream may grow to n_splits_max * split_keys
- * keys.
+ * The host table sizes the launch: its row counts and its longest stream's
+ * partials.  A call that is captured and replayed over a changing device table
+ * is given a host table with the most rows and keys the replays will see; a
+ * replay whose stream asks for more partials reports TF_DEV_SPLITS and flags the
+ * stream's rows.  Without one the launch is sized for n_splits_max partials of
+ * every stream, and decode rows do not take the kernel made for them: slower.
  *
  *  workspace   device scratch of at least tf_paged_attn_q8_workspace_bytes(...)
  *              bytes, 16-byte aligned; needs no initialisation
- *  out         f32 or bf16 (out_dtype TF_OUT_F32 / TF_OUT_BF16, rounded once)
+ *  out         f32 or bf16 (out_dtype TF_OUT_F32 / TF_OUT_BF16, rounded once; for
+ *              bf16 the softmax weights may be fed to the value product in f16)
  *              [n_rows_total][n_q_heads][head_dim], 16-byte aligned
  *  flags       u8 [n_rows_total][n_q_heads]: 1 where a visible score, value or
  *              the output is nonfinite, or the table's entry is bad; out is NaN there

@@ -54,9 +54,8 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
                                       n_splits_max)
                        : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), 256,
                                         n_splits_max);
-        // a chosen split gets the partial slots its longest stream takes; a given one all n_splits_max, so that a
-        // captured call may be replayed over streams that have grown
-        if (split_keys == 0) splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);
+        // the partial slots (and, in the tensor-core kernel, the CTAs) that the longest stream takes
+        splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);
     }
     const int64_t n_qgroups = ((int64_t)max_rows * group + 63) / 64;
     if (n_qgroups * c.n_kv_heads > 65535 || (int64_t)max_rows * n_q_heads > ((int64_t)1 << 31))
@@ -129,7 +128,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         t.part_flag = b.flag;
         t.status = status;
         if ((int64_t)t.n_qt * splits > 0x7fffffff || c.n_kv_heads > 65535) return TF_ERR_UNSUPPORTED;
-        e = launch_verify_q8(t, c.head_dim, c.kv_type, n_segs, st);
+        e = launch_verify_q8(t, c.head_dim, c.kv_type, out_dtype == TF_OUT_F32, n_segs, st);
     } else {
         AttnParams p{};
         p.q = static_cast<const uint16_t *>(q);

@@ -61,12 +61,11 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         if (rc != TF_OK || rows == 0) return rc;
         // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave; the decode kernel
         // with the CTA an SM that it has beside the other
-        if (split == 0) {
+        if (split == 0)
             split = (int64_t)rows * group > 8
                         ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), 128, splits)
                         : decode_split(host, n, n_kv_heads, device_sms(), 1024, splits);
-            splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
-        }
+        splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
         return TF_OK;
     };
     if (segs_host) {

@@ -90,7 +90,9 @@ __device__ __forceinline__ bool vq_wait(uint32_t bar, uint32_t phase, volatile u
     return false;
 }
 
-template <int D, int TYPE>
+// HILO: weights as f16 hi + f16 lo (f32 output); otherwise as one f16, whose
+// rounding is a quarter of a bf16 output's own.
+template <int D, int TYPE, bool HILO>
 __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcParams p) {
     using C = VqCfg<D>;
     extern __shared__ unsigned char smem_raw[];
@@ -271,7 +273,11 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
             for (int i = 0; i < kN / kStep; ++i) {
                 w[i] = *reinterpret_cast<const uint4 *>(src + src0 + i * kStep * D);
-                if (r0 + i * kStep >= rows) w[i] = make_uint4(0, 0, 0, 0);
+            }
+            if (rows < kN) {
+#pragma unroll
+                for (int i = 0; i < kN / kStep; ++i)
+                    if (r0 + i * kStep >= rows) w[i] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < kN / kStep; ++i) {
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 for (int kk = 0; kk < kN / 16; ++kk) {
                     const uint64_t bd = umma_desc_sw128(sV(s) + kk * 16 * 128, kSlab, 1024);
                     umma_ts(tmem + kColO, sb + kk * 8, bd, idesc_wv, (j > 0 || kk > 0) ? 1u : 0u);
-                    umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
+                    if (HILO) umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
                 }
                 umma_commit(bar(kBarO + b));
                 umma_commit(bar(kBarVFree + s));
@@ -534,13 +540,15 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             }
             const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;
             {
-                uint32_t hi[16], lo[16];
+                uint32_t hi[16], lo[HILO ? 16 : 1];
                 uint64_t ls2 = 0;  // two zeros
                 const uint64_t nmu2 = pk2(-mu, -mu);
                 auto split = [&](int c, float w0, float w1) {
                     hi[c / 2] = pack_f16x2(w0, w1);
-                    const float2 f = f16x2_to_f32(hi[c / 2]);
-                    lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
+                    if constexpr (HILO) {
+                        const float2 f = f16x2_to_f32(hi[c / 2]);
+                        lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
+                    }
                 };
                 if (__all_sync(0xffffffffu, vmax + mu - ru <= 90.f)) {
                     // a weight is its probability times 2^(e + mu - ru): a probability
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 float ls0, ls1;
                 unpk2(ls2, ls0, ls1);
                 l_run += ls0 + ls1;
-                tmem_st16(lane_base + colS + 32 + 16 * h, lo);
+                if constexpr (HILO) tmem_st16(lane_base + colS + 32 + 16 * h, lo);
                 tmem_st16(lane_base + colS + 16 * h, hi);
             }
             // O holds the tiles before this one: rescale it once W V(j - 1) is done
@@ -676,10 +684,10 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     if (sent_row) bulk_wait_read();
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool HILO>
 cudaError_t launch_t(const Q8TcParams &p, int n_segs, cudaStream_t st) {
     using C = VqCfg<D>;
-    auto kern = verify_q8_kernel<D, TYPE>;
+    auto kern = verify_q8_kernel<D, TYPE, HILO>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     Q8TcParams q = p;
@@ -692,6 +700,13 @@ cudaError_t launch_t(const Q8TcParams &p, int n_segs, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_d(const Q8TcParams &p, int kv_type, bool hilo, int n_segs, cudaStream_t st) {
+    if (kv_type == TF_KV_E4M3)
+        return hilo ? launch_t<D, TF_KV_E4M3, true>(p, n_segs, st) : launch_t<D, TF_KV_E4M3, false>(p, n_segs, st);
+    return hilo ? launch_t<D, TF_KV_INT8, true>(p, n_segs, st) : launch_t<D, TF_KV_INT8, false>(p, n_segs, st);
+}
+
 }  // namespace
 
 bool verify_q8_supported(int head_dim, int group, int split_keys) {
@@ -699,12 +714,11 @@ bool verify_q8_supported(int head_dim, int group, int split_keys) {
            split_keys > 0 && split_keys % kN == 0;
 }
 
-cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, int n_segs, cudaStream_t st) {
-    const bool e = kv_type == TF_KV_E4M3;
+cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, bool hilo, int n_segs, cudaStream_t st) {
     switch (head_dim) {
-        case 64: return e ? launch_t<64, TF_KV_E4M3>(p, n_segs, st) : launch_t<64, TF_KV_INT8>(p, n_segs, st);
-        case 128: return e ? launch_t<128, TF_KV_E4M3>(p, n_segs, st) : launch_t<128, TF_KV_INT8>(p, n_segs, st);
-        case 256: return e ? launch_t<256, TF_KV_E4M3>(p, n_segs, st) : launch_t<256, TF_KV_INT8>(p, n_segs, st);
+        case 64: return launch_d<64>(p, kv_type, hilo, n_segs, st);
+        case 128: return launch_d<128>(p, kv_type, hilo, n_segs, st);
+        case 256: return launch_d<256>(p, kv_type, hilo, n_segs, st);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -140,21 +140,24 @@ def test_two_streams_at_once_with_their_own_workspaces():
         sv.check_attention(j["out"].cpu().numpy(), j["fl"].cpu().numpy(), ref, fl, vmax, False)
 
 
-def test_a_captured_step_follows_streams_that_grow():
-    """With a given split the same captured call serves longer streams: only device memory changes."""
-    b, sides, c = q8_batch("e4m3", 9, rows=[1, 1], keys=[900, 300], n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=32)
+@pytest.mark.parametrize("split", [0, 128])
+@pytest.mark.parametrize("rows", [1, 6])
+def test_a_captured_step_follows_streams_that_grow(rows, split):
+    """A call captured with a host table of the largest lengths serves every shorter table written to the device."""
+    b, sides, c = q8_batch("e4m3", 9, rows=[rows] * 2, keys=[900, 300], n_q_heads=8, n_kv_heads=2, head_dim=128,
+                           page_size=32)
     n, hq, d = b.q.shape
     ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 8), dtype=torch.uint8, device=DEV)
     out, fl, st = torch.zeros((n, hq, d), device=DEV), torch.zeros((n, hq), dtype=torch.uint8, device=DEV), status_word()
     short = b.segs.copy()
-    short[:, 2] = [100, 5]
+    short[:, 2] = [100, 6]
     sg = dev(short)
     args = (dev(b.q), c, dev(b.page_table), sg)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        tf.tf_paged_attn_q8(*args, scale=b.scale, split_keys=128, n_splits_max=8, workspace=ws, out=out, flags=fl,
-                            status=st, segs_host=short)
-    for keys in ([100, 5], [128, 129], [900, 300]):
+        tf.tf_paged_attn_q8(*args, scale=b.scale, split_keys=split, n_splits_max=8, workspace=ws, out=out, flags=fl,
+                            status=st, segs_host=b.segs)
+    for keys in ([100, 6], [128, 129], [900, 300]):
         s = b.segs.copy()
         s[:, 2] = keys
         sg.copy_(dev(s))
