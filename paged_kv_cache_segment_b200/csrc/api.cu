@@ -144,7 +144,6 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
         w.split_keys = split_keys;
         w.n_splits_max = n_splits_max;
         w.full = full ? 1 : 0;
-        w.beside = beside ? 1 : 0;
         w.part_o = part_o;
         w.part_m = part_m;
         w.part_l = part_l;

@@ -3,7 +3,18 @@
 // keys every row sees, so the prefix's partials come from the FULL partial
 // kernels with all of those rows as queries and its keys are read once for
 // them; the streams' own keys take the causal ones, and one merge joins both
-// sets.
+// sets.  With p, q the two sets' (m, l, o) of a row, M = max(m_p, m_q):
+//   out = (2^(m_p - M) o_p + 2^(m_q - M) o_q) / (2^(m_p - M) l_p + 2^(m_q - M) l_q).
+//
+// The streams' partials go first and the prefixes' beside them, as the
+// programmatic dependent: the prefixes' CTAs fill the SMs that the others leave
+// (7 streams x 1-5 rows behind prefixes of 500-1,300 keys, D 256: both kernels on
+// disjoint SMs, 16.9 us against 28.4 one after the other).  64 one-row streams of
+// 16-1,024 keys behind 8,192 (32/8 heads, D 128) take 60 us: some 30 of the decode
+// kernel at the HBM rate (134 MB), 26 of the tensor-core kernel, 4 of the merge.
+// Those two do not overlap more than at the seam: the decode kernel's two CTAs an
+// SM leave no shared memory for the other, and with one CTA an SM beside it the
+// decode kernel took 66 us.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -59,12 +70,12 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         const tf_status rc = check_segs_host(host, n, n_rows_total, page_table_len, page_size, n_pages,
                                              page_table_host, split_keys, splits, &rows, full);
         if (rc != TF_OK || rows == 0) return rc;
-        // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave; the decode kernel
-        // with the CTA an SM that it has beside the other
+        // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave: 8,192 keys x 256 queries
+        // take 26 us in 1,024-key splits (128 CTAs), 30 in 512 and in 1,280; the decode kernel two CTAs an SM
         if (split == 0)
             split = (int64_t)rows * group > 8
                         ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), 128, splits)
-                        : decode_split(host, n, n_kv_heads, device_sms(), 1024, splits);
+                        : decode_split(host, n, n_kv_heads, device_sms() * 2, 1024, splits);
         splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
         return TF_OK;
     };
@@ -95,19 +106,19 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
     const PartBuffers pre = part_buffers(ws, n_rows_total, n_q_heads, head_dim, pre_splits);
     const PartBuffers own = part_buffers(ws + part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits),
                                          n_rows_total, n_q_heads, head_dim, own_splits);
+    const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
+                                        n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
+                                        page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
+                                        status, stream);
+    if (rc != TF_OK) return rc;
+
     if (n_prefixes > 0 && pre_rows > 0) {
         const tf_status rc = paged_partials(true, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                             n_kv_heads, head_dim, page_table, page_table_len, prefixes, n_prefixes,
                                             prefixes_host, page_table_host, scale, pre_split, pre_splits, pre.o,
-                                            pre.m, pre.l, pre.flag, status, stream);
+                                            pre.m, pre.l, pre.flag, status, stream, true);
         if (rc != TF_OK) return rc;
     }
-    const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
-                                        n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
-                                        page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
-                                        status, stream, n_prefixes > 0 && pre_rows > 0);
-    if (rc != TF_OK) return rc;
-
     MergeSegsParams m{};
     m.own = PartSet{own.o, own.m, own.l, own.flag, own_splits, own_split};
     m.prefix = PartSet{pre.o, pre.m, pre.l, pre.flag, pre_splits, pre_split};

@@ -32,7 +32,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "api_common.h"
 #include "tf_common.cuh"
 #include "tf_internal.h"
 #include "tf_sm100.cuh"
@@ -613,8 +612,6 @@ __global__ void __launch_bounds__(WsCfg<D>::kThreads, WsCfg<D>::kMinBlocks)
             mbar_wait(smem_u32(&qfull_bar[i]), 1u, 20000000ull);
         }
     }
-    // beside another partial kernel: this grid ends after that one
-    if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -669,22 +666,6 @@ static cudaError_t launch_ws_t(const WsParams &p, const void *k, const void *v, 
     if (const uint64_t runout = test_wait_runout_ns()) {
         q.test_idle = 1;
         q.wait_ns = runout;
-    }
-    if (p.beside) {
-        // (the SM's shared memory has to be split as it is for the kernel already there)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)n_items_bound);
-        cfg.blockDim = dim3(WsCfg<D>::kThreads);
-        cfg.dynamicSmemBytes = WsCfg<D>::kSmem;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, kern, mk, mv, q);
     }
     kern<<<(unsigned)grid, WsCfg<D>::kThreads, WsCfg<D>::kSmem, st>>>(mk, mv, q);
     return cudaGetLastError();

@@ -130,10 +130,6 @@ struct WsParams {
     int64_t ring_slots_total;
     // an 8-bit cache's scale bytes [pages][Hkv][P]
     const uint8_t *k_scale, *v_scale;
-    // run beside the partial kernel launched before this one (see
-    // PromptTcParams::beside), with a CTA an item: an SM holds one of these beside
-    // one of that kernel's and two once that is gone, so the hardware deals them out
-    int beside;
     // an 8-bit cache, one split a stream: the final rows instead of partials
     void *out;
     int out_bf16;
@@ -166,7 +162,7 @@ uint64_t test_wait_runout_ns();
 // Split-KV partials of tf_paged_attn_decode / tf_paged_attn_block, arguments
 // checked (csrc/api.cu).  `beside`: the launch before it on the stream is another
 // call of this function, whose outputs it neither reads nor writes; the
-// kernel may then run beside it (PromptTcParams::beside, WsParams::beside).
+// tensor-core kernel then runs beside it (PromptTcParams::beside).
 tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                          const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
                          const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
