@@ -27,6 +27,14 @@
 //    (f16 hi + f16 lo, two MMAs into one fp32 accumulator).
 //  - The references move only when a term would pass 2^8 above them, so a tile
 //    takes one vote instead of two butterfly maxima.
+// Measured (partials and merge): 16 streams of 1,024-8,192 keys, 32/8 heads, D 128
+// (123 MB) in 30 us, 4.1 TB/s, 28 of them this kernel; D 256 32 us, D 64 39 us for
+// as many bytes (a key there has a quarter of the time; four CTAs an SM, where
+// three took 45 us); one stream of 32,000 keys 20 us; two streams of 37 and 70
+// keys, written directly, 6.5 us (8.3 with a merge).  What is left over the bytes'
+// 19 us is some 5 us of start-up (table, page ids, first tiles, one after
+// another) and the merge.  Tried and not kept: four CTAs an SM at D 128 with two
+// stages each (36 us), one with three stages at D 256 (43 us).
 #include <atomic>
 #include <cfloat>
 #include <cstdint>

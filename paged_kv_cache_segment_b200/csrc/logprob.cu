@@ -16,24 +16,29 @@
 //
 // Top k: elements are ordered by a 64-bit key, the value's order-preserving image
 // above the complement of the column, so keys are distinct and ties go to the
-// lower column.  During the pass a thread keeps only its largest value.  The k-th
-// largest of 32 groups' largest values is a threshold that at least k elements
-// reach, and few others do (some 32 ln(32 / (32 - k)) of random rows): only the
-// threads whose own maximum reaches it have their columns read again, from L2,
-// and the elements that reach it go to a list that is ranked by counting.  A list
-// that overflows means ties (a mask of the type's lowest value): then the
-// elements above the threshold are listed, and the columns equal to it in order
-// until there are k.  If even the former overflow (columns left to a few threads
-// only) the k largest keys are taken one at a time: slow, but never wrong.
+// lower column.  During the pass a thread keeps only its largest value (and which
+// chunk it came from, and the largest of its other chunks).  The k-th largest of
+// some groups' largest values is a threshold that at least k elements reach, and
+// few others do: only the chunks that reach it, nearly always one a thread, are
+// read again, from L2, and the elements that reach it go to a list that is ranked
+// by counting.  A list that overflows means ties (a mask of the type's lowest
+// value, a row of equal logits): then the elements above the threshold are listed,
+// and the columns equal to it in order until there are k.  If even the former
+// overflow (columns left to a few threads only) the k largest keys are taken one
+// at a time: slow, but never wrong.
 //
-// What follows a row's pass is latency: a threshold, a second look at L2, a
-// ranking, some 4 us for one warp or for many.  So one warp does it, beside the
-// streaming ones:
-//  - CTA mode: NT streaming threads leave their statistics in shared memory and
-//    go on to the next row while a finishing warp works on the last one (two
-//    buffers, four named barriers).  Persistent, four CTAs of 224 + 32 threads an
-//    SM; with few rows, 480 + 32 threads and a cluster of up to eight CTAs a row.
-//  - warp mode, for short rows: every warp streams and finishes rows of its own.
+// The logits are read once, so HBM bounds many rows; few rows, and the end of
+// every row (a threshold, a second look, a ranking: 3-4 us), are latency.
+//  - CTA mode: a CTA a row, several CTAs an SM so that one's row end hides behind
+//    the others' streaming; with few rows 1,024 threads and a cluster of up to
+//    eight CTAs a row, whose statistics and lists meet in distributed shared memory.
+//  - warp mode, for short rows: a warp streams and ends a row of its own.
+// Measured (bf16): 1,024 rows x 128,000 columns 59 us with 5 alternatives (262 MB,
+// 4.4 TB/s), 67 with 20, 50 without; 62 rows with 20 13 us; one row of 128,000 f32
+// with 5 10.5 us; 20,000 rows x 3,000 45 us by warps, 151 by CTAs.  A persistent
+// form with a warp of each CTA for the row ends was slower (75 us): one warp is
+// slow at them.  So were five or six smaller CTAs an SM (56-60 us without
+// alternatives).
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -174,6 +179,7 @@ struct RowView {
     const T *at;
     int mis, v0, v1, n_cols;
 
+    RowView() = default;
     __device__ __forceinline__ RowView(const LogprobParams &p, int64_t row, int rank, int cl) {
         at = static_cast<const T *>(p.logits) + row * p.ld;
         n_cols = p.n_cols;
@@ -265,42 +271,62 @@ __device__ __forceinline__ float fold(Stat &st, const uint32_t (&x)[kLpBatch][4]
     return mx;
 }
 
-// Shared memory of a finishing warp.
-template <int NT, int LIST>
+// A warp appends the columns equal to `tau`, lowest first, to a list of n keys
+// until it has K; the new count.
+template <typename T>
+__device__ __forceinline__ int take_equal(const RowView<T> &w, float tau, uint64_t *list, int n, int K) {
+    using E = Elem<T>;
+    const int lane = threadIdx.x & 31;
+    for (int v = w.v0; n < K && v < w.v1; v += 32) {
+        uint32_t x[4];
+        w.vec(v + lane, x);
+        const int c0 = (v + lane) * E::kPer - w.mis;
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < E::kPer; ++e) mine += E::get(x, e) == tau ? 1 : 0;
+        int before = mine;  // equal columns in this and the lower lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
+        }
+        const int found = __shfl_sync(0xffffffffu, before, 31);
+        before -= mine;
+#pragma unroll
+        for (int e = 0; e < E::kPer; ++e)
+            if (E::get(x, e) == tau) {
+                if (n + before < K) list[n + before] = key64(tau, c0 + e);
+                ++before;
+            }
+        n = min(K, n + found);
+    }
+    return n;
+}
+
+// Shared memory of a warp that ends a row.
+template <int LIST>
 struct FinishBuf {
     uint64_t list[LIST], top[kLpMaxTop];
-    uint16_t hits[NT];
+    uint8_t hits[32];
     int n;
 };
 
-// One warp ends a row (or a CTA's share): lane's s[i] are the statistics of
-// streaming thread 32 i + lane of NT.  Returns the joined statistics; with TOP
-// the K largest keys are in b.top, largest first, 0 past the unmasked columns.
-template <typename T, bool TOP, int NT, int LIST>
-__device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT / 32], FinishBuf<NT, LIST> &b, int K,
-                                       float c) {
+// A warp ends a row of its own, `own` being the lane's statistics.  Returns the
+// joined ones; with TOP the K largest keys are in b.top, largest first, 0 past the
+// unmasked columns.
+template <typename T, bool TOP, int LIST>
+__device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, FinishBuf<LIST> &b, int K, float c) {
     using E = Elem<T>;
-    constexpr int NI = NT / 32, EPV = E::kPer;
+    constexpr int EPV = E::kPer;
     const int lane = threadIdx.x & 31;
-    float lm = s[0].m;  // the lane's largest
-#pragma unroll
-    for (int i = 1; i < NI; ++i) lm = fmaxf(lm, s[i].m);
-    float M = lm;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    Stat all{M, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        Stat y = s[i];
-        if (M != -INFINITY) y.to(M, c);
-        all.l += y.l;
-        all.t += y.t;
-    }
+    Stat all = own;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        all.l += __shfl_xor_sync(0xffffffffu, all.l, o);
-        all.t += __shfl_xor_sync(0xffffffffu, all.t, o);
+        const Stat y{__shfl_xor_sync(0xffffffffu, all.m, o), __shfl_xor_sync(0xffffffffu, all.l, o),
+                     __shfl_xor_sync(0xffffffffu, all.t, o)};
+        all = join(all, y, c);
     }
+    const float lm = own.m;  // the lane's largest
     if constexpr (TOP) {
         // ---- the threshold: the K-th largest of the lanes' largest values (equal ones rank by lane)
         int r = 0;
@@ -310,22 +336,16 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT /
             r += (y > lm || (y == lm && j < lane)) ? 1 : 0;
         }
         const float tau = __shfl_sync(0xffffffffu, lm, __ffs(__ballot_sync(0xffffffffu, r == K - 1)) - 1);
-        const int nk = (w.v1 - w.v0 + NT - 1) / NT;  // vectors a thread
-        // the streaming threads whose largest value is at least `want` (above it, if strict)
+        const int nk = (w.v1 - w.v0 + 31) / 32;  // vectors a lane
+        // the lanes whose largest value is at least `want` (above it, if strict)
         auto find = [&](float want, bool strict) -> int {
-            int n = 0;
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const float m = s[i].m;
-                const bool hit = (strict ? m > want : m >= want) && m > -INFINITY;
-                const uint32_t who = __ballot_sync(0xffffffffu, hit);
-                if (hit) b.hits[n + __popc(who & ((1u << lane) - 1u))] = (uint16_t)(32 * i + lane);
-                n += __popc(who);
-            }
+            const bool hit = (strict ? lm > want : lm >= want) && lm > -INFINITY;
+            const uint32_t who = __ballot_sync(0xffffffffu, hit);
+            if (hit) b.hits[__popc(who & ((1u << lane) - 1u))] = (uint8_t)lane;
             if (lane == 0) b.n = 0;
             __syncwarp();
-            return n;
+            return __popc(who);
         };
         // a vector's elements at least (above, if strict) `want`, to the list
         auto take = [&](const uint32_t (&x)[4], int v, float want, bool strict) {
@@ -341,7 +361,7 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT /
                 }
             }
         };
-        // the hit threads' vectors, four a lane in flight; false if the list overflows
+        // those lanes' vectors, four a lane in flight; false if the list overflows
         auto look = [&](int n_hits, float want, bool strict) -> bool {
             const int total = n_hits * nk;
             for (int base = 0; base < total; base += 4 * 32) {
@@ -350,7 +370,7 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT /
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int idx = base + 32 * k + lane, h = idx / nk;
-                    v[k] = idx < total ? w.v0 + b.hits[h] + (idx - h * nk) * NT : w.v1;
+                    v[k] = idx < total ? w.v0 + b.hits[h] + (idx - h * nk) * 32 : w.v1;
                     w.vec(v[k], x[k]);
                 }
 #pragma unroll
@@ -367,29 +387,7 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat (&s)[NT /
             // ties: what is above the threshold, then the first columns equal to it
             ok = look(find(tau, true), tau, true);
             int n = b.n;
-            for (int v = w.v0; ok && n < K && v < w.v1; v += 32) {
-                uint32_t x[4];
-                w.vec(v + lane, x);
-                const int c0 = (v + lane) * EPV - w.mis;
-                int mine = 0;
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) mine += E::get(x, e) == tau ? 1 : 0;
-                int before = mine;  // equal columns in this and the lower lanes
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, before, o);
-                    if (lane >= o) before += y;
-                }
-                const int found = __shfl_sync(0xffffffffu, before, 31);
-                before -= mine;
-#pragma unroll
-                for (int e = 0; e < EPV; ++e)
-                    if (E::get(x, e) == tau) {
-                        if (n + before < K) b.list[n + before] = key64(tau, c0 + e);
-                        ++before;
-                    }
-                n = min(K, n + found);
-            }
+            if (ok) n = take_equal(w, tau, b.list, n, K);
             __syncwarp();
             if (lane == 0 && ok) b.n = n;
             __syncwarp();
@@ -492,6 +490,87 @@ __device__ __forceinline__ void rank_top(const uint64_t *list, int n, int k, uin
     for (int i = n + threadIdx.x; i < k; i += NT) top[i] = 0ull;
 }
 
+// The K largest keys of a row's part whose list of columns that reach `tau` did not
+// hold them all: ties.  A CTA lists what is above `tau`, then the columns equal to
+// it, lowest first, until there are K; if that does not fit either it takes the keys
+// one at a time.  (Seldom called, and apart from the kernel, which is short of
+// registers: inside it the kernel spills, and rows without ties take 3% longer.)
+template <typename T, int NT>
+__device__ __noinline__ void top_of_ties(const T *at, int v0, int v1, int n_cols, float tau, uint64_t *list,
+                                         int *count, uint64_t *best_of, int K, uint64_t *top) {
+    using E = Elem<T>;
+    const int tid = threadIdx.x;
+    RowView<T> w;
+    w.at = at;
+    w.mis = (int)((reinterpret_cast<uintptr_t>(at) & 15u) / sizeof(T));
+    w.v0 = v0;
+    w.v1 = v1;
+    w.n_cols = n_cols;
+    auto all = [&](auto &&each) {  // the part's vectors, a batch at a time
+        for (int v = v0 + tid; v < v1; v += kLpBatch * NT) {
+            uint32_t x[kLpBatch][4];
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k) w.vec(v + k * NT, x[k]);
+#pragma unroll
+            for (int k = 0; k < kLpBatch; ++k) each(x[k], (v + k * NT) * E::kPer - w.mis);
+        }
+    };
+    __syncthreads();  // every thread has read the count
+    if (tid == 0) *count = 0;
+    __syncthreads();
+    if (tau > -INFINITY) {
+        all([&](const uint32_t(&x)[4], int c0) {
+            if (!(E::most(x) > tau)) return;
+#pragma unroll
+            for (int e = 0; e < E::kPer; ++e) {
+                const float y = E::get(x, e);
+                if (y > tau) {
+                    const int i = atomicAdd(count, 1);
+                    if (i < kLpList) list[i] = key64(y, c0 + e);
+                }
+            }
+        });
+        __syncthreads();
+        int n = *count;
+        if (n <= kLpList) {
+            __syncthreads();
+            if (tid < 32) {
+                n = take_equal(w, tau, list, n, K);
+                if (tid == 0) *count = n;
+            }
+            __syncthreads();
+            rank_top<NT>(list, *count, K, top);
+            return;
+        }
+    }
+    uint64_t best = 0;
+    auto look = [&](uint64_t below) {  // this thread's largest key below the last one taken
+        best = 0;
+        all([&](const uint32_t(&x)[4], int c0) {
+#pragma unroll
+            for (int e = 0; e < E::kPer; ++e) {
+                const uint64_t key = key64(E::get(x, e), c0 + e);
+                if (key < below && key > best) best = key;
+            }
+        });
+    };
+    look(~0ull);
+    for (int q = 0; q < K; ++q) {
+        uint64_t b = best;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
+            b = y > b ? y : b;
+        }
+        if ((tid & 31) == 0) best_of[tid >> 5] = b;
+        __syncthreads();
+        for (int i = 0; i < NT / 32; ++i) b = best_of[i] > b ? best_of[i] : b;
+        if (tid == 0) top[q] = b;
+        if (b != 0 && b == best) look(b);
+        __syncthreads();
+    }
+}
+
 template <typename T, bool TOP, int NT>
 __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel(const LogprobParams p) {
     using E = Elem<T>;
@@ -577,83 +656,56 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
         }
         __syncthreads();
         const float tau = s_tau;
-        // ---- the threads that reach it go over their columns again
-        // f(value, column) for the unmasked columns of a vector no smaller than `want`
-        auto each = [&](const uint32_t (&x)[4], int v, float want, auto &&f) {
-            const float most = E::most(x);
-            if (!(most >= want) || most == -INFINITY) return;
-            const int c0 = v * EPV - w.mis;
+        // ---- the threads that reach it have their columns read again
+        {
+            auto push = [&](const uint32_t (&x)[4], int v) {
+                const float most = E::most(x);
+                if (!(most >= tau) || most == -INFINITY) return;
+                const int c0 = v * EPV - w.mis;
 #pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                const float y = E::get(x, e);
-                if (y >= want && y > -INFINITY) f(y, c0 + e);
+                for (int e = 0; e < EPV; ++e) {
+                    const float y = E::get(x, e);
+                    if (y >= tau && y > -INFINITY) {
+                        const int i = atomicAdd(&s_n, 1);
+                        if (i < kLpList) s_list[i] = key64(y, c0 + e);
+                    }
+                }
+            };
+            const bool hit = mine >= tau && mine > -INFINITY, more = second >= tau;
+            // most have one chunk that reaches it: its vectors, eight threads' at a time
+            uint32_t one = __ballot_sync(0xffffffffu, hit && !more);
+            while (one) {
+                int from = -1;  // lane 4 i + k: vector k of the i-th such thread
+                for (int i = 0; i < 32 / kLpBatch && one; ++i, one &= one - 1)
+                    if (lane / kLpBatch == i) from = __ffs(one) - 1;
+                const int ch = __shfl_sync(0xffffffffu, best_ch, from < 0 ? 0 : from);
+                if (from >= 0) {
+                    const int v = w.v0 + (ch * kLpBatch + lane % kLpBatch) * NT + warp * 32 + from;
+                    uint32_t x[4];
+                    w.vec(v, x);
+                    push(x, v);
+                }
             }
-        };
-        auto push = [&](float y, int col) {
-            const int i = atomicAdd(&s_n, 1);
-            if (i < kLpList) s_list[i] = key64(y, col);
-        };
-        const bool hit = mine >= tau && mine > -INFINITY;
-        // most have one chunk that reaches it: its vectors, eight threads' at a time
-        uint32_t one = __ballot_sync(0xffffffffu, hit && second < tau);
-        while (one) {
-            int from = -1;  // lane 4 i + k: vector k of the i-th such thread
-            for (int i = 0; i < 32 / kLpBatch && one; ++i, one &= one - 1)
-                if (lane / kLpBatch == i) from = __ffs(one) - 1;
-            const int ch = __shfl_sync(0xffffffffu, best_ch, from < 0 ? 0 : from);
-            if (from >= 0) {
-                const int v = w.v0 + (ch * kLpBatch + lane % kLpBatch) * NT + warp * 32 + from;
-                uint32_t x[4];
-                w.vec(v, x);
-                each(x, v, tau, push);
-            }
-        }
-        // the others' vectors, a vector a lane
-        for (uint32_t all = __ballot_sync(0xffffffffu, hit && !(second < tau)); all; all &= all - 1) {
-            const int first = w.v0 + warp * 32 + __ffs(all) - 1;
-            for (int v = first + lane * NT; v - lane * NT < w.v1; v += 2 * 32 * NT) {
-                uint32_t x[2][4];
-                w.vec(v, x[0]);
-                w.vec(v + 32 * NT, x[1]);
+            // the others' vectors, a vector a lane
+            for (uint32_t all = __ballot_sync(0xffffffffu, hit && more); all; all &= all - 1) {
+                const int first = w.v0 + warp * 32 + __ffs(all) - 1;
+                for (int v = first + lane * NT; v - lane * NT < w.v1; v += 2 * 32 * NT) {
+                    uint32_t x[2][4];
+                    w.vec(v, x[0]);
+                    w.vec(v + 32 * NT, x[1]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) each(x[k], v + k * 32 * NT, tau, push);
+                    for (int k = 0; k < 2; ++k) push(x[k], v + k * 32 * NT);
+                }
+                // (a list that has overflowed is of no use: stop)
+                if (*static_cast<volatile int *>(&s_n) > kLpList) break;
             }
         }
         __syncthreads();
-        if (s_n > kLpList) {
-            // one at a time: the largest key below the last one taken
-            uint64_t best = 0;
-            auto look = [&](uint64_t below) {
-                best = 0;
-                for (int v = w.v0 + tid; v < w.v1; v += kLpBatch * NT) {
-                    uint32_t x[kLpBatch][4];
-#pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k) w.vec(v + k * NT, x[k]);
-#pragma unroll
-                    for (int k = 0; k < kLpBatch; ++k)
-                        each(x[k], v + k * NT, -INFINITY, [&](float y, int col) {
-                            const uint64_t key = key64(y, col);
-                            if (key < below && key > best) best = key;
-                        });
-                }
-            };
-            look(~0ull);
-            for (int q = 0; q < K; ++q) {
-                uint64_t b = best;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    const uint64_t y = __shfl_xor_sync(0xffffffffu, b, o);
-                    b = y > b ? y : b;
-                }
-                if (lane == 0) s_best[warp] = b;
-                __syncthreads();
-                for (int i = 0; i < NW; ++i) b = s_best[i] > b ? s_best[i] : b;
-                if (tid == 0) s_top[q] = b;
-                if (b != 0 && b == best) look(b);
-                __syncthreads();
-            }
+        const int listed = s_n;
+        if (listed > kLpList) {
+            top_of_ties<T, NT>(w.at, w.v0, w.v1, w.n_cols, tau, s_list, &s_n, s_best, K, s_top);
         } else {
-            rank_top<NT>(s_list, s_n, K, s_top);
+            rank_top<NT>(s_list, listed, K, s_top);
         }
     }
     __syncthreads();
@@ -722,25 +774,25 @@ constexpr int kLpWarpList = 256;
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const LogprobParams p) {
-    __shared__ FinishBuf<32, TOP ? kLpWarpList : 1> s_fin[kLpWarpRows];
+    __shared__ FinishBuf<TOP ? kLpWarpList : 1> s_fin[kLpWarpRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float c = p.scale * kLog2e;
     const int64_t row = (int64_t)blockIdx.x * kLpWarpRows + warp;
     if (row >= p.n_rows) return;
     const RowView<T> w(p, row, 0, 1);
-    Stat s[1] = {{-INFINITY, 0.f, 0.f}};
+    Stat st{-INFINITY, 0.f, 0.f};
     uint32_t a[kLpBatch][4], b[kLpBatch][4];
     const int n_chunks = w.chunks(32);
     w.chunk(0, lane, 32, a);
     for (int ch = 0; ch < n_chunks; ch += 2) {
         if (ch + 1 < n_chunks) w.chunk(ch + 1, lane, 32, b);
-        fold<T>(s[0], a, c);
+        fold<T>(st, a, c);
         if (ch + 1 < n_chunks) {
             if (ch + 2 < n_chunks) w.chunk(ch + 2, lane, 32, a);
-            fold<T>(s[0], b, c);
+            fold<T>(st, b, c);
         }
     }
-    const Stat all = finish<T, TOP>(w, s, s_fin[warp], p.top_k, c);
+    const Stat all = finish<T, TOP>(w, st, s_fin[warp], p.top_k, c);
     write_row<T, TOP>(p, row, all, s_fin[warp].top);
 }
 
@@ -764,17 +816,19 @@ template <typename T, bool TOP>
 cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     const int sms = device_sms();
     const int chunk = Elem<T>::kPer * kLpBatch;  // columns a thread holds
-    // short rows (up to four chunks of a warp): a warp a row
+    // short rows (up to four chunks of a warp): a warp a row (60,000 rows x 1,000 with 5: 77 us; 356 by CTAs of 64)
     if (p.n_cols <= 4 * 32 * chunk && p.n_rows > 4 * sms) {
         const int64_t grid = ((int64_t)p.n_rows + kLpWarpRows - 1) / kLpWarpRows;
         logprob_warp_kernel<T, TOP><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
         return cudaGetLastError();
     }
-    // many rows: eight or four CTAs an SM
+    // many rows: eight CTAs an SM where a row is short (4,000 rows x 32,000 with 20: 93 us, 106 by four), else four
+    // (1,024 x 128,000 with 5: 64 us, 68 by eight)
     if (p.n_rows > 4 * sms && p.n_cols <= 2 * 1024 * chunk) return launch_cta<T, TOP, 128>(p, 1, st);
     if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_cta<T, TOP, 256>(p, 1, st);
     if (p.n_rows > sms) return launch_cta<T, TOP, 512>(p, 1, st);
-    // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads
+    // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads (62 rows x 128,000 with
+    // 20: 13 us; 15 by clusters of four CTAs of 512, two an SM)
     int cl = 1;
     while (cl < kLpMaxCluster && p.n_rows * 2 * cl <= sms && cl * 1024 * chunk < p.n_cols) cl *= 2;
     return launch_cta<T, TOP, 1024>(p, cl, st);
