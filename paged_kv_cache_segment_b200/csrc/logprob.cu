@@ -28,14 +28,14 @@
 // at a time: slow, but never wrong.
 //
 // The logits are read once, so HBM bounds many rows; few rows, and the end of
-// every row (a threshold, a second look, a ranking: 3-4 us), are latency.
+// every row (a threshold, a second look, a ranking: 3 us), are latency.
 //  - CTA mode: a CTA a row, several CTAs an SM so that one's row end hides behind
 //    the others' streaming; with few rows 1,024 threads and a cluster of up to
 //    eight CTAs a row, whose statistics and lists meet in distributed shared memory.
 //  - warp mode, for short rows: a warp streams and ends a row of its own.
 // Measured (bf16): 1,024 rows x 128,000 columns 59 us with 5 alternatives (262 MB,
-// 4.4 TB/s), 67 with 20, 50 without; 62 rows with 20 13 us; one row of 128,000 f32
-// with 5 10.5 us; 20,000 rows x 3,000 45 us by warps, 151 by CTAs.  A persistent
+// 4.4 TB/s), 67 with 20, 50 without; 62 rows with 20 12 us; one row of 128,000 f32
+// with 5 8.6 us; 20,000 rows x 3,000 45 us by warps, 151 by CTAs.  A persistent
 // form with a warp of each CTA for the row ends was slower (75 us): one warp is
 // slow at them.  So were five or six smaller CTAs an SM (56-60 us without
 // alternatives).
@@ -440,9 +440,28 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, Fin
     return all;
 }
 
+// A row's first 32 given tokens and their logits, a lane each, fetched while the
+// row is read: after it the two loads, one behind the other, were a call's tail
+// (one row of 128,000 f32 with 5: 8.6 us; 10.5 before this and the join of a
+// cluster's lists by a thread a (key, list)).
+struct GivenToken {
+    int tok = -1;
+    float x = 0.f;
+
+    __device__ __forceinline__ void ask(const LogprobParams &p, int64_t row, bool here) {
+        const int lane = threadIdx.x & 31;
+        if (here && lane < p.n_tokens) tok = __ldg(p.tokens + row * p.n_tokens + lane);
+    }
+    template <typename T>
+    __device__ __forceinline__ void fetch(const LogprobParams &p, const T *at) {
+        if (tok >= 0 && tok < p.n_cols) x = Elem<T>::load(at + tok);
+    }
+};
+
 // One warp writes a row's outputs.
 template <typename T, bool TOP>
-__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const Stat &all, const uint64_t *top) {
+__device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, const Stat &all, const uint64_t *top,
+                                          const GivenToken &given) {
     const int lane = threadIdx.x & 31, K = p.top_k;
     const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
     const float nan = __int_as_float(0x7fc00000);
@@ -455,12 +474,16 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, c
     const T *at = static_cast<const T *>(p.logits) + row * p.ld;
     for (int i = lane; i < p.n_tokens; i += 32) {
         const int64_t to = row * p.n_tokens + i;
-        const int tok = p.tokens[to];
+        GivenToken g = given;
+        if (i >= 32) {
+            g.tok = p.tokens[to];
+            g.fetch(p, at);
+        }
         float lp = nan;
-        if (tok < 0 || tok >= p.n_cols)
+        if (g.tok < 0 || g.tok >= p.n_cols)
             atomicOr(p.status, TF_DEV_BAD_TOKEN);
         else if (!bad)
-            lp = (Elem<T>::load(at + tok) - all.m) * p.scale - log_l;
+            lp = (g.x - all.m) * p.scale - log_l;
         p.token_logprobs[to] = lp;
     }
     if constexpr (TOP) {
@@ -597,6 +620,8 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
     Stat st{-INFINITY, 0.f, 0.f};
     uint32_t cur[kLpBatch][4];
     w.chunk(0, tid, NT, cur);
+    GivenToken given;
+    given.ask(p, row, rank == 0 && warp == 0);
     if constexpr (TOP) {
         if (tid == 0) s_n = 0;
     }
@@ -620,6 +645,7 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
         }
     }
 
+    given.fetch(p, w.at);
     // ---- the CTA's statistics
     {
         Stat all = st;
@@ -738,25 +764,24 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
         }
         if constexpr (TOP) {
             // a key's rank: its place in its own sorted list and, in each of the
-            // others, how many are larger; empty places (0) come last
-            for (int i = tid; i < CL * K; i += NT) {
-                const uint64_t mine = x_top[i];
-                int r = i % K;
-                for (int a = 0; a < CL; ++a) {
-                    if (a == i / K) continue;
-                    const uint64_t *list = x_top + a * K;
-                    int lo = 0, hi = K;  // list[0 .. lo) before mine
-                    while (lo < hi) {
-                        const int mid = (lo + hi) >> 1;
-                        // equal only when both are empty: by list, so that every place is taken once
-                        if (list[mid] > mine || (list[mid] == mine && a < i / K))
-                            lo = mid + 1;
-                        else
-                            hi = mid;
-                    }
-                    r += lo;
+            // others, how many are larger, a thread a list (CL is a power of two);
+            // empty places (0) come last
+            for (int i = tid; i < ((CL * K * CL + 31) & ~31); i += NT) {
+                const int a = i % CL, key = min(i / CL, CL * K - 1), own = key / K;
+                const uint64_t mine = x_top[key];
+                const uint64_t *list = x_top + a * K;
+                int lo = 0, hi = K;  // list[0 .. lo) before mine
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    // equal only when both are empty: by list, so that every place is taken once
+                    if (list[mid] > mine || (list[mid] == mine && a < own))
+                        lo = mid + 1;
+                    else
+                        hi = mid;
                 }
-                if (r < K) s_top[r] = mine;
+                int r = a == own ? key % K : lo;
+                for (int o = 1; o < CL; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+                if (a == 0 && i < CL * K * CL && r < K) s_top[r] = mine;
             }
             __syncthreads();
         }
@@ -765,7 +790,7 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
     if (warp != 0) return;
     all.m = __shfl_sync(0xffffffffu, all.m, 0);
     all.l = __shfl_sync(0xffffffffu, all.l, 0);
-    write_row<T, TOP>(p, row, all, s_top);
+    write_row<T, TOP>(p, row, all, s_top, given);
 }
 
 // ---- warp mode: a warp a row
@@ -784,6 +809,8 @@ __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const
     uint32_t a[kLpBatch][4], b[kLpBatch][4];
     const int n_chunks = w.chunks(32);
     w.chunk(0, lane, 32, a);
+    GivenToken given;
+    given.ask(p, row, true);
     for (int ch = 0; ch < n_chunks; ch += 2) {
         if (ch + 1 < n_chunks) w.chunk(ch + 1, lane, 32, b);
         fold<T>(st, a, c);
@@ -792,8 +819,9 @@ __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const
             fold<T>(st, b, c);
         }
     }
+    given.fetch(p, w.at);
     const Stat all = finish<T, TOP>(w, st, s_fin[warp], p.top_k, c);
-    write_row<T, TOP>(p, row, all, s_fin[warp].top);
+    write_row<T, TOP>(p, row, all, s_fin[warp].top, given);
 }
 
 template <typename T, bool TOP, int NT>
@@ -828,7 +856,7 @@ cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_cta<T, TOP, 256>(p, 1, st);
     if (p.n_rows > sms) return launch_cta<T, TOP, 512>(p, 1, st);
     // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads (62 rows x 128,000 with
-    // 20: 13 us; 15 by clusters of four CTAs of 512, two an SM)
+    // 20: 12 us; two more by clusters of four CTAs of 512, two an SM)
     int cl = 1;
     while (cl < kLpMaxCluster && p.n_rows * 2 * cl <= sms && cl * 1024 * chunk < p.n_cols) cl *= 2;
     return launch_cta<T, TOP, 1024>(p, cl, st);
