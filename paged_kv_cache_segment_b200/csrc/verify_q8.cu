@@ -24,12 +24,18 @@
 //
 // Measured: 8 streams of 1-16 rows over 2,048-16,384 keys, 16/2 heads, D 256, int8
 // (87 MB) in 47 us for bf16 output, 51 for f32; the kernel 45 us of it: 5 us until
-// the first tile's scores, 1.5 us a tile, 3.5 us of epilogue.  A tile's MMAs take
-// some 1,500 cycles at D 256 (QK at N = 64 runs at half rate), 2,000 with W V
-// twice, and shared memory about as much: 33 KB of codes in, out and back as 64 KB
-// of f16, read once or twice by the MMAs.  Four converter warps took 64 us where
-// eight take 51; sixteen softmax warps instead of eight changed nothing, and
-// neither did moving registers from the converters to them.
+// the first tile's scores, then 19 tiles a CTA, 3.5 us of epilogue.  A tile takes
+// some 2,600 cycles, and no unit is busy that long: its MMAs take 1,500 (QK at N =
+// 64 runs at half rate; 2,000 with W V twice), shared memory as much (33 KB of codes
+// in, out and back as 64 KB of f16, read by the MMAs).  It is a chain: 1,900 cycles
+// from a tile's scores to its weights, then W V, then the scores that take the
+// weights' place in tensor memory (at D 256 there is no room for a third buffer).
+// Without the converters' work it would take 43 us, without the exponentials 47,
+// with half of the MMAs 45.  Four converter warps took 64 us where eight take 51;
+// slower or no faster: four converter warps for K and four for V (53), fetching the
+// next codes before converting the last (47), sixteen softmax warps, registers moved
+// to them from the converters, one poll of the MMA warp for all three barriers
+// (46 for bf16 output but 53 for f32).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
