@@ -1,4 +1,5 @@
-// api_common.h - argument checks shared by the extern "C" entry points.
+// api_common.h - argument checks, split sizes and workspace layouts shared by the
+// extern "C" entry points.
 #pragma once
 
 #include <cstdint>
@@ -88,7 +89,6 @@ inline bool q8_pointers(const tf_q8_cache &c) { return c.k_codes && c.v_codes &&
 inline bool q8_aligned(const tf_q8_cache &c) {
     return aligned16(c.k_codes) && aligned16(c.v_codes) && aligned16(c.k_scale) && aligned16(c.v_scale);
 }
-
 
 // SMs of the current device.
 inline int device_sms() {

@@ -18,14 +18,37 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <utility>
-#include <vector>
+#include <memory>
+#include <new>
 #include <cuda_runtime.h>
 
 #include "api_common.h"
 #include "tf_internal.h"
 
 using namespace tfp;
+
+namespace {
+
+// Whether two entries name one row.  (No exception may leave a C entry: without
+// memory for the sort every pair is compared.)
+bool rows_overlap(const tf_seg *host, int n) {
+    std::unique_ptr<int64_t[]> runs(new (std::nothrow) int64_t[n]);  // first row, row count
+    int m = 0;
+    for (int a = 0; a < n; ++a) {
+        if (host[a].n_rows == 0) continue;
+        if (runs) runs[m++] = ((int64_t)host[a].q_row << 32) | host[a].n_rows;
+        for (int b = runs ? n : 0; b < a; ++b)
+            if (host[a].q_row < host[b].q_row + host[b].n_rows && host[b].q_row < host[a].q_row + host[a].n_rows &&
+                host[b].n_rows > 0)
+                return true;
+    }
+    std::sort(runs.get(), runs.get() + m);
+    for (int a = 1; a < m; ++a)
+        if ((runs[a] >> 32) < (runs[a - 1] >> 32) + (runs[a - 1] & 0x7fffffff)) return true;
+    return false;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -87,15 +110,7 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         const tf_status rc = plan(prefixes_host, n_prefixes, true, pre_rows, pre_splits, pre_split);
         if (rc != TF_OK) return rc;
         // a row belongs to one prefix
-        if (n_prefixes > 1) {
-            std::vector<std::pair<int, int>> runs;  // [first row, past the last)
-            for (int a = 0; a < n_prefixes; ++a)
-                if (prefixes_host[a].n_rows > 0)
-                    runs.emplace_back(prefixes_host[a].q_row, prefixes_host[a].q_row + prefixes_host[a].n_rows);
-            std::sort(runs.begin(), runs.end());
-            for (size_t a = 1; a < runs.size(); ++a)
-                if (runs[a].first < runs[a - 1].second) return TF_ERR_ARG;
-        }
+        if (n_prefixes > 1 && rows_overlap(prefixes_host, n_prefixes)) return TF_ERR_ARG;
     }
     if (max_rows == 0) return TF_OK;
     // what either partial launch would refuse, before the first one

@@ -60,6 +60,15 @@ struct Arg {
     }
 };
 
+int32_t len32(int64_t n);
+void must(bool ok, const char *what);
+
+// Entries of a segment table.
+int32_t entries(const Arg &a, const char *what) {
+    must(a.n() % 5 == 0, what);
+    return len32(a.n() / 5);
+}
+
 void must(bool ok, const char *what) {
     if (ok) return;
     PyErr_SetString(PyExc_ValueError, what);
@@ -182,7 +191,7 @@ PyObject *kv_append(PyObject *, Args a, Py_ssize_t n) {
         const Arg pt(a[3], "page_table", kI32, dev), sg(a[4], "segs", kI32, dev), st(a[5], "status", kStatus, dev);
         const Table sh(a[6], "segs_host", sg.n()), ph(a[7], "page_table_host", pt.n());
         return tf_kv_append_q8(k.p, v.p, len32(k.dim(0)), c, (const int32_t *)pt.p, len32(pt.n()),
-                               (const tf_seg *)sg.p, len32(sg.n() / 5), (const tf_seg *)sh.p, ph.p, (uint32_t *)st.p,
+                               (const tf_seg *)sg.p, entries(sg, "segs must hold five numbers an entry"), (const tf_seg *)sh.p, ph.p, (uint32_t *)st.p,
                                stream_of(a[8], dev));
     });
 }
@@ -201,7 +210,7 @@ PyObject *kv_read(PyObject *, Args a, Py_ssize_t n) {
         must(dt.n() == pt.n(), "page_table and dst_page_table differ in length");
         const Table sh(a[7], "segs_host", sg.n()), ph(a[8], "page_table_host", pt.n()),
             dh(a[9], "dst_page_table_host", dt.n());
-        return tf_kv_read_q8(c, (const int32_t *)pt.p, len32(pt.n()), (const tf_seg *)sg.p, len32(sg.n() / 5),
+        return tf_kv_read_q8(c, (const int32_t *)pt.p, len32(pt.n()), (const tf_seg *)sg.p, entries(sg, "segs must hold five numbers an entry"),
                              (const tf_seg *)sh.p, ph.p, k.p, v.p, len32(k.dim(0)), (const int32_t *)dt.p, dh.p,
                              (uint32_t *)st.p, stream_of(a[10], dev));
     });
@@ -223,7 +232,7 @@ PyObject *attn_q8(PyObject *, Args a, Py_ssize_t n) {
         const int full = PyObject_IsTrue(a[5]);
         if (full < 0) throw Raised{};
         return tf_paged_attn_q8(q.p, len32(q.dim(0)), len32(q.dim(1)), c, (const int32_t *)pt.p, len32(pt.n()),
-                                (const tf_seg *)sg.p, len32(sg.n() / 5), (const tf_seg *)sh.p, ph.p, f32(a[4]), full,
+                                (const tf_seg *)sg.p, entries(sg, "segs must hold five numbers an entry"), (const tf_seg *)sh.p, ph.p, f32(a[4]), full,
                                 i32(a[6]), i32(a[7]), ws.p, (size_t)ws.n(), out.p, out_type(out), (uint8_t *)fl.p,
                                 (uint32_t *)st.p, stream_of(a[14], dev));
     });
@@ -245,8 +254,8 @@ PyObject *attn_shared(PyObject *, Args a, Py_ssize_t n) {
             ph(a[16], "page_table_host", pt.n());
         return tf_paged_attn_shared(q.p, len32(q.dim(0)), len32(q.dim(1)), k.p, v.p, len32(k.dim(0)), len32(k.dim(2)),
                                     len32(k.dim(1)), len32(k.dim(3)), (const int32_t *)pt.p, len32(pt.n()),
-                                    (const tf_seg *)pre.p, len32(pre.n() / 5), (const tf_seg *)xh.p,
-                                    (const tf_seg *)sg.p, len32(sg.n() / 5), (const tf_seg *)sh.p, ph.p, f32(a[6]),
+                                    (const tf_seg *)pre.p, entries(pre, "prefixes must hold five numbers an entry"), (const tf_seg *)xh.p,
+                                    (const tf_seg *)sg.p, entries(sg, "segs must hold five numbers an entry"), (const tf_seg *)sh.p, ph.p, f32(a[6]),
                                     i32(a[7]), i32(a[8]), i32(a[9]), ws.p, (size_t)ws.n(), out.p, out_type(out),
                                     (uint8_t *)fl.p, (uint32_t *)st.p, stream_of(a[17], dev));
     });

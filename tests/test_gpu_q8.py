@@ -424,6 +424,8 @@ def test_shapes_and_devices_the_binding_refuses():
         tf.tf_kv_append_q8(k, k, c, pt, sg, status=st, segs_host=b.segs[:1])
     with pytest.raises(ValueError, match="CUDA device"):
         tf.tf_kv_append_q8(k, k.cpu(), c, pt, sg, status=st)
+    with pytest.raises(ValueError, match="five numbers"):
+        tf.tf_kv_append_q8(k, k, c, pt, sg.reshape(-1)[:9].contiguous(), status=st)
     out, fl = torch.zeros((2, 8, 64), device=DEV), torch.zeros((2, 8), dtype=torch.uint8, device=DEV)
     ws = torch.zeros(tf.tf_paged_attn_q8_workspace_bytes(2, 8, 64, 2), dtype=torch.uint8, device=DEV)
     kw = dict(scale=0.125, n_splits_max=2, workspace=ws, status=st)

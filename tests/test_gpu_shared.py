@@ -55,9 +55,9 @@ def shared(b, prefixes, segs, *, split=0, n_pre=16, n_own=16, host=True, out_dty
     tf.tf_paged_attn_shared(dev(b.q), dev(b.k_pool).view(torch.bfloat16), dev(b.v_pool).view(torch.bfloat16),
                             dev(b.page_table), dev(prefixes.reshape(-1, 5)), dev(segs), scale=b.scale,
                             split_keys=split, n_prefix_splits=n_pre, n_splits_max=n_own, workspace=ws, out=out,
-                            flags=flags, status=st, prefixes_host=prefixes if host else None,
-                            segs_host=segs if host else None,
-                            page_table_host=b.page_table if host and pages_host else None, stream=stream)
+                            flags=flags, status=st, prefixes_host=prefixes if host in (True, "prefixes") else None,
+                            segs_host=segs if host in (True, "segs") else None,
+                            page_table_host=b.page_table if host is True and pages_host else None, stream=stream)
     return out.float().cpu().numpy(), flags.cpu().numpy(), int(st.item())
 
 
@@ -83,6 +83,17 @@ def test_matches_float64_over_both_key_lists(case):
         out, flags, st = shared(b, prefixes, segs, split=split, n_pre=n_pre, n_own=n_own, host=host, out_dtype=dt)
         assert st == 0
         sv.check_attention(out, flags, ref, fl, vmax, dt == torch.bfloat16, f"{split} {host} {dt}")
+
+
+@pytest.mark.parametrize("host", ["prefixes", "segs"])
+@pytest.mark.parametrize("case", [1, 2, 3, 4])
+def test_one_host_table_without_the_other(case, host):
+    pre, groups, rows, keys, hq, hkv, d, psz = CASES[case]
+    b, prefixes, segs = batch(200 + case, pre, groups, rows, keys, hq, hkv, d, psz)
+    ref, fl, vmax = reference(b, prefixes, segs, groups)
+    out, flags, st = shared(b, prefixes, segs, n_pre=5, n_own=3, host=host)
+    assert st == 0
+    sv.check_attention(out, flags, ref, fl, vmax, False)
 
 
 def test_equals_one_paged_call_over_the_joined_pages():

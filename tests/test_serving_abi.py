@@ -151,6 +151,15 @@ def test_shared_prefix_checks():
     assert shared(d=96) == 4 and shared(psz=24) == 4 and shared(k=ODD) == 6
 
 
+def test_prefixes_in_any_order_must_not_share_a_row():
+    none = SEGS.copy()
+    none[:, 1] = 0  # no stream has rows: a table that is taken launches nothing
+    for runs, want in (([(3, 2), (0, 3), (5, 1)], 0), ([(3, 2), (0, 4), (5, 1)], 1), ([(0, 6), (2, 0)], 0),
+                       ([(5, 1), (2, 2), (0, 6)], 1), ([(4, 1), (4, 1)], 1), ([(0, 0), (0, 0)], 0)):
+        pre = np.array([[q, r, 40, 0, 3] for q, r in runs], np.int32)
+        assert shared(rows=6, pre_host=host(pre), n_pre=len(runs), segs_host=host(none)) == want, runs
+
+
 def test_logprob_checks():
     assert logprob(rows=0) == 0
     assert logprob(rows=-1) == 1 and logprob(cols=0) == 1 and logprob(ld=99) == 1 and logprob(dt=2) == 1
