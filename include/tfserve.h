@@ -80,7 +80,9 @@ typedef struct {
  * for bit; an element is off by at most 2^-4 of itself (e4m3, above 2^(k-6)) or
  * by 2^(k-1) (int8).  A row holding a NaN or an infinity is stored as codes 0
  * and scale byte 255.  (A magnitude that rounds to 2^128 reads as infinity.)
- * Streams must not share the slots they write.
+ * Streams must not share the slots they write.  As a host table sizes the launch,
+ * an entry on the device with more rows than any of its is reported
+ * (TF_DEV_BAD_SEG) and skipped, here and in tf_kv_read_q8.
  */
 TFS_API tf_status tf_kv_append_q8(const void *k_rows, const void *v_rows, int32_t n_rows_total,
                                   const tf_q8_cache *cache_host, const int32_t *page_table, int32_t page_table_len,
@@ -125,8 +127,9 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  * The host table sizes the launch: its row counts and its longest stream's
  * partials.  A call that is captured and replayed over a changing device table
  * is given a host table with the most rows and keys the replays will see; a
- * replay whose stream asks for more partials reports TF_DEV_SPLITS and flags the
- * stream's rows.  Without one the launch is sized for n_splits_max partials of
+ * replay whose stream asks for more partials reports TF_DEV_SPLITS, one whose
+ * stream has more rows than the launch holds TF_DEV_BAD_SEG, and those of the
+ * stream's rows that the launch holds are flagged.  Without one the launch is sized for n_splits_max partials of
  * every stream, and decode rows do not take the kernel made for them: slower.
  *
  *  workspace   device scratch of at least tf_paged_attn_q8_workspace_bytes(...)

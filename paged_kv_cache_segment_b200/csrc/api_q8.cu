@@ -163,10 +163,9 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     if (ws && splits == 1) return TF_OK;
 
     MergeSegsParams m{};
-    m.own = PartSet{b.o, b.m, b.l, b.flag, splits, split};
+    m.own = PartSet{b.o, b.m, b.l, b.flag, splits, split, max_rows};
     m.segs = segs;
     m.n_segs = n_segs;
-    m.max_rows = max_rows;
     m.n_rows_total = n_rows_total;
     m.hq = n_q_heads;
     m.log2_page = lp;

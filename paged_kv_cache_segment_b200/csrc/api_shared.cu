@@ -135,13 +135,12 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         if (rc != TF_OK) return rc;
     }
     MergeSegsParams m{};
-    m.own = PartSet{own.o, own.m, own.l, own.flag, own_splits, own_split};
-    m.prefix = PartSet{pre.o, pre.m, pre.l, pre.flag, pre_splits, pre_split};
+    m.own = PartSet{own.o, own.m, own.l, own.flag, own_splits, own_split, max_rows};
+    m.prefix = PartSet{pre.o, pre.m, pre.l, pre.flag, pre_splits, pre_split, pre_rows};
     m.segs = segs;
     m.prefixes = prefixes;
     m.n_segs = n_segs;
     m.n_prefixes = n_prefixes;
-    m.max_rows = max_rows;
     m.n_rows_total = n_rows_total;
     m.hq = n_q_heads;
     m.log2_page = lp;

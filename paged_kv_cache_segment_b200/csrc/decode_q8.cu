@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                     const int lo = max(e.q_row, 0);
                     const int64_t hi = min((int64_t)e.q_row + e.n_rows, (int64_t)p.n_rows_total);
                     if (hi > lo) flag_rows(lo, (int)(hi - lo), 0, p.hq, lane, 32);
+                    // (more rows than the launch holds: with partials the merge reports it)
+                    if (lane == 0 && (int64_t)e.n_rows * p.group > kWsQ) atomicOr(p.status, TF_DEV_BAD_SEG);
                 }
         }
         cp_async_commit();

@@ -38,7 +38,7 @@ struct KvQ8Params {
     uint8_t *k_codes, *v_codes;       // u8 [n_pages][hkv][P][D]
     uint8_t *k_scale, *v_scale;       // u8 [n_pages][hkv][P]
     uint16_t *k_pool, *v_pool;        // read: bf16 [n_pages_dst][hkv][P][D]
-    int n_rows_total, hkv, n_pages, n_pages_dst, log2_page, pt_len;
+    int n_rows_total, max_rows, hkv, n_pages, n_pages_dst, log2_page, pt_len;  // max_rows: that the grid holds
     const int32_t *page_table, *dst_page_table;
     const tf_seg *segs;
     uint32_t *status;
@@ -48,7 +48,7 @@ struct KvQ8Params {
 __device__ __forceinline__ bool kv_q8_seg(const KvQ8Params &p, bool rows_used, tf_seg &e) {
     e = p.segs[blockIdx.y];
     uint32_t bit = 0;
-    if ((rows_used && (e.q_row < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total)) || e.n_rows < 0 ||
+    if ((rows_used && (e.q_row < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total)) || e.n_rows < 0 || e.n_rows > p.max_rows ||
         e.n_keys < e.n_rows || e.pt_base < 0 || e.n_pages < 0 || (int64_t)e.pt_base + e.n_pages > p.pt_len)
         bit = TF_DEV_BAD_SEG;
     else if ((int64_t)e.n_keys > ((int64_t)e.n_pages << p.log2_page))
@@ -250,6 +250,7 @@ tf_status tf_kv_append_q8(const void *k_rows, const void *v_rows, int32_t n_rows
     p.k_rows = static_cast<const uint16_t *>(k_rows);
     p.v_rows = static_cast<const uint16_t *>(v_rows);
     p.n_rows_total = n_rows_total;
+    p.max_rows = max_rows;
     p.pt_len = page_table_len;
     p.page_table = page_table;
     p.segs = segs;
@@ -291,6 +292,7 @@ tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *page_table
     p.k_pool = static_cast<uint16_t *>(k_pool);
     p.v_pool = static_cast<uint16_t *>(v_pool);
     p.n_pages_dst = n_pages_dst;
+    p.max_rows = (int)max_rows;
     p.pt_len = page_table_len;
     p.page_table = page_table;
     p.dst_page_table = dst_page_table;

@@ -27,8 +27,13 @@
 namespace tfp {
 namespace {
 
-// Partials an entry's rows have (0: a bad entry or no keys).
+// Partials an entry's rows have (0: a bad entry, no keys, or more rows than the
+// partials' launch was sized for, which only this kernel reports).
 __device__ __forceinline__ int seg_parts(const tf_seg &e, const PartSet &s, const MergeSegsParams &p, bool full) {
+    if (e.n_rows > s.max_rows) {
+        atomicOr(p.status, TF_DEV_BAD_SEG);
+        return 0;
+    }
     const bool bad = e.q_row < 0 || e.n_rows < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total ||
                      e.n_keys < (full ? 1 : e.n_rows) || e.pt_base < 0 || e.n_pages < 0 ||
                      (int64_t)e.pt_base + e.n_pages > p.pt_len ||
@@ -208,7 +213,7 @@ template <int D, bool BF16, bool WIDE>
 cudaError_t launch_t(const MergeSegsParams &p, cudaStream_t st) {
     constexpr int units = WIDE ? 1 : (D > 128 ? 4 / (D / 128) : 4);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((int64_t)p.max_rows * p.hq + units - 1) / units), (unsigned)p.n_segs);
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.own.max_rows * p.hq + units - 1) / units), (unsigned)p.n_segs);
     cfg.blockDim = dim3(WIDE ? 256 : 128);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -229,7 +234,7 @@ cudaError_t launch_d(const MergeSegsParams &p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_merge_segs(const MergeSegsParams &p, int head_dim, cudaStream_t st) {
-    if (p.n_segs == 0 || p.max_rows == 0) return cudaSuccess;
+    if (p.n_segs == 0 || p.own.max_rows == 0) return cudaSuccess;
     switch (head_dim) {
         case 64: return launch_d<64>(p, st);
         case 128: return launch_d<128>(p, st);

@@ -172,23 +172,23 @@ tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t
 
 // Partials of one kind for the merge of tf_paged_attn_q8 and
 // tf_paged_attn_shared: arrays [n_rows_total][hq][n_splits](*D), of which a row
-// of an entry with N keys has ceil(N / len), len being the split rule's.
+// of an entry with N keys has ceil(N / len), len being the split rule's.  The
+// launch that wrote them held max_rows rows of an entry.
 struct PartSet {
     const float *o, *m, *l;
     const uint8_t *flag;
-    int n_splits, split_keys;
+    int n_splits, split_keys, max_rows;
 };
 struct MergeSegsParams {
     PartSet own, prefix;
     const tf_seg *segs, *prefixes;
     int n_segs, n_prefixes;  // n_prefixes = 0: no prefix partials
-    int max_rows;            // rows a stream has at most
     int n_rows_total, hq, log2_page, pt_len;
     int full;
     void *out;
     int out_bf16;
     uint8_t *flags;
-    const uint32_t *status;
+    uint32_t *status;
 };
 cudaError_t launch_merge_segs(const MergeSegsParams &p, int head_dim, cudaStream_t st);
 

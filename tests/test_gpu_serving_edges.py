@@ -192,3 +192,66 @@ def test_a_replay_past_its_partials_is_flagged(keys):
     assert int(st.item()) == binding.TF_DEV_SPLITS
     assert np.isnan(out[0].cpu().numpy()).all() and (fl[0] == 1).all()
     sv.check_attention(out[1:].cpu().numpy(), fl[1:].cpu().numpy(), ref[1:], rf[1:], vmax, False)
+
+
+@pytest.mark.parametrize("hq,hkv,keys", [(8, 2, [60, 20]), (8, 2, [2000, 300]), (16, 2, [900, 90]), (12, 1, [300, 40])])
+def test_a_replay_with_more_rows_than_its_launch_is_flagged(hq, hkv, keys):
+    """A host table of one or two rows a stream and nine on the device: reported, what the launch holds flagged, the
+    rest and the other stream as they were or as they should be (decode with and without a merge, the tensor-core
+    kernel, the general one)."""
+    few = [1, 1] if hq == 8 else [2, 1]
+    b, sides, c = q8_batch("int8", 11, rows=[9, 1], keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=128,
+                           page_size=32)
+    n, _, d = b.q.shape
+    held = b.segs.copy()
+    held[:, 1] = few
+    ws = torch.full((tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 64),), 255, dtype=torch.uint8, device=DEV)
+    out, fl = torch.full((n, hq, d), 5.0, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV)
+    st = status_word()
+    tf.tf_paged_attn_q8(dev(b.q), c, dev(b.page_table), dev(b.segs), scale=b.scale, n_splits_max=64, workspace=ws,
+                        out=out, flags=fl, status=st, segs_host=held)
+    ref, rf, vmax = reference(b, sides, "int8")
+    got, flags = out.cpu().numpy(), fl.cpu().numpy()
+    assert int(st.item()) == binding.TF_DEV_BAD_SEG
+    sv.check_attention(got[9:], flags[9:], ref[9:], rf[9:], vmax, False)
+    assert np.isnan(got[: few[0]]).all() and (flags[: few[0]] == 1).all()
+    rest = flags[few[0] : 9]
+    assert ((rest == 9) | (rest == 1)).all() and (got[few[0] : 9][rest == 9] == 5.0).all()
+    assert np.isnan(got[few[0] : 9][rest == 1]).all()
+
+
+def test_a_prefix_with_more_rows_than_its_launch_is_flagged():
+    b, prefixes, segs = batch(12, [300], [0] * 40, [1] * 40, [9 + i for i in range(40)], 16, 2, 128, 32)
+    few = prefixes.copy()
+    few[0, 1] = 3
+    n, hq, d = b.q.shape
+    ws = torch.full((tf.tf_paged_attn_shared_workspace_bytes(n, hq, d, 8, 8),), 255, dtype=torch.uint8, device=DEV)
+    out, fl = torch.full((n, hq, d), 5.0, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV)
+    st = status_word()
+    tf.tf_paged_attn_shared(dev(b.q), dev(b.k_pool), dev(b.v_pool), dev(b.page_table), dev(prefixes), dev(segs),
+                            scale=b.scale, n_prefix_splits=8, n_splits_max=8, workspace=ws, out=out, flags=fl,
+                            status=st, prefixes_host=few, segs_host=segs)
+    assert int(st.item()) == binding.TF_DEV_BAD_SEG
+    assert torch.isnan(out).all() and (fl == 1).all()
+
+
+@pytest.mark.parametrize("read", [False, True])
+def test_cache_rows_past_the_launch_are_reported(read):
+    b, sides, c = q8_batch("int8", 13, rows=[40, 2], keys=[50, 30], n_q_heads=2, n_kv_heads=2, head_dim=128,
+                           page_size=16)
+    held = b.segs.copy()
+    held[0, 1] = 3
+    st, pt, sg = status_word(), dev(b.page_table), dev(b.segs)
+    before = [t.view(torch.uint8).clone() for t in c.tensors]
+    if read:
+        pools = [torch.full(c.tensors[0].shape, 7.0, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+        tf.tf_kv_read_q8(c, pt, sg, *pools, pt, status=st, segs_host=held)
+        changed = [(p != 7.0).flatten(1).any(1) for p in pools]
+    else:
+        kr = torch.full((42, 2, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+        tf.tf_kv_append_q8(kr, kr, c, pt, sg, status=st, segs_host=held)
+        changed = [(t.view(torch.uint8) != o).flatten(1).any(1) for t, o in zip(c.tensors[:2], before)]
+    assert int(st.item()) == binding.TF_DEV_BAD_SEG
+    mine = set(b.page_table[b.segs[1, 3] : b.segs[1, 3] + 2].tolist())
+    for x in changed:  # the first stream is skipped, the second one's last two keys are in its second page
+        assert set(torch.nonzero(x).flatten().tolist()) == {int(b.page_table[b.segs[1, 3] + 1])} <= mine
