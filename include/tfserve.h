@@ -34,7 +34,7 @@ extern "C" {
 
 /*
  * A launch whose bounded wait gave up (TF_DEV_TIMEOUT in the status word) leaves
- * the rows of tf_paged_attn_q8 and tf_paged_attn_shared flagged NaN, as does any
+ * the rows of tf_paged_attn_q8 and tf_paged_attn_shared flagged NaN, as may any
  * later call while the caller has not cleared that bit.
  */
 

@@ -66,6 +66,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     const int lp = log2_exact(c.page_size);
     const float scale_log2 = scale * 1.4426950408889634f;
     cudaError_t e = cudaSuccess;
+    bool direct = false;  // the kernel writes the final rows
     if (ws) {
         WsParams w{};
         w.q = static_cast<const uint16_t *>(q);
@@ -94,6 +95,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
             w.out = out;
             w.out_bf16 = out_dtype == TF_OUT_BF16;
             w.out_flags = flags;
+            direct = true;
         }
         int64_t items = 0;
         for (int s = 0; s < n_segs; ++s)
@@ -126,7 +128,13 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         t.part_m = b.m;
         t.part_l = b.l;
         t.part_flag = b.flag;
+        if (splits == 1) {  // nothing to merge
+            t.out = out;
+            t.out_flags = flags;
+        }
+        t.max_rows = max_rows;
         t.status = status;
+        direct = splits == 1;
         if ((int64_t)t.n_qt * splits > 0x7fffffff || c.n_kv_heads > 65535) return TF_ERR_UNSUPPORTED;
         e = launch_verify_q8(t, c.head_dim, c.kv_type, out_dtype == TF_OUT_F32, n_segs, st);
     } else {
@@ -160,7 +168,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         e = launch_attn_partial(p, c.head_dim, false, false, grid, st);
     }
     if (e != cudaSuccess) return TF_ERR_CUDA;
-    if (ws && splits == 1) return TF_OK;
+    if (direct) return TF_OK;
 
     MergeSegsParams m{};
     m.own = PartSet{b.o, b.m, b.l, b.flag, splits, split, max_rows};

@@ -98,9 +98,13 @@ struct Q8TcParams {
     int n_rows_total, hq, hkv, group, n_pages, log2_page, pt_len;
     float scale_log2;
     int split_keys, n_splits, n_qt;  // n_qt: 128-query tiles of the longest stream's rows
+    int max_rows;                    // rows of a stream the launch holds
     int full;
     float *part_o, *part_m, *part_l;
     uint8_t *part_flag;
+    // one split a stream: the final rows (f32, or bf16 without hi-lo weights) instead of partials
+    void *out;
+    uint8_t *out_flags;
     uint32_t *status;
     int test_idle;  // the timeout test hook, as in PromptTcParams
     uint64_t wait_ns;

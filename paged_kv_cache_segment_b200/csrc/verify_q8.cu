@@ -36,6 +36,9 @@
 // next codes before converting the last (47), sixteen softmax warps, registers moved
 // to them from the converters, one poll of the MMA warp for all three barriers
 // (46 for bf16 output but 53 for f32).
+// One split a stream is written as final rows (18 streams of 10-16 rows over 20-121
+// keys, 64/8 heads, D 128: 13 us, 25 with partials and a merge; over 900-1,100 keys
+// 28 and 36 us).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -135,10 +138,24 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     const int split = (int)blockIdx.x / p.n_qt, qt = p.n_qt - 1 - (int)blockIdx.x % p.n_qt;
     const tf_seg e = p.segs[blockIdx.z];
     const int q_row = e.q_row, T = e.n_rows, N = e.n_keys, pt_base = e.pt_base, n_pg = e.n_pages;
+    // final rows of the tile flagged, when there is no merge to do it
+    auto flag_rows = [&]() {
+        const int64_t lo = max((int64_t)q_row + (int64_t)qt * RT, (int64_t)0);
+        const int64_t hi = min((int64_t)q_row + min((int64_t)T, (int64_t)(qt + 1) * RT), (int64_t)p.n_rows_total);
+        for (int64_t x = tid; x < (hi - lo) * G * D; x += kVqThreads) {
+            const int64_t r = x / (G * D), c = x - r * (G * D);  // a row's G heads lie together
+            const int64_t at = ((lo + r) * p.hq + g * G) * D + c;
+            if (HILO)
+                static_cast<float *>(p.out)[at] = __int_as_float(0x7fc00000);
+            else
+                static_cast<uint16_t *>(p.out)[at] = 0x7fc0;
+            if (c % D == 0) p.out_flags[at / D] = 1;
+        }
+    };
     {
         const bool bad = q_row < 0 || T < 0 || (int64_t)q_row + T > p.n_rows_total ||
                          N < (p.full ? (T > 0 ? 1 : 0) : T) || pt_base < 0 || n_pg < 0 ||
-                         (int64_t)pt_base + n_pg > p.pt_len;
+                         (int64_t)pt_base + n_pg > p.pt_len || T > p.max_rows;
         uint32_t bit = 0;
         if (bad)
             bit = TF_DEV_BAD_SEG;
@@ -148,6 +165,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             bit = TF_DEV_SPLITS;
         if (bit) {
             if (tid == 0) atomicOr(p.status, bit);
+            if (p.out) flag_rows();
             return;
         }
     }
@@ -638,41 +656,87 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         // 2^(r - m) in two steps: it may itself be past the floats where o is small
         const float gf = r_ref == -INFINITY ? 0.f : ex2(0.5f * (r_ref - (m_ref == -INFINITY ? 0.f : m_ref)));
         const int d0 = h * (D / 2);
-        const bool staged = rows_here * G >= 64;  // see prompt_tc.cu: many rows leave by bulk copies
-        uint32_t *stage = reinterpret_cast<uint32_t *>(base_ptr + C::kOffK) + qi * (D + 4) + d0;
-        uint32_t *gout = reinterpret_cast<uint32_t *>(p.part_o + at * D + d0);
-        const bool direct = !staged && valid_row && !aborted;
-        uint32_t obad = 0;
+        if (p.out) {
+            // ---- one split: normalise, look the row over, write it
+            const float il = 1.f / l_sum;
+            auto load = [&](int cc, float(&o)[32]) {
+                uint32_t r[32];
+                tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int w = 0; w < 32; ++w) o[w] = __uint_as_float(r[w]) * gf * gf * il;
+            };
+            uint32_t obad = 0;
 #pragma unroll 1
-        for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
-            tmem_wait_ld();
-            float o[32];
+            for (int cc = 0; cc < D / 64; ++cc) {
+                float o[32];
+                load(cc, o);
 #pragma unroll
-            for (int w = 0; w < 32; ++w) {
-                o[w] = __uint_as_float(r[w]) * gf * gf;
-                obad |= !isfinite(o[w]);
+                for (int w = 0; w < 32; ++w) obad |= !isfinite(o[w]);
             }
-            if ((staged && !aborted) || direct) {
-                float4 *d4 = reinterpret_cast<float4 *>((staged ? stage : gout) + cc * 32);
+            s_x[0][h][qi] = obad;
+            named_bar_sync(pair_bar, 64);
+            bad |= s_x[0][0][qi] | s_x[0][1][qi] | (l_sum > 0.f ? 0u : 1u);
+#pragma unroll 1
+            for (int cc = 0; cc < D / 64; ++cc) {
+                float o[32];
+                load(cc, o);
+                if (!valid_row) continue;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) d4[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                for (int w = 0; w < 32; ++w) o[w] = bad ? __int_as_float(0x7fc00000) : o[w];
+                if constexpr (HILO) {
+                    float4 *d4 = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + d0 + cc * 32);
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) d4[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                } else {
+                    uint4 *d4 = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at * D + d0 + cc * 32);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        d4[w] = bad ? make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u)
+                                    : make_uint4(pack_bf16x2(o[8 * w], o[8 * w + 1]),
+                                                 pack_bf16x2(o[8 * w + 2], o[8 * w + 3]),
+                                                 pack_bf16x2(o[8 * w + 4], o[8 * w + 5]),
+                                                 pack_bf16x2(o[8 * w + 6], o[8 * w + 7]));
+                }
             }
-        }
-        s_x[0][h][qi] = obad;
-        named_bar_sync(pair_bar, 64);
-        bad |= s_x[0][0][qi] | s_x[0][1][qi];
-        if (staged && valid_row && !aborted) {
-            fence_proxy_async_smem();
-            bulk_store(gout, smem_u32(stage), (uint32_t)(D / 2) * 4u);
-            bulk_commit();
-            sent_row = true;
-        }
-        if (valid_row && h == 0) {
-            p.part_m[at] = m_ref == -INFINITY ? -INFINITY : m_ref * kLn2;
-            p.part_l[at] = l_sum;
-            p.part_flag[at] = (uint8_t)(bad ? 1 : 0);
+            if (valid_row && h == 0) p.out_flags[at] = (uint8_t)(bad ? 1 : 0);
+        } else {
+            const bool staged = rows_here * G >= 64;  // see prompt_tc.cu: many rows leave by bulk copies
+            uint32_t *stage = reinterpret_cast<uint32_t *>(base_ptr + C::kOffK) + qi * (D + 4) + d0;
+            uint32_t *gout = reinterpret_cast<uint32_t *>(p.part_o + at * D + d0);
+            const bool direct = !staged && valid_row && !aborted;
+            uint32_t obad = 0;
+#pragma unroll 1
+            for (int cc = 0; cc < D / 64; ++cc) {
+                uint32_t r[32];
+                tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
+                tmem_wait_ld();
+                float o[32];
+#pragma unroll
+                for (int w = 0; w < 32; ++w) {
+                    o[w] = __uint_as_float(r[w]) * gf * gf;
+                    obad |= !isfinite(o[w]);
+                }
+                if ((staged && !aborted) || direct) {
+                    float4 *d4 = reinterpret_cast<float4 *>((staged ? stage : gout) + cc * 32);
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) d4[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
+                }
+            }
+            s_x[0][h][qi] = obad;
+            named_bar_sync(pair_bar, 64);
+            bad |= s_x[0][0][qi] | s_x[0][1][qi];
+            if (staged && valid_row && !aborted) {
+                fence_proxy_async_smem();
+                bulk_store(gout, smem_u32(stage), (uint32_t)(D / 2) * 4u);
+                bulk_commit();
+                sent_row = true;
+            }
+            if (valid_row && h == 0) {
+                p.part_m[at] = m_ref == -INFINITY ? -INFINITY : m_ref * kLn2;
+                p.part_l[at] = l_sum;
+                p.part_flag[at] = (uint8_t)(bad ? 1 : 0);
+            }
         }
     }
     // everyone: report a timeout, give in-flight work a bounded chance to land,

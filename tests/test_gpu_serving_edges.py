@@ -28,7 +28,8 @@ def with_hook(fn):
 
 @pytest.mark.parametrize("rows,keys,hq,hkv,d", [([1, 1], [700, 1500], 32, 8, 128),  # decode, partials and merge
                                                 ([1, 1, 1], [60, 100, 7], 8, 2, 64),  # decode, one split: no merge
-                                                ([5, 14], [900, 2100], 16, 2, 256)])  # the tensor-core kernel
+                                                ([5, 14], [900, 2100], 16, 2, 256),  # the tensor-core kernel
+                                                ([5, 20], [90, 130], 16, 2, 128)])  # the same, one split
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
 def test_q8_wait_runs_out_flags_every_row_then_recovers(rows, keys, hq, hkv, d, dt):
     b, sides, c = q8_batch("e4m3", 3, rows=rows, keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32)
@@ -168,13 +169,13 @@ def test_a_captured_step_follows_streams_that_grow(rows, split):
         sv.check_attention(out.cpu().numpy(), fl.cpu().numpy(), ref, rf, vmax, False, str(keys))
 
 
-@pytest.mark.parametrize("keys", [[100, 5], [1200, 300]])
-def test_a_replay_past_its_partials_is_flagged(keys):
+@pytest.mark.parametrize("rows,hq,keys", [([1, 1], 8, [100, 5]), ([1, 1], 8, [1200, 300]), ([20, 3], 16, [100, 30])])
+def test_a_replay_past_its_partials_is_flagged(rows, hq, keys):
     """A chosen split holds the streams it was captured with: one that outgrows its partials is reported and flagged,
     with one split (no merge) and with several."""
-    b, sides, c = q8_batch("e4m3", 10, rows=[1, 1], keys=[3000, 300], n_q_heads=8, n_kv_heads=2, head_dim=128,
+    b, sides, c = q8_batch("e4m3", 10, rows=rows, keys=[3000, 300], n_q_heads=hq, n_kv_heads=2, head_dim=128,
                            page_size=32)
-    n, hq, d = b.q.shape
+    n, _, d = b.q.shape
     ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 64), dtype=torch.uint8, device=DEV)
     out, fl, st = torch.zeros((n, hq, d), device=DEV), torch.zeros((n, hq), dtype=torch.uint8, device=DEV), status_word()
     s = b.segs.copy()
@@ -190,15 +191,17 @@ def test_a_replay_past_its_partials_is_flagged(keys):
     torch.cuda.synchronize()
     ref, rf, vmax = reference(b, sides, "e4m3", segs=s)
     assert int(st.item()) == binding.TF_DEV_SPLITS
-    assert np.isnan(out[0].cpu().numpy()).all() and (fl[0] == 1).all()
-    sv.check_attention(out[1:].cpu().numpy(), fl[1:].cpu().numpy(), ref[1:], rf[1:], vmax, False)
+    r = rows[0]
+    assert torch.isnan(out[:r]).all() and (fl[:r] == 1).all()
+    sv.check_attention(out[r:].cpu().numpy(), fl[r:].cpu().numpy(), ref[r:], rf[r:], vmax, False)
 
 
-@pytest.mark.parametrize("hq,hkv,keys", [(8, 2, [60, 20]), (8, 2, [2000, 300]), (16, 2, [900, 90]), (12, 1, [300, 40])])
+@pytest.mark.parametrize("hq,hkv,keys", [(8, 2, [60, 20]), (8, 2, [2000, 300]), (16, 2, [900, 90]), (16, 2, [100, 9]),
+                                         (12, 1, [300, 40])])
 def test_a_replay_with_more_rows_than_its_launch_is_flagged(hq, hkv, keys):
     """A host table of one or two rows a stream and nine on the device: reported, what the launch holds flagged, the
-    rest and the other stream as they were or as they should be (decode with and without a merge, the tensor-core
-    kernel, the general one)."""
+    rest and the other stream as they were or as they should be (decode and the tensor-core kernel with and
+    without a merge, the general kernel)."""
     few = [1, 1] if hq == 8 else [2, 1]
     b, sides, c = q8_batch("int8", 11, rows=[9, 1], keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=128,
                            page_size=32)
