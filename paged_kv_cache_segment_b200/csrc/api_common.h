@@ -107,6 +107,19 @@ inline int longest_keys(const tf_seg *sh, int n_segs) {
     return n;
 }
 
+// The least split worth a CTA of its own: one 64-key tile, as long as a stream has
+// at most 32 partials for the merge, and two tiles where that leaves one split and
+// the kernel needs no merge (`direct`).  8-bit, 1 stream, us: 8 rows, D 256, 512
+// keys 13.8 by tiles, 14.5 by 128, 17.6 by 256; 4,096 keys 17.4 by 64, 15.6 by 128;
+// 100 keys 13.5 by 64, 12.6 direct; one row, D 128, 600 keys 8.9, 9.1, 10.8.  (2
+// one-row streams of 353-2,000 keys behind a short prefix, 16/8 heads: 17.7 against
+// 24.2 by 256 and, for the prefix, 128; 15 streams of 2,000 behind 3 of 846 lose 1.4
+// to a wider merge.)
+inline int least_split(int longest, bool direct) {
+    if (direct && longest <= 128) return 128;
+    return longest <= 64 * 32 ? 64 : (longest + 31) / 32;
+}
+
 // A split size for kernels of one CTA an SM with a fixed cost a CTA (start-up
 // and epilogue, some eight 64-key tiles' worth): the smallest whole number of
 // tiles that leaves one wave of CTAs (streams x kv-heads x query tiles x splits)
@@ -141,8 +154,9 @@ inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows
 // after another): one wave of items when that is balanced, that is when its
 // longest item is near the slots' average load; otherwise half of that load, up
 // to `most` keys, since the items of a CTA follow one another without a new start.
-inline int decode_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t slots, int most, int n_splits_max) {
-    const int one = one_wave_split(sh, n_segs, n_kv_heads, 1 << 30, (int)slots, 256, n_splits_max);
+inline int decode_split(const tf_seg *sh, int n_segs, int n_kv_heads, int64_t slots, int most, int least,
+                        int n_splits_max) {
+    const int one = one_wave_split(sh, n_segs, n_kv_heads, 1 << 30, (int)slots, least, n_splits_max);
     int64_t tiles = 0;
     for (int s = 0; s < n_segs; ++s)
         if (sh[s].n_rows > 0) tiles += ((int64_t)sh[s].n_keys + 63) / 64 * n_kv_heads;

@@ -49,10 +49,11 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
              (split == 0 || split % std::min(c.page_size, 64) == 0);
         // (64 streams of 256-4,096 keys take 70 us in one split each, 57 us in splits of 1,280 keys; 16 of
         // 1,024-8,192 take 29.8 us in one wave of 1,152, 35 in splits of 768)
+        const int least = least_split(longest_keys(segs_host, n_segs), true);
         if (split == 0)
             split = ws ? decode_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 1280,
-                                      n_splits_max)
-                       : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), 256,
+                                      least, n_splits_max)
+                       : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), least,
                                         n_splits_max);
         // the partial slots (and, in the tensor-core kernel, the CTAs) that the longest stream takes
         splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);

@@ -95,10 +95,11 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         if (rc != TF_OK || rows == 0) return rc;
         // the tensor-core kernel (prefixes, and more than 8 queries a kv-head) in one wave: 8,192 keys x 256 queries
         // take 26 us in 1,024-key splits (128 CTAs), 30 in 512 and in 1,280; the decode kernel two CTAs an SM
+        const int least = least_split(longest_keys(host, n), false);
         if (split == 0)
             split = (int64_t)rows * group > 8
-                        ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), 128, splits)
-                        : decode_split(host, n, n_kv_heads, device_sms() * 2, 1024, splits);
+                        ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), least, splits)
+                        : decode_split(host, n, n_kv_heads, device_sms() * 2, 1024, least, splits);
         splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
         return TF_OK;
     };
