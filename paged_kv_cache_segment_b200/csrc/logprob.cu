@@ -311,11 +311,12 @@ struct FinishBuf {
     int n;
 };
 
-// A warp ends a row of its own, `own` being the lane's statistics.  Returns the
-// joined ones; with TOP the K largest keys are in b.top, largest first, 0 past the
+// A warp ends a row of its own, `own` being the lane's statistics and, if DEEP,
+// `other` the largest of another part of the lane's columns.  Returns the joined ones; with TOP the K largest keys are in b.top, largest first, 0 past the
 // unmasked columns.
-template <typename T, bool TOP, int LIST>
-__device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, FinishBuf<LIST> &b, int K, float c) {
+template <typename T, bool TOP, bool DEEP, int LIST>
+__device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, float other, FinishBuf<LIST> &b, int K,
+                                       float c) {
     using E = Elem<T>;
     constexpr int EPV = E::kPer;
     const int lane = threadIdx.x & 31;
@@ -328,14 +329,27 @@ __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, Fin
     }
     const float lm = own.m;  // the lane's largest
     if constexpr (TOP) {
-        // ---- the threshold: the K-th largest of the lanes' largest values (equal ones rank by lane)
-        int r = 0;
+        // ---- the threshold: the K-th largest of the lanes' largest values (equal ones rank by lane),
+        // if DEEP of two a lane: of one, some 18 elements reach it for K = 14 but 130 for K = 32
+        int r = 0, r2 = 0;
+        if constexpr (!DEEP) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float y = __shfl_sync(0xffffffffu, lm, j);
-            r += (y > lm || (y == lm && j < lane)) ? 1 : 0;
+            for (int j = 0; j < 32; ++j) {
+                const float y = __shfl_sync(0xffffffffu, lm, j);
+                r += (y > lm || (y == lm && j < lane)) ? 1 : 0;
+            }
+            r2 = 32;
+        } else {
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {  // (the others after every largest of the same value)
+                const float y = __shfl_sync(0xffffffffu, lm, j), z = __shfl_sync(0xffffffffu, other, j);
+                r += ((y > lm || (y == lm && j < lane)) ? 1 : 0) + (z > lm ? 1 : 0);
+                r2 += (y >= other ? 1 : 0) + ((z > other || (z == other && j < lane)) ? 1 : 0);
+            }
         }
-        const float tau = __shfl_sync(0xffffffffu, lm, __ffs(__ballot_sync(0xffffffffu, r == K - 1)) - 1);
+        const uint32_t one = __ballot_sync(0xffffffffu, r == K - 1), two = __ballot_sync(0xffffffffu, r2 == K - 1);
+        const float tau = one ? __shfl_sync(0xffffffffu, lm, __ffs(one) - 1)
+                              : __shfl_sync(0xffffffffu, other, two ? __ffs(two) - 1 : 0);
         const int nk = (w.v1 - w.v0 + 31) / 32;  // vectors a lane
         // the lanes whose largest value is at least `want` (above it, if strict)
         auto find = [&](float want, bool strict) -> int {
@@ -797,7 +811,8 @@ __global__ void __launch_bounds__(NT, NT >= 1024 ? 1 : 1024 / NT) logprob_kernel
 constexpr int kLpWarpRows = 8;   // warps a CTA
 constexpr int kLpWarpList = 256;
 
-template <typename T, bool TOP>
+// DEEP: many alternatives, see finish().
+template <typename T, bool TOP, bool DEEP>
 __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const LogprobParams p) {
     __shared__ FinishBuf<TOP ? kLpWarpList : 1> s_fin[kLpWarpRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -806,21 +821,30 @@ __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const
     if (row >= p.n_rows) return;
     const RowView<T> w(p, row, 0, 1);
     Stat st{-INFINITY, 0.f, 0.f};
+    float other = -INFINITY;  // the largest outside the chunk with the lane's largest
     uint32_t a[kLpBatch][4], b[kLpBatch][4];
     const int n_chunks = w.chunks(32);
     w.chunk(0, lane, 32, a);
     GivenToken given;
     given.ask(p, row, true);
+    auto step = [&](const uint32_t (&x)[kLpBatch][4]) {
+        const float before = st.m, mx = fold<T>(st, x, c);
+        if constexpr (DEEP) other = fmaxf(other, fminf(before, mx));
+    };
     for (int ch = 0; ch < n_chunks; ch += 2) {
         if (ch + 1 < n_chunks) w.chunk(ch + 1, lane, 32, b);
-        fold<T>(st, a, c);
+        step(a);
         if (ch + 1 < n_chunks) {
             if (ch + 2 < n_chunks) w.chunk(ch + 2, lane, 32, a);
-            fold<T>(st, b, c);
+            step(b);
         }
     }
+    if (DEEP && n_chunks == 1) {  // of one chunk, the smaller of its halves' largest
+        static_assert(kLpBatch == 4, "two vectors a half");
+        other = fminf(fmaxf(Elem<T>::most(a[0]), Elem<T>::most(a[1])), fmaxf(Elem<T>::most(a[2]), Elem<T>::most(a[3])));
+    }
     given.fetch(p, w.at);
-    const Stat all = finish<T, TOP>(w, st, s_fin[warp], p.top_k, c);
+    const Stat all = finish<T, TOP, DEEP>(w, st, other, s_fin[warp], p.top_k, c);
     write_row<T, TOP>(p, row, all, s_fin[warp].top, given);
 }
 
@@ -847,7 +871,11 @@ cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     // short rows (up to four chunks of a warp): a warp a row (60,000 rows x 1,000 with 5: 77 us; 356 by CTAs of 64)
     if (p.n_cols <= 4 * 32 * chunk && p.n_rows > 4 * sms) {
         const int64_t grid = ((int64_t)p.n_rows + kLpWarpRows - 1) / kLpWarpRows;
-        logprob_warp_kernel<T, TOP><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
+        // (20,000 rows x 3,000 with 32: 98 us deep, 298 not; 60,000 x 1,000 with 20: 140 and 130)
+        if (TOP && p.top_k > 24)
+            logprob_warp_kernel<T, TOP, TOP><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
+        else
+            logprob_warp_kernel<T, TOP, false><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
         return cudaGetLastError();
     }
     // many rows: eight CTAs an SM where a row is short (4,000 rows x 32,000 with 20: 93 us, 106 by four), else four

@@ -59,7 +59,8 @@ def check_rows(x, tokens, top_k, scale=1.0, n_cols=None, **kw):
 @pytest.mark.parametrize("rows,cols,top_k,n_tok", [(1, 1, 1, 1), (3, 2, 32, 2), (5, 7, 3, 1), (2, 31, 31, 0),
                                                    (4, 33, 32, 3), (2, 1000, 0, 1), (7, 4097, 20, 2),
                                                    (1, 50257, 20, 1), (33, 16385, 5, 1), (3, 128000, 20, 4),
-                                                   (301, 2500, 1, 1), (700, 300, 8, 1), (3, 9000, 4, 70), (700, 200, 2, 33)])
+                                                   (301, 2500, 1, 1), (700, 300, 8, 1), (3, 9000, 4, 70), (700, 200, 2, 33),
+                                                   (700, 700, 32, 1), (800, 3500, 32, 1), (600, 45, 17, 1)])
 def test_rows_match_float64(dtype, rows, cols, top_k, n_tok):
     rng = np.random.default_rng(rows * 7 + cols)
     x = torch.from_numpy(rng.normal(0, 3, (rows, cols)).astype(np.float32)).to(DEV).to(DT[dtype])
