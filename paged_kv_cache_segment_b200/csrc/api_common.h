@@ -107,17 +107,17 @@ inline int longest_keys(const tf_seg *sh, int n_segs) {
     return n;
 }
 
-// The least split worth a CTA of its own: one 64-key tile, as long as a stream has
-// at most 32 partials for the merge, and two tiles where that leaves one split and
-// the kernel needs no merge (`direct`).  8-bit, 1 stream, us: 8 rows, D 256, 512
-// keys 13.8 by tiles, 14.5 by 128, 17.6 by 256; 4,096 keys 17.4 by 64, 15.6 by 128;
-// 100 keys 13.5 by 64, 12.6 direct; one row, D 128, 600 keys 8.9, 9.1, 10.8.  (2
-// one-row streams of 353-2,000 keys behind a short prefix, 16/8 heads: 17.7 against
-// 24.2 by 256 and, for the prefix, 128; 15 streams of 2,000 behind 3 of 846 lose 1.4
-// to a wider merge.)
+// The least split worth a CTA of its own: one 64-key tile, more for a longer stream,
+// whose partials the merge has to read; two tiles where that leaves one split and the
+// kernel needs no merge (`direct`).  8-bit, 1 stream, us by splits of 64, 128 and 256:
+// 8 rows, D 256, 512 keys 13.8, 14.5 and 17.6; 4,096 keys 17.4, 15.6 and 18.3; 8,000
+// 19.2 by 128, 18.5 by 256; 100 keys 13.5, 12.6 direct; one row, D 128, 600 keys 8.9,
+// 9.1 and 10.8; 16,000 11.2 and 11.1.  (2 one-row streams of 353-2,000 keys behind a
+// short prefix, 16/8 heads: 17.7 against 24.2 by 256; 15 streams of 2,000 behind 3 of
+// 846 lose 1.4 to a wider merge.)
 inline int least_split(int longest, bool direct) {
     if (direct && longest <= 128) return 128;
-    return longest <= 64 * 32 ? 64 : (longest + 31) / 32;
+    return longest <= 2048 ? 64 : longest <= 8192 ? 128 : 256;
 }
 
 // A split size for kernels of one CTA an SM with a fixed cost a CTA (start-up
