@@ -134,9 +134,9 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  *
  *  workspace   device scratch of at least tf_paged_attn_q8_workspace_bytes(...)
  *              bytes, 16-byte aligned; needs no initialisation
- *  out         f32 or bf16 (out_dtype TF_OUT_F32 / TF_OUT_BF16, rounded once; for
- *              bf16 the softmax weights may be fed to the value product in f16)
- *              [n_rows_total][n_q_heads][head_dim], 16-byte aligned
+ *  out         f32 or bf16 (out_dtype TF_OUT_F32 / TF_OUT_BF16: the bf16 rows are
+ *              the f32 ones, rounded once) [n_rows_total][n_q_heads][head_dim],
+ *              16-byte aligned
  *  flags       u8 [n_rows_total][n_q_heads]: 1 where a visible score, value or
  *              the output is nonfinite, or the table's entry is bad; out is NaN there
  *

@@ -131,13 +131,14 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         t.part_flag = b.flag;
         if (splits == 1) {  // nothing to merge
             t.out = out;
+            t.out_bf16 = out_dtype == TF_OUT_BF16;
             t.out_flags = flags;
         }
         t.max_rows = max_rows;
         t.status = status;
         direct = splits == 1;
         if ((int64_t)t.n_qt * splits > 0x7fffffff || c.n_kv_heads > 65535) return TF_ERR_UNSUPPORTED;
-        e = launch_verify_q8(t, c.head_dim, c.kv_type, out_dtype == TF_OUT_F32, n_segs, st);
+        e = launch_verify_q8(t, c.head_dim, c.kv_type, n_segs, st);
     } else {
         AttnParams p{};
         p.q = static_cast<const uint16_t *>(q);

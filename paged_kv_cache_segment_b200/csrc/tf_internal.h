@@ -102,8 +102,9 @@ struct Q8TcParams {
     int full;
     float *part_o, *part_m, *part_l;
     uint8_t *part_flag;
-    // one split a stream: the final rows (f32, or bf16 without hi-lo weights) instead of partials
+    // one split a stream: the final rows instead of partials
     void *out;
+    int out_bf16;
     uint8_t *out_flags;
     uint32_t *status;
     int test_idle;  // the timeout test hook, as in PromptTcParams
@@ -210,7 +211,7 @@ int decode_q8_grid(int head_dim, int kv_type);  // CTAs of a full launch on the 
 cudaError_t launch_decode_q8(const WsParams &p, int head_dim, int kv_type, const void *k, const void *v,
                              int64_t n_items_bound, cudaStream_t st);
 bool verify_q8_supported(int head_dim, int group, int split_keys);
-cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, bool hilo, int n_segs, cudaStream_t st);
+cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, int n_segs, cudaStream_t st);
 cudaError_t launch_kv_append(const AppendParams &p, int head_dim, int n_segs, int max_rows, cudaStream_t st);
 cudaError_t launch_prompt_tc(const PromptTcParams &p, int head_dim, const void *k, const void *v, cudaStream_t st);
 bool partial_tc_supported(int head_dim, int group, int page_size, int split_keys);

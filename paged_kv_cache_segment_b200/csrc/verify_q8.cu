@@ -20,8 +20,6 @@
 // the converters never multiply, and an element costs them about one
 // instruction: with bf16 tiles that carry the scales it would be four.
 //
-// For bf16 output W is one f16 (see HILO below).
-//
 // Measured: 8 streams of 1-16 rows over 2,048-16,384 keys, 16/2 heads, D 256, int8
 // (87 MB) in 47 us for bf16 output, 51 for f32; the kernel 45 us of it: 5 us until
 // the first tile's scores, then 19 tiles a CTA, 3.5 us of epilogue.  A tile takes
@@ -105,9 +103,7 @@ __device__ __forceinline__ bool vq_wait(uint32_t bar, uint32_t phase, volatile u
     return false;
 }
 
-// HILO: weights as f16 hi + f16 lo (f32 output); otherwise as one f16, whose
-// rounding is a quarter of a bf16 output's own.
-template <int D, int TYPE, bool HILO>
+template <int D, int TYPE>
 __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcParams p) {
     using C = VqCfg<D>;
     extern __shared__ unsigned char smem_raw[];
@@ -145,10 +141,10 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         for (int64_t x = tid; x < (hi - lo) * G * D; x += kVqThreads) {
             const int64_t r = x / (G * D), c = x - r * (G * D);  // a row's G heads lie together
             const int64_t at = ((lo + r) * p.hq + g * G) * D + c;
-            if (HILO)
-                static_cast<float *>(p.out)[at] = __int_as_float(0x7fc00000);
-            else
+            if (p.out_bf16)
                 static_cast<uint16_t *>(p.out)[at] = 0x7fc0;
+            else
+                static_cast<float *>(p.out)[at] = __int_as_float(0x7fc00000);
             if (c % D == 0) p.out_flags[at / D] = 1;
         }
     };
@@ -399,7 +395,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 for (int kk = 0; kk < kN / 16; ++kk) {
                     const uint64_t bd = umma_desc_sw128(sV(s) + kk * 16 * 128, kSlab, 1024);
                     umma_ts(tmem + kColO, sb + kk * 8, bd, idesc_wv, (j > 0 || kk > 0) ? 1u : 0u);
-                    if (HILO) umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
+                    umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
                 }
                 umma_commit(bar(kBarO + b));
                 umma_commit(bar(kBarVFree + s));
@@ -570,15 +566,13 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             }
             const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;
             {
-                uint32_t hi[16], lo[HILO ? 16 : 1];
+                uint32_t hi[16], lo[16];
                 uint64_t ls2 = 0;  // two zeros
                 const uint64_t nmu2 = pk2(-mu, -mu);
                 auto split = [&](int c, float w0, float w1) {
                     hi[c / 2] = pack_f16x2(w0, w1);
-                    if constexpr (HILO) {
-                        const float2 f = f16x2_to_f32(hi[c / 2]);
-                        lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
-                    }
+                    const float2 f = f16x2_to_f32(hi[c / 2]);
+                    lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
                 };
                 if (__all_sync(0xffffffffu, vmax + mu - ru <= 90.f)) {
                     // a weight is its probability times 2^(e + mu - ru): a probability
@@ -619,7 +613,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 float ls0, ls1;
                 unpk2(ls2, ls0, ls1);
                 l_run += ls0 + ls1;
-                if constexpr (HILO) tmem_st16(lane_base + colS + 32 + 16 * h, lo);
+                tmem_st16(lane_base + colS + 32 + 16 * h, lo);
                 tmem_st16(lane_base + colS + 16 * h, hi);
             }
             // O holds the tiles before this one: rescale it once W V(j - 1) is done
@@ -684,7 +678,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 if (!valid_row) continue;
 #pragma unroll
                 for (int w = 0; w < 32; ++w) o[w] = bad ? __int_as_float(0x7fc00000) : o[w];
-                if constexpr (HILO) {
+                if (!p.out_bf16) {
                     float4 *d4 = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * D + d0 + cc * 32);
 #pragma unroll
                     for (int w = 0; w < 8; ++w) d4[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
@@ -760,10 +754,10 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     if (sent_row) bulk_wait_read();
 }
 
-template <int D, int TYPE, bool HILO>
+template <int D, int TYPE>
 cudaError_t launch_t(const Q8TcParams &p, int n_segs, cudaStream_t st) {
     using C = VqCfg<D>;
-    auto kern = verify_q8_kernel<D, TYPE, HILO>;
+    auto kern = verify_q8_kernel<D, TYPE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     Q8TcParams q = p;
@@ -777,10 +771,8 @@ cudaError_t launch_t(const Q8TcParams &p, int n_segs, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_d(const Q8TcParams &p, int kv_type, bool hilo, int n_segs, cudaStream_t st) {
-    if (kv_type == TF_KV_E4M3)
-        return hilo ? launch_t<D, TF_KV_E4M3, true>(p, n_segs, st) : launch_t<D, TF_KV_E4M3, false>(p, n_segs, st);
-    return hilo ? launch_t<D, TF_KV_INT8, true>(p, n_segs, st) : launch_t<D, TF_KV_INT8, false>(p, n_segs, st);
+cudaError_t launch_d(const Q8TcParams &p, int kv_type, int n_segs, cudaStream_t st) {
+    return kv_type == TF_KV_E4M3 ? launch_t<D, TF_KV_E4M3>(p, n_segs, st) : launch_t<D, TF_KV_INT8>(p, n_segs, st);
 }
 
 }  // namespace
@@ -790,11 +782,11 @@ bool verify_q8_supported(int head_dim, int group, int split_keys) {
            split_keys > 0 && split_keys % kN == 0;
 }
 
-cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, bool hilo, int n_segs, cudaStream_t st) {
+cudaError_t launch_verify_q8(const Q8TcParams &p, int head_dim, int kv_type, int n_segs, cudaStream_t st) {
     switch (head_dim) {
-        case 64: return launch_d<64>(p, kv_type, hilo, n_segs, st);
-        case 128: return launch_d<128>(p, kv_type, hilo, n_segs, st);
-        case 256: return launch_d<256>(p, kv_type, hilo, n_segs, st);
+        case 64: return launch_d<64>(p, kv_type, n_segs, st);
+        case 128: return launch_d<128>(p, kv_type, n_segs, st);
+        case 256: return launch_d<256>(p, kv_type, n_segs, st);
         default: return cudaErrorInvalidValue;
     }
 }
