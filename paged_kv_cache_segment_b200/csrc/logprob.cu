@@ -124,10 +124,11 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
 }
 
 // A masked column (-infinity) enters the sums as this finite value, whose term
-// is 0 and whose product with 0 is 0; x - m cannot overflow from it.  It also
-// stands in for logits below it, so a thread whose maximum is not far above it
-// takes the careful form instead.
-constexpr float kLpFloor = -0x1p126f, kLpCareful = -0x1p125f;
+// is 0 and whose product with 0 is 0: x - m stays finite while m < 2^127 (past
+// 2^128 - 2^126 it would be -infinity, and 0 times it NaN).  It also stands in
+// for logits below it.  So a thread whose maximum is not far above it, or is
+// 2^127 or more, takes the careful form instead, where x - m itself is clamped.
+constexpr float kLpFloor = -0x1p126f, kLpLow = -0x1p125f, kLpHigh = 0x1p127f;
 
 template <typename T>
 struct Elem;
@@ -236,7 +237,7 @@ __device__ __forceinline__ float fold(Stat &st, const uint32_t (&x)[kLpBatch][4]
 #pragma unroll
     for (int k = 0; k < kLpBatch; ++k) mx = fmaxf(mx, E::most(x[k]));
     if (mx > st.m) st.to(mx, c);
-    if (st.m > kLpCareful || st.m == -INFINITY) {
+    if ((st.m > kLpLow && st.m < kLpHigh) || st.m == -INFINITY) {
         // (all masked so far: the reference is 0, every term 0 or a NaN)
         const float ref = st.m == -INFINITY ? 0.f : -st.m;
         const uint64_t ref2 = pk2(ref, ref), c2 = pk2(c, c);
@@ -262,7 +263,8 @@ __device__ __forceinline__ float fold(Stat &st, const uint32_t (&x)[kLpBatch][4]
         for (int k = 0; k < kLpBatch; ++k)
 #pragma unroll
             for (int e = 0; e < E::kPer; ++e) {
-                const float d = max_nan(E::get(x[k], e) - st.m, -FLT_MAX);  // a masked column: 0 * finite
+                // (a masked column, or one more than FLT_MAX below: 0 * finite)
+                const float d = max_nan(E::get(x[k], e) - st.m, -FLT_MAX);
                 const float q = ex2(d * c);
                 st.l += q;
                 st.t = fmaf(q, d, st.t);

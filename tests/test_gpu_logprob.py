@@ -186,3 +186,41 @@ def test_the_first_alternative_is_the_argmax():
     ids, fl = torch.empty(62, device=DEV, dtype=torch.int32), torch.empty(62, device=DEV, dtype=torch.uint8)
     tf.tf_argmax_rows(x, ids, fl)
     assert (ids.cpu().numpy() == got[3][:, 0]).all()
+
+
+HIGHEST = {k: -v for k, v in LOWEST.items()}
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("rows,cols,top_k", [(8, 40, 8), (8, 3001, 0), (8, 20000, 5), (8, 130000, 20),  # a CTA, a cluster
+                                             (640, 300, 4), (640, 3500, 32)])  # a warp a row
+def test_rows_whose_largest_logit_is_the_types_highest(dtype, rows, cols, top_k):
+    """A token forced with the type's highest value: the others weigh nothing, so the entropy is 0 and not NaN,
+    whatever they are (masked, the lowest value, ordinary) and wherever the row's own padding lies."""
+    rng = np.random.default_rng(cols)
+    hi, lo, inf = HIGHEST[dtype], LOWEST[dtype], float("inf")
+    x = torch.from_numpy(rng.normal(0, 2, (rows, cols)).astype(np.float32)).to(DEV).to(DT[dtype])
+    at = rng.integers(0, cols, rows)
+    for r in range(0, rows, 8):
+        x[r + 1] = -inf
+        x[r + 2] = lo
+        x[r + 3, cols // 2 :] = -inf
+        x[r + 4, ::3] = lo
+    x[torch.arange(rows, device=DEV), torch.from_numpy(at).to(DEV)] = hi
+    x[5::8, 0] = hi  # twice (unless it is the same column)
+    x[6::8] = hi / 4 * 3  # below the border of the plain form's own rule, every column the same
+    x[7::8] = -inf
+    x[7::8, cols - 1] = 2.0**127
+    tok = np.stack([at, rng.integers(0, cols, rows)], 1)
+    got, st = run(x, tok, top_k)
+    # (lowest - highest is -2^129 (1 - 2^-8) or less, below the floats: -infinity in the outputs' type)
+    xs = x.double().cpu().numpy()
+    m = xs.max(1)
+    want = list(sv.logprobs(xs - m[:, None], 1.0, tok, top_k))  # log p does not change; log n is lost next to 2^127
+    want[2] = want[2] + m
+    want[3] = sv.logprobs(xs, 1.0, tok, top_k)[3]  # (and the order of ordinary logits in x - m)
+    with np.errstate(over="ignore"):
+        want = [w.astype(np.float32) if w.dtype == np.float64 else w for w in want]
+    check(got, want, 1.0, 8.0)
+    assert st == 0 and (got[5] == 0).all() and np.isfinite(got[1]).all()
+    assert (got[1][0::8] == 0).all() and (got[1][1::8] == 0).all() and (got[1][2::8] == 0).all()
