@@ -116,7 +116,9 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  * Attention of every stream's rows over an 8-bit cache, partials and merge in
  * one call: what tf_paged_attn_decode (or, with full != 0,
  * tf_paged_attn_block) and tf_attn_merge compute, with K and V the values the
- * codes stand for.  Scores, softmax statistics and sums are held in fp32.
+ * codes stand for.  Scores, softmax statistics and sums are held in fp32; a
+ * weight, times its value row's scale, enters the value product with 22 bits and
+ * at least to 2^-32 of the largest such product of its partial.
  *
  *  scale       > 0
  *  split_keys  keys a partial covers: 0 lets the library choose (from the host
@@ -129,8 +131,9 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  * is given a host table with the most rows and keys the replays will see; a
  * replay whose stream asks for more partials reports TF_DEV_SPLITS, one whose
  * stream has more rows than the launch holds TF_DEV_BAD_SEG, and those of the
- * stream's rows that the launch holds are flagged.  Without one the launch is sized for n_splits_max partials of
- * every stream, and decode rows do not take the kernel made for them: slower.
+ * stream's rows that the launch holds are flagged.  Without one the launch is
+ * sized for n_splits_max partials of every stream, and decode rows do not take
+ * the kernel made for them: slower.
  *
  *  workspace   device scratch of at least tf_paged_attn_q8_workspace_bytes(...)
  *              bytes, 16-byte aligned; needs no initialisation

@@ -22,11 +22,12 @@
 //    2^-29 of the largest and off by 2^-40 of it below that.
 //  - Scales never touch the codes.  K's multiplies the score.  V's joins the
 //    weight: with s_j the score and e_j the value's scale, both in base 2,
-//    l = sum 2^(s_j - m) and o = sum 2^(s_j + e_j - M) c_j each keep their own
-//    running reference, so value rows of any sizes keep 22 bits of their weight
-//    (f16 hi + f16 lo, two MMAs into one fp32 accumulator).
-//  - The references move only when a term would pass 2^8 above them, so a tile
-//    takes one vote instead of two butterfly maxima.
+//    l = sum 2^(s_j - m) and o = sum 2^((s_j - m) + (e_j - r)) c_j, r being a whole
+//    number, so that e_j - r is exact and a weight carries the rounding of s_j - m
+//    alone, whatever the value rows' sizes.  It is fed as f16 hi + f16 lo (two MMAs
+//    into one fp32 accumulator; see kRefLift for what they hold).
+//  - The references move only when a term would pass 2^15, so a tile takes one
+//    vote instead of two butterfly maxima.
 // Measured (partials and merge): 16 streams of 1,024-8,192 keys, 32/8 heads, D 128
 // (123 MB) in 30 us, 4.1 TB/s, 28 of them this kernel; D 256 32 us, D 64 39 us for
 // as many bytes (a key there has a quarter of the time; four CTAs an SM, where
@@ -347,9 +348,9 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
             float o[D / 16][4];
 #pragma unroll
             for (int u = 0; u < D / 16; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
-            // m: reference of the scores; r: reference of score + value scale (both in
-            // base 2; -FLT_MAX before the first key, so nothing is special-cased)
-            float m0 = -FLT_MAX, m1 = -FLT_MAX, r0 = -FLT_MAX, r1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
+            // m: reference of the scores (-FLT_MAX before the first key, so nothing is
+            // special-cased); m + r: that of score + value scale (base 2 both)
+            float m0 = -FLT_MAX, m1 = -FLT_MAX, r0 = 0.f, r1 = 0.f, l0 = 0.f, l1 = 0.f;
             float n0 = INFINITY, n1 = INFINITY;  // the smallest scores (-inf: an overflow, flagged)
             uint32_t e0 = 0, e1 = 0, tb0 = 0, tb1 = 0, badp = 0, vtop = 0;
             const uint64_t f2 = pk2(fa, fb_);
@@ -432,16 +433,15 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                         xa = pk2(va0 ? x0 : -INFINITY, va1 ? x1 : -INFINITY);
                         xb = pk2(vb0 ? x2 : -INFINITY, vb1 ? x3 : -INFINITY);
                     }
-                    const uint64_t ya = add2(xa, pk2(fva, fva)), yb = add2(xb, pk2(fvb, fvb));
-                    // ---- exponents over the references, which move when one would pass 2^8
+                    // ---- exponents over the references, which move when one would pass 2^15
                     uint64_t da, db, ga, gb;
                     float d0, d1, d2, d3, g0, g1, g2, g3;
                     auto over = [&]() {
                         const uint64_t nm = pk2(-m0, -m1), nr = pk2(-r0, -r1);
                         da = add2(xa, nm);
                         db = add2(xb, nm);
-                        ga = add2(ya, nr);
-                        gb = add2(yb, nr);
+                        ga = add2(da, add2(pk2(fva, fva), nr));
+                        gb = add2(db, add2(pk2(fvb, fvb), nr));
                         unpk2(da, d0, d1);
                         unpk2(db, d2, d3);
                         unpk2(ga, g0, g1);
@@ -449,13 +449,12 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                     };
                     over();
                     const float most = max3(max3(d0, d1, d2), max3(d3, g0, g1), fmaxf(g2, g3));
-                    if (__any_sync(0xffffffffu, most > 8.f)) {
-                        float x0, x1, x2, x3, y0, y1, y2, y3;
+                    if (__any_sync(0xffffffffu, most > kRefTop)) {
+                        float x0, x1, x2, x3;
                         unpk2(xa, x0, x1);
                         unpk2(xb, x2, x3);
-                        unpk2(ya, y0, y1);
-                        unpk2(yb, y2, y3);
-                        float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3), b0 = fmaxf(y0, y2), b1 = fmaxf(y1, y3);
+                        float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
+                        float b0 = fmaxf(x0 + fva, x2 + fvb), b1 = fmaxf(x1 + fva, x3 + fvb);
 #pragma unroll
                         for (int s = 4; s < 32; s <<= 1) {
                             a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, s));
@@ -463,14 +462,18 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                             b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, s));
                             b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, s));
                         }
-                        auto move = [](float &ref, float to) -> float {  // the factor of what was summed so far
-                            const float n = fmaxf(ref, to), f = ex2(ref - n);
-                            ref = n;
-                            return f;
+                        // to the tile's largest score and score + scale; the factors of what was summed so far
+                        auto move = [](float &m, float &r, float top, float both, float &fo) -> float {
+                            const float n = fmaxf(m, top - kRefLift), down = m - n;
+                            const float rn = fmaxf(ceilf(both - n) - kRefLift, ceilf(down + r));
+                            fo = ex2(down + (r - rn));
+                            m = n;
+                            r = rn;
+                            return ex2(down);
                         };
-                        l0 *= move(m0, a0);
-                        l1 *= move(m1, a1);
-                        const float h0 = move(r0, b0), h1 = move(r1, b1);
+                        float h0, h1;
+                        l0 *= move(m0, r0, a0, b0, h0);
+                        l1 *= move(m1, r1, a1, b1, h1);
 #pragma unroll
                         for (int u = 0; u < D / 16; ++u) {
                             o[u][0] *= h0;
@@ -556,21 +559,21 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                 const float *src = comb_o + slot * kWsQ * C::kCombStride;
                 f0 |= comb_f[slot][qa];
                 f1 |= comb_f[slot][qb_];
-                // weights of this warp's and the slot's sums at the larger reference
-                auto pair = [](float &ref, float other, float &mine, float &theirs) {
-                    const float n = fmaxf(ref, other);
-                    mine = ex2(ref - n);
-                    theirs = ex2(other - n);
-                    ref = n;
+                // this warp's and the slot's sums at the larger references: the joined l, the weights of o
+                // (r need not be whole any more)
+                auto pair = [](float &m, float &r, float l, float om, float orr, float ol, float &mine,
+                               float &theirs) -> float {
+                    const float n = fmaxf(m, om), dm = m - n, dt = om - n;
+                    const float rm = dm + r, rt = dt + orr, rn = fmaxf(rm, rt);
+                    mine = ex2(rm - rn);
+                    theirs = ex2(rt - rn);
+                    m = n;
+                    r = rn;
+                    return l * ex2(dm) + ol * ex2(dt);
                 };
-                float a, b;
-                pair(m0, comb_m[slot][qa], a, b);
-                l0 = l0 * a + comb_l[slot][qa] * b;
-                pair(m1, comb_m[slot][qb_], a, b);
-                l1 = l1 * a + comb_l[slot][qb_] * b;
                 float a0, b0, a1, b1;
-                pair(r0, comb_r[slot][qa], a0, b0);
-                pair(r1, comb_r[slot][qb_], a1, b1);
+                l0 = pair(m0, r0, l0, comb_m[slot][qa], comb_r[slot][qa], comb_l[slot][qa], a0, b0);
+                l1 = pair(m1, r1, l1, comb_m[slot][qb_], comb_r[slot][qb_], comb_l[slot][qb_], a1, b1);
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u) {
                     const float2 y = *reinterpret_cast<const float2 *>(src + qa * C::kCombStride + 16 * u + 2 * gq);
@@ -591,9 +594,9 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
             }
             if (warp == 0) {
                 take(0);
-                // o in units of 2^m, as the merge wants it (in two steps: 2^(r - m)
-                // itself may be past the floats where o is small)
-                const float g0 = ex2(0.5f * (r0 - m0)), g1 = ex2(0.5f * (r1 - m1));
+                // o in units of 2^m, as the merge wants it (in two steps: 2^r itself
+                // may be past the floats where o is small)
+                const float g0 = ex2(0.5f * r0), g1 = ex2(0.5f * r1);
                 bool nf0 = !isfinite(l0), nf1 = !isfinite(l1);
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u) {

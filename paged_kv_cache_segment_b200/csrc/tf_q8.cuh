@@ -19,6 +19,17 @@ constexpr int kE8Bias = 127;
 constexpr int kE8MinExp = -100;   // the smallest exponent an append writes
 constexpr uint32_t kE8Nan = 255;  // the scale byte of a row that held a NaN or an infinity
 
+// References of the softmax over an 8-bit cache, in base 2: one is set to
+// kRefLift below the largest exponent seen and stays until an exponent passes
+// kRefTop above it.  So a weight is at most 2^15, inside f16, and the largest at
+// least 2^7: f16 hi + f16 lo hold 22 bits of a weight down to 2^-10 of the largest
+// and, as f16 ends at 2^-24, 2^-32 of the largest below that.  (With the references
+// at the largest exponent that floor is 2^-25: 32,000 keys just below it, behind one
+// that weighs 1, lost 8e-4 of an output whose sum counted them.  A lift of 11 would
+// put it at 2^-36, but the references then move oftener: a verify round of 1-16
+// rows takes 58.5 us a call instead of 54.8, a decode step 32.8 with either.)
+constexpr float kRefLift = 7.f, kRefTop = 15.f;
+
 // 2^(e - 127) (e = 0: the subnormal 2^-127), NaN for 255.
 __device__ __forceinline__ float e8m0_f32(uint32_t e) {
     return __uint_as_float(e == kE8Nan ? 0x7fc00000u : (e == 0 ? 0x00400000u : e << 23));

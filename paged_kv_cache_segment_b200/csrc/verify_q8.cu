@@ -16,7 +16,7 @@
 //  - eight softmax warps, two threads a query row, as in prompt_tc.cu.
 // The numerics are those of decode_q8.cu: Q's rows scaled by a power of two into
 // f16, K's scale multiplying the score, V's joining the weight, whose sum o
-// keeps a reference of its own (W = f16 hi + f16 lo, 22 bits of a weight).  So
+// keeps a reference of its own (W = f16 hi + f16 lo: see kRefLift).  So
 // the converters never multiply, and an element costs them about one
 // instruction: with bf16 tiles that carry the scales it would be four.
 //
@@ -535,18 +535,18 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             s_xmax[b][h][qi] = mx;
             named_bar_sync(pair_bar, 64);
             mx = fmaxf(mx, s_xmax[b][h ^ 1][qi]);
-            // lazy references: they move when a term would pass 2^8 above them
-            // (both halves see the same maxima, so they move together)
-            if (mx > m_ref + 8.f) {
-                l_run *= ex2(m_ref - mx);
-                m_ref = mx;
+            // lazy references: they move when a term would pass 2^15 (both halves see
+            // the same maxima, so they move together)
+            if (mx > m_ref + kRefTop) {
+                l_run *= ex2(m_ref - (mx - kRefLift));
+                m_ref = mx - kRefLift;
             }
             const uint64_t fq2 = pk2(fq, fq);
             float alpha = 1.f;
             // score + value exponent is at most mx + vmax: its own maximum is
             // looked for only when that bound is past the reference
             const float vmax = (float)((int)max(s_vmax[fs][0], s_vmax[fs][1]) - kE8Bias);
-            if (__any_sync(0xffffffffu, mx + vmax > r_ref + 8.f)) {
+            if (__any_sync(0xffffffffu, mx + vmax > r_ref + kRefTop)) {
                 float my = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 s_ymax[h][qi] = my;
                 named_bar_sync(pair_bar, 64);
                 my = fmaxf(my, s_ymax[h ^ 1][qi]);
-                if (my > r_ref + 8.f) {
-                    alpha = ex2(r_ref - my);
-                    r_ref = my;
+                if (my > r_ref + kRefTop) {
+                    alpha = ex2(r_ref - (my - kRefLift));
+                    r_ref = my - kRefLift;
                 }
             }
             const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;

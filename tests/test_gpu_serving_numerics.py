@@ -1,9 +1,13 @@
-"""What the serving calls' outputs hold beyond the common bounds: bf16 rows that are the f32 rows rounded."""
+"""What the serving calls' outputs hold beyond the common bounds: bf16 rows that are the f32 rows rounded, weights far
+below the largest."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_q8 import attn, q8_batch
+from paged_kv_cache_segment_b200 import workloads as wl
+
+import _serving as sv
+from test_gpu_q8 import attn, cache_of, q8_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +33,62 @@ def test_bf16_rows_are_the_f32_rows_rounded_once(kind, rows, keys, hq, hkv, d):
         assert (got == want).all(), f"{np.mean(got != want):.1%} of the elements differ"
         again, _, _ = attn(c, b, kind)
         assert (again == wide).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,hq,hkv,d", [(1, 4, 1, 64), (1, 8, 2, 128), (1, 2, 1, 256),  # decode
+                                           (12, 1, 1, 64), (5, 8, 2, 128), (9, 2, 1, 256)])  # tcgen05
+@pytest.mark.parametrize("n,split", [(32000, 32000), (32000, 4096), (4000, 4032)])
+def test_keys_far_below_one_dominant_key_keep_their_weight(kind, rows, hq, hkv, d, n, split):
+    """One key of score 1.625 sqrt(D) and all others of score 0, their values in columns where its own is 0.  In base
+    2 the others lie 18.8 (D 64), 26.5 and 37.5 below it; their sum is that column's output.  A weight may be off by
+    2^-32 of the largest, so the n of them by n 2^-32, and a weight is else held to 2^-14 of itself.  The matrix
+    units' fp32 sums of a column take two additions (hi, lo) every 16 keys, each off by at most a step, 2^-23 of a sum
+    that grows evenly from 0 (half of the final one on average): n / 16 * 2 * 2^-23 / 2 = n 2^-27 of it."""
+    psz = 64
+    b = wl.make_paged_batch(17, rows=[rows], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=psz,
+                            unused="normal")
+    k, v = np.zeros(b.k_pool.shape, np.float32), np.zeros(b.v_pool.shape, np.float32)
+    v[..., 1], v[..., 2] = 1.0, -0.375
+    at = n // 3
+    page = b.page_table[b.segs[0][3] + at // psz]
+    k[page, :, at % psz] = 1.625
+    v[page, :, at % psz] = 0
+    v[page, :, at % psz, 0] = 1.0
+    sides = [sv.quantise(wl.f32_to_bf16_bits(x), kind) for x in (k, v)]
+    b.q = wl.f32_to_bf16_bits(np.ones((rows, hq, d), np.float32))
+    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
+    out, flags, st = attn(c, b, kind, split=split, n_splits_max=-(-n // split))
+    assert st == 0 and (flags == 0).all()
+    small = np.exp(-1.625 * d * b.scale)
+    for i in range(rows):
+        seen = n - rows + i  # keys the row sees beside the dominant one
+        want = np.zeros(d)
+        want[:3] = np.array([1.0, seen * small, -0.375 * seen * small]) / (1 + seen * small)
+        err = np.abs(out[i].astype(np.float64) - want)
+        assert (err <= n * 2.0**-32 + (2.0**-14 + n * 2.0**-27) * np.abs(want)).all(), err.max()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (4, 16, 2)])
+def test_value_scales_and_scores_far_from_one(kind, rows, hq, hkv):
+    """Values of size 2^-90 and scores near 100: a weight's exponent is a small difference of the two, and carries no
+    rounding of their sum.  A score of 100 (in base 2) is itself rounded twice (100 * 2^-23 ln 2 = 2^-16.9 of a
+    weight), a weight kept to 22 bits: each head is held to 2^-15 of its own size."""
+    b = wl.make_paged_batch(18, rows=[rows], keys=[700], n_q_heads=hq, n_kv_heads=hkv, head_dim=128, page_size=32,
+                            unused="normal")
+    x = wl.bf16_bits_to_f32(b.v_pool) * np.float32(2.0**-90)
+    kk = wl.bf16_bits_to_f32(b.k_pool)
+    kk[..., 0] = 24.0
+    q = wl.bf16_bits_to_f32(b.q)
+    q[..., 0] = 32.0  # 768 / sqrt(128) = 68 nats, 98 in base 2, for every key
+    b.q = wl.f32_to_bf16_bits(q)
+    sides = [sv.quantise(wl.f32_to_bf16_bits(y), kind) for y in (kk, x)]
+    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
+    out, flags, st = attn(c, b, kind)
+    assert st == 0 and (flags == 0).all()
+    n, base = b.segs[0][2], b.segs[0][3]
+    k, v = (sv.values(sv.keys_of(cc, b.page_table, base, n), sv.keys_of(s, b.page_table, base, n), kind) for cc, s in sides)
+    ref, _ = sv.attend(sv.bf16(b.q), k, v, [n - rows + i + 1 for i in range(rows)], b.scale)
+    err = np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert err.max() <= 2.0**-15, err.max()
