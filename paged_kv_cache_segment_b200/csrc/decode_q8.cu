@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
         }
         cp_async_commit();
         cp_async_wait<0>();  // no scale byte is in flight when this CTA ends
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        // (the merge, which waits for this grid; final rows have none, and another launch need not wait)
+        if constexpr (!DIRECT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     } else {
         // ---- consumer warps
         const int gq = lane >> 2, t4 = lane & 3;

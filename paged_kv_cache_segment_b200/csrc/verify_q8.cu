@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint64_t lim = p.wait_ns ? p.wait_ns : 2000000000ull;  // every bounded wait's limit
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the merge may start: it waits for this grid.  Final rows have none, and what
+    // follows on the stream need not wait (a prompt chunk does not): no early start then.
+    if (!p.out) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char *base_ptr = smem_raw + (sbase - smem_u32(smem_raw));
     auto sK = [&](int s) { return sbase + C::kOffK + s * C::kTile; };
