@@ -130,9 +130,14 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     volatile uint32_t *abort_flag = &s_abort;
     bool sent_row = false;  // this thread sent a staged row with a bulk copy
-    // beside another partial kernel (PromptTcParams::beside): this grid ends after that one
+    // a grid that may have started before the one it follows had finished ends after
+    // it, so that what comes next on the stream is ordered behind both: a prompt chunk
+    // by one thread of its last block (the one that starts last), partials beside
+    // another partial kernel (PromptTcParams::beside) by all
     auto leave = [&]() {
-        if (PARTIAL && p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (PARTIAL ? p.beside != 0
+                    : blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && threadIdx.x == 0)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
     };
 
     const int G = p.group, RT = kQM / p.group;  // rows a tile
@@ -805,7 +810,7 @@ static cudaError_t launch_tc_t(const PromptTcParams &p, const void *k, const voi
     // library's previous chunk, or another of its attention calls) finishes:
     // it reads q, the pools and the page table, which none of them writes, so
     // the next chunk's tiles fill the SMs the previous chunk's last wave
-    // leaves idle.  (So may partials beside another partial kernel, whose outputs
+    // leaves idle; it ends after that call (leave() in the kernel).  (So may partials beside another partial kernel, whose outputs
     // they neither read nor write.)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;

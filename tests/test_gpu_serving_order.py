@@ -72,3 +72,47 @@ def test_a_prompt_chunk_behind_a_one_split_call(kind, rows, hq, hkv, d, graph):
         first = chunk.out.clone() if first is None else first
         assert torch.equal(chunk.out, first)
     assert int(st.item()) == 0 and int(chunk.st.item()) == 0
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,keys", [(1, 32, 8, 128, [6000, 1000]), (12, 16, 2, 256, [3000, 2000]),
+                                                (3, 6, 1, 64, [900, 300])])
+def test_a_prompt_chunk_between_partials_and_their_merge(rows, hq, hkv, d, keys):
+    """Decode partials, a prompt chunk, the merge, two more chunks, then the pools overwritten and the outputs copied:
+    the merge and the copy see what they would see without the chunks."""
+    b = wl.make_paged_batch(6, rows=[rows] * 2, keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32,
+                            split_keys=512, n_splits_max=12)
+    n, c = b.q.shape[0], 12
+    f = dict(device=DEV, dtype=torch.float32)
+    po, pm, pl = torch.empty((n, hq, c, d), **f), torch.empty((n, hq, c), **f), torch.empty((n, hq, c), **f)
+    pf = torch.empty((n, hq, c), dtype=torch.uint8, device=DEV)
+    out, fl, st = torch.empty((n, hq, d), **f), torch.empty((n, hq), dtype=torch.uint8, device=DEV), status_word()
+    q, pt, sg, pools = dev(b.q), dev(b.page_table), dev(b.segs), [dev(b.k_pool), dev(b.v_pool)]
+    keep = [x.clone() for x in pools]
+    chunk, copy = Chunk(d), torch.empty_like(out)
+
+    def partials():
+        tf.tf_paged_attn_decode(q, pools[0], pools[1], pt, sg, scale=b.scale, split_keys=512, n_splits_max=c,
+                                part_o=po, part_m=pm, part_l=pl, part_flag=pf, status=st, segs_host=b.segs)
+
+    partials()
+    tf.tf_attn_merge(po, pm, pl, pf, out, fl)
+    torch.cuda.synchronize()
+    want = out.clone()
+    assert int(st.item()) == 0 and int(fl.sum()) == 0
+    for _ in range(10):
+        for x, was in zip(pools, keep):
+            x.copy_(was)
+        po.fill_(float("nan"))
+        pl.zero_()
+        out.zero_()
+        partials()
+        chunk()
+        tf.tf_attn_merge(po, pm, pl, pf, out, fl)
+        chunk()
+        chunk()
+        copy.copy_(out)
+        for x in pools:
+            x.zero_()
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
+    assert int(st.item()) == 0 and int(chunk.st.item()) == 0
