@@ -310,7 +310,11 @@ TF_API tf_status tf_attn_merge(const float *part_o, const float *part_m, const f
  * one's final wave leaves idle).  It reads only q, the pools and the page
  * table, which those calls never write; two such calls must not write the
  * same out rows.  After any other work on the stream (a kernel of the
- * caller's, tf_kv_append, a copy) it starts when that work has finished.
+ * caller's, tf_kv_append, a copy) it starts when that work has finished, but
+ * for a kernel of the caller's that itself lets programmatic dependents start
+ * early (griddepcontrol.launch_dependents): put another launch between such a
+ * kernel and the chunk if the chunk reads what it writes.  It ends after the
+ * call before it has ended, so later work is ordered behind both.
  *
  * Supported: head_dim in {64, 128, 256}; page sizes as for decode.
  */

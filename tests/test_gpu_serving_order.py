@@ -116,3 +116,52 @@ def test_a_prompt_chunk_between_partials_and_their_merge(rows, hq, hkv, d, keys)
         torch.cuda.synchronize()
         assert torch.equal(copy, want)
     assert int(st.item()) == 0 and int(chunk.st.item()) == 0
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_prompt_chunk_sees_the_rows_written_just_before_it(quantised, graph):
+    """Rows appended (or read back from an 8-bit cache) and a prompt chunk over them, the next call on the stream."""
+    n, hq, hkv, d, psz = 4000, 8, 2, 128, 32
+    b = wl.make_paged_batch(7, rows=[n], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=psz)
+    rng = np.random.default_rng(7)
+    kr, vr = (dev(wl.normal_bf16(rng, (n, hkv, d))) for _ in "kv")
+    q, pt, sg, st = dev(b.q), dev(b.page_table), dev(b.segs), status_word()
+    pools = [torch.zeros((b.n_pages, hkv, psz, d), dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    out = torch.empty((n, hq, d), device=DEV)
+    c = tf.Q8Cache(*(torch.zeros((b.n_pages, hkv, psz, d), dtype=torch.int8, device=DEV) for _ in "kv"),
+                   *(torch.zeros((b.n_pages, hkv, psz), dtype=torch.uint8, device=DEV) for _ in "kv"))
+    tf.tf_kv_append_q8(kr, vr, c, pt, sg, status=st, segs_host=b.segs)
+
+    def write():
+        if quantised:
+            tf.tf_kv_read_q8(c, pt, sg, *pools, pt, status=st, segs_host=b.segs)
+        else:
+            tf.tf_kv_append(kr, vr, *pools, pt, sg, status=st, segs_host=b.segs)
+
+    def attend():
+        tf.tf_paged_attn_prompt(q, *pools, pt, b.segs[0], scale=b.scale, out=out, status=st)
+
+    write()
+    torch.cuda.synchronize()
+    attend()
+    torch.cuda.synchronize()
+    want = out.clone()
+
+    def round_():
+        for x in pools:
+            x.fill_(float("nan"))
+        write()
+        attend()
+
+    run = round_
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            round_()
+        run = g.replay
+    for _ in range(10):
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert int(st.item()) == 0
