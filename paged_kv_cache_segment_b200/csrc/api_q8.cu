@@ -83,6 +83,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         w.pt_len = page_table_len;
         w.k_scale = c.k_scale;
         w.v_scale = c.v_scale;
+        w.max_rows = max_rows;
         w.scale_log2 = scale_log2;
         w.split_keys = split;
         w.n_splits_max = splits;

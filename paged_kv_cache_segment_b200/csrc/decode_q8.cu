@@ -286,12 +286,10 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
         if constexpr (DIRECT) {
             for (int s = bid; s < p.n_segs; s += grid)
                 if (prefix[s + 1] == prefix[s]) {  // an entry found bad (or with no rows)
+                    // its rows that the launch holds, as the merge flags them
                     const tf_seg e = p.segs[s];
-                    const int lo = max(e.q_row, 0);
-                    const int64_t hi = min((int64_t)e.q_row + e.n_rows, (int64_t)p.n_rows_total);
-                    if (hi > lo) flag_rows(lo, (int)(hi - lo), 0, p.hq, lane, 32);
-                    // (more rows than the launch holds: with partials the merge reports it)
-                    if (lane == 0 && (int64_t)e.n_rows * p.group > kWsQ) atomicOr(p.status, TF_DEV_BAD_SEG);
+                    const int rows = e.q_row < 0 ? 0 : min(min(e.n_rows, p.max_rows), p.n_rows_total - e.q_row);
+                    if (rows > 0) flag_rows(e.q_row, rows, 0, p.hq, lane, 32);
                 }
         }
         cp_async_commit();

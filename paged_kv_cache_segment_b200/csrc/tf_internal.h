@@ -139,6 +139,7 @@ struct WsParams {
     void *out;
     int out_bf16;
     uint8_t *out_flags;
+    int max_rows;  // rows of a stream the launch holds (0: any that fit an item)
     float scale_log2;
     int split_keys, n_splits_max;
     int full;  // every row sees all of its stream's keys (no causal count)

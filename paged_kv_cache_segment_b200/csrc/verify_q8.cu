@@ -136,10 +136,12 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     const int split = (int)blockIdx.x / p.n_qt, qt = p.n_qt - 1 - (int)blockIdx.x % p.n_qt;
     const tf_seg e = p.segs[blockIdx.z];
     const int q_row = e.q_row, T = e.n_rows, N = e.n_keys, pt_base = e.pt_base, n_pg = e.n_pages;
-    // final rows of the tile flagged, when there is no merge to do it
+    // final rows of the tile that the launch holds flagged, as the merge would where there is one
     auto flag_rows = [&]() {
-        const int64_t lo = max((int64_t)q_row + (int64_t)qt * RT, (int64_t)0);
-        const int64_t hi = min((int64_t)q_row + min((int64_t)T, (int64_t)(qt + 1) * RT), (int64_t)p.n_rows_total);
+        if (q_row < 0) return;
+        const int64_t lo = (int64_t)q_row + (int64_t)qt * RT;
+        const int64_t hi = min((int64_t)q_row + min((int64_t)min(T, p.max_rows), (int64_t)(qt + 1) * RT),
+                               (int64_t)p.n_rows_total);
         for (int64_t x = tid; x < (hi - lo) * G * D; x += kVqThreads) {
             const int64_t r = x / (G * D), c = x - r * (G * D);  // a row's G heads lie together
             const int64_t at = ((lo + r) * p.hq + g * G) * D + c;

@@ -45,7 +45,7 @@ __device__ __forceinline__ int ws_stream_splits(const WsParams &p, int s, uint32
         const tf_seg e = p.segs[s];
         const bool bad = e.q_row < 0 || e.n_rows < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total ||
                          e.n_keys < (p.full ? (e.n_rows > 0 ? 1 : 0) : e.n_rows) || e.pt_base < 0 || e.n_pages < 0 ||
-                         (int64_t)e.pt_base + e.n_pages > p.pt_len;
+                         (int64_t)e.pt_base + e.n_pages > p.pt_len || (p.max_rows > 0 && e.n_rows > p.max_rows);
         if (bad) {
             bits |= TF_DEV_BAD_SEG;
             return 0;

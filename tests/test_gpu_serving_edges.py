@@ -258,3 +258,55 @@ def test_cache_rows_past_the_launch_are_reported(read):
     mine = set(b.page_table[b.segs[1, 3] : b.segs[1, 3] + 2].tolist())
     for x in changed:  # the first stream is skipped, the second one's last two keys are in its second page
         assert set(torch.nonzero(x).flatten().tolist()) == {int(b.page_table[b.segs[1, 3] + 1])} <= mine
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,hkv,held,keys", [(8, 2, 1, 60), (8, 2, 1, 1500),  # decode: one split, partials
+                                              (16, 2, 12, 60), (16, 2, 12, 1500),  # the tensor-core kernel
+                                              (12, 1, 3, 300)])  # the general kernel
+def test_a_damaged_entry_touches_its_own_rows_only(hq, hkv, held, keys, dt):
+    """Whatever the form of the call, of a bad device entry the rows the launch holds are flagged and reported, no
+    others are written, and the streams beside it come out as they should."""
+    b, sides, c = q8_batch("int8", 14, rows=[held, 2 * held, held, 2 * held], keys=[keys + 60, keys, keys // 2 + 30, 40],
+                           n_q_heads=hq, n_kv_heads=hkv, head_dim=128, page_size=32)
+    n, _, d = b.q.shape
+    good = b.segs.copy()
+    good[[1, 3], 1] = held  # the second half of streams 1 and 3's rows belongs to no one
+    ref, rf, vmax = reference(b, sides, "int8", segs=good)
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 32), dtype=torch.uint8, device=DEV)
+
+    def case(change, flagged, bit=binding.TF_DEV_BAD_SEG):
+        segs = good.copy()
+        change(segs)
+        out, fl = torch.full((n, hq, d), 5.0, dtype=dt, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV)
+        st = status_word()
+        tf.tf_paged_attn_q8(dev(b.q), c, dev(b.page_table), dev(segs), scale=b.scale, n_splits_max=32, workspace=ws,
+                            out=out, flags=fl, status=st, segs_host=good)
+        assert int(st.item()) == bit
+        out, fl = out.float().cpu().numpy(), fl.cpu().numpy()
+        named = np.zeros(n, bool)
+        for s, (q_row, r, *_) in enumerate(good):
+            if (segs[s] == good[s]).all():
+                named[q_row : q_row + r] = True
+        sv.check_attention(out[named], fl[named], ref[named], rf[named], vmax, dt == torch.bfloat16)
+        gone = np.zeros(n, bool)
+        gone[flagged] = True
+        assert np.isnan(out[gone]).all() and (fl[gone] == 1).all()
+        rest = ~named & ~gone
+        assert (out[rest] == 5.0).all() and (fl[rest] == 9).all()
+
+    q1, q3 = good[1, 0], good[3, 0]
+
+    def put(s, at, x):
+        def change(segs):
+            segs[s, at] = x
+
+        return change
+
+    case(put(1, 1, 2 * held), slice(q1, q1 + held))  # more rows than the launch holds
+    case(put(1, 1, held + 1), slice(q1, q1 + held))
+    case(put(1, 0, -held), slice(0, 0))  # before the first row: nothing of it is written
+    if held > 1:
+        case(put(3, 0, n - 1), slice(n - 1, n))  # past the last one
+    case(put(1, 4, 0), slice(q1, q1 + held), binding.TF_DEV_PAST_PAGES)
+    case(put(3, 3, -1), slice(q3, q3 + held))
