@@ -191,6 +191,20 @@ def test_the_first_alternative_is_the_argmax():
 HIGHEST = {k: -v for k, v in LOWEST.items()}
 
 
+def of_large_logits(x, tok, top_k):
+    """sv.logprobs (scale 1) where logits are as large as the type's ends: log p from x - m, since log n is lost next
+    to 2^127; the order from x itself, since ordinary logits are lost in x - m; in the outputs' type, since lowest -
+    highest, -2^129 (1 - 2^-8) or less, is below its floats: -infinity."""
+    xs = x.double().cpu().numpy()
+    m = xs.max(1)
+    m = np.where(np.isfinite(m), m, 0.0)
+    want = list(sv.logprobs(xs - m[:, None], 1.0, tok, top_k))
+    want[2] = want[2] + m
+    want[3] = sv.logprobs(xs, 1.0, tok, top_k)[3]
+    with np.errstate(over="ignore"):
+        return [w.astype(np.float32) if w.dtype == np.float64 else w for w in want]
+
+
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("rows,cols,top_k", [(8, 40, 8), (8, 3001, 0), (8, 20000, 5), (8, 130000, 20),  # a CTA, a cluster
                                              (640, 300, 4), (640, 3500, 32)])  # a warp a row
@@ -213,14 +227,36 @@ def test_rows_whose_largest_logit_is_the_types_highest(dtype, rows, cols, top_k)
     x[7::8, cols - 1] = 2.0**127
     tok = np.stack([at, rng.integers(0, cols, rows)], 1)
     got, st = run(x, tok, top_k)
-    # (lowest - highest is -2^129 (1 - 2^-8) or less, below the floats: -infinity in the outputs' type)
-    xs = x.double().cpu().numpy()
-    m = xs.max(1)
-    want = list(sv.logprobs(xs - m[:, None], 1.0, tok, top_k))  # log p does not change; log n is lost next to 2^127
-    want[2] = want[2] + m
-    want[3] = sv.logprobs(xs, 1.0, tok, top_k)[3]  # (and the order of ordinary logits in x - m)
-    with np.errstate(over="ignore"):
-        want = [w.astype(np.float32) if w.dtype == np.float64 else w for w in want]
-    check(got, want, 1.0, 8.0)
+    check(got, of_large_logits(x, tok, top_k), 1.0, 8.0)
     assert st == 0 and (got[5] == 0).all() and np.isfinite(got[1]).all()
     assert (got[1][0::8] == 0).all() and (got[1][1::8] == 0).all() and (got[1][2::8] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("cols", [300, 512, 700, 3500])
+@pytest.mark.parametrize("top_k", [8, 24, 25, 32])
+def test_short_rows_with_masks_and_ties(dtype, cols, top_k):
+    """Many short rows, a warp each: masks that leave a few lanes, equal columns, the lowest value as a mask, rows of
+    few distinct values; their lists overflow, and the search by ties and the one key by key take over."""
+    rng = np.random.default_rng(cols + top_k)
+    per, inf = (8 if dtype == "bf16" else 4), float("inf")
+    x = torch.from_numpy(rng.normal(0, 2, (640, cols)).astype(np.float32)).to(DEV).to(DT[dtype])
+    col = torch.arange(cols, device=DEV)
+    lane = (col // per) % 32
+    x[0::16] = 0.25
+    x[1::16, lane >= 3] = -inf
+    x[2::16, lane >= 20] = -inf
+    x[3::16, lane >= 31] = LOWEST[dtype]
+    x[4::16] = LOWEST[dtype]
+    x[5::16] = col.to(x.dtype)  # ascending (ties where bf16 cannot tell columns apart)
+    x[6::16] = -inf
+    x[7::16, 5:] = LOWEST[dtype]
+    x[8::16] = torch.from_numpy(rng.integers(0, 3, (40, cols)).astype(np.float32)).to(DEV).to(x.dtype)
+    x[9::16] = torch.where(lane == 7, 3.0, -1.0).to(x.dtype)
+    x[10::16, : cols // 2] = -inf
+    x[11::16, cols // 2 :] = 1.0
+    x[12::16, cols // 3] = float("nan")
+    tok = rng.integers(0, cols, (640, 2))
+    got, st = run(x, tok, top_k)
+    check(got, of_large_logits(x, tok, top_k), 1.0, 8.0)
+    assert st == 0
