@@ -482,6 +482,12 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, c
     const bool bad = !(all.l > 0.f) || !isfinite(all.l) || !isfinite(all.m);
     const float nan = __int_as_float(0x7fc00000);
     const float log_l = logf(all.l);
+    auto log_p = [&](float x) {
+        float y = (x - all.m) * p.scale;
+        // (a logit more than FLT_MAX below the largest: halved, the distance is a float again)
+        if (y == -INFINITY && x != -INFINITY) y = (0.5f * x - 0.5f * all.m) * (2.f * p.scale);
+        return y - log_l;
+    };
     if (lane == 0) {
         if (p.entropy) p.entropy[row] = bad ? nan : log_l - p.scale * (all.t / all.l);
         if (p.lse) p.lse[row] = bad ? nan : fmaf(p.scale, all.m, log_l);
@@ -499,7 +505,7 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, c
         if (g.tok < 0 || g.tok >= p.n_cols)
             atomicOr(p.status, TF_DEV_BAD_TOKEN);
         else if (!bad)
-            lp = (g.x - all.m) * p.scale - log_l;
+            lp = log_p(g.x);
         p.token_logprobs[to] = lp;
     }
     if constexpr (TOP) {
@@ -508,7 +514,7 @@ __device__ __forceinline__ void write_row(const LogprobParams &p, int64_t row, c
             const int64_t to = row * K + lane;
             p.top_ids[to] = (bad || y == 0) ? -1 : (int)~(uint32_t)y;
             p.top_logprobs[to] =
-                bad ? nan : (y == 0 ? -INFINITY : (unkey32((uint32_t)(y >> 32)) - all.m) * p.scale - log_l);
+                bad ? nan : (y == 0 ? -INFINITY : log_p(unkey32((uint32_t)(y >> 32))));
         }
     }
 }

@@ -260,3 +260,24 @@ def test_short_rows_with_masks_and_ties(dtype, cols, top_k):
     got, st = run(x, tok, top_k)
     check(got, of_large_logits(x, tok, top_k), 1.0, 8.0)
     assert st == 0
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("rows,cols", [(2, 40), (2, 130000), (640, 700)])
+def test_a_cold_row_of_logits_from_end_to_end(dtype, rows, cols):
+    """Logits over the type's whole range under a scale of 2^-10 or 2^-64: the distance from the largest is past the
+    floats, the log p is not.  A scaled distance is rounded twice: 2^-23 of the log p."""
+    hi, lo = HIGHEST[dtype], LOWEST[dtype]
+    x = torch.full((rows, cols), lo, device=DEV, dtype=DT[dtype])
+    x[:, 1], x[:, 3], x[:, 5], x[:, 7] = hi, hi / 2, 0.0, -float("inf")
+    tok = np.tile(np.array([[0, 1, 3, 5, 7]]), (rows, 1))
+    xs = x[0].double().cpu().numpy()
+    for scale in (2.0**-10, 2.0**-64):
+        got, st = run(x, tok, 4, scale=scale)
+        want = (xs[[0, 1, 3, 5, 7]] - xs[1]) * scale
+        assert st == 0 and (got[5] == 0).all() and (got[1] == 0).all()
+        assert (got[3] == [1, 3, 5, 0]).all()
+        for g, w in ((got[0], want), (got[4], want[[1, 2, 3, 0]])):
+            assert (np.isneginf(g) == np.isneginf(w)).all()
+            ok = np.isfinite(w)
+            assert (np.abs(g[:, ok] - w[ok]) <= 2.0**-23 * np.abs(w[ok])).all()
