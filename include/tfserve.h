@@ -144,7 +144,8 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  *              the output is nonfinite, or the table's entry is bad; out is NaN there
  *
  * Only the rows the table names are written.  Rows of different streams must
- * not overlap.  Other arguments, shapes and errors: tf_paged_attn_decode.
+ * not overlap.  A stream has up to 2^30 keys (more: TF_ERR_UNSUPPORTED /
+ * TF_DEV_BAD_SEG).  Other arguments, shapes and errors: tf_paged_attn_decode.
  */
 TFS_API tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_heads,
                                    const tf_q8_cache *cache_host, const int32_t *page_table, int32_t page_table_len,
@@ -153,7 +154,7 @@ TFS_API tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t 
                                    int32_t n_splits_max, void *workspace, size_t workspace_bytes, void *out,
                                    int32_t out_dtype, uint8_t *flags, uint32_t *status, tf_stream_t stream);
 
-/* Workspace bytes tf_paged_attn_q8 needs for these sizes (0 on bad sizes). */
+/* Workspace bytes tf_paged_attn_q8 needs for these sizes (0 on bad sizes and past 2^60). */
 TFS_API size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
                                                 int32_t n_splits_max);
 
@@ -182,7 +183,8 @@ TFS_API size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_
  *  out, out_dtype, flags  as for tf_paged_attn_q8; only the rows segs names
  *              are written
  *
- * Other arguments, shapes and errors: tf_paged_attn_decode.
+ * Streams and prefixes have up to 2^30 keys each.  Other arguments, shapes and
+ * errors: tf_paged_attn_decode.
  */
 TFS_API tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                                        const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads,
@@ -194,7 +196,7 @@ TFS_API tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int3
                                        size_t workspace_bytes, void *out, int32_t out_dtype, uint8_t *flags,
                                        uint32_t *status, tf_stream_t stream);
 
-/* Workspace bytes tf_paged_attn_shared needs for these sizes (0 on bad sizes). */
+/* Workspace bytes tf_paged_attn_shared needs for these sizes (0 on bad sizes and past 2^60). */
 TFS_API size_t tf_paged_attn_shared_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
                                                     int32_t n_prefix_splits, int32_t n_splits_max);
 

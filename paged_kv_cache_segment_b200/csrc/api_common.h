@@ -24,9 +24,7 @@ inline bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 inline tf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TF_OK : TF_ERR_CUDA; }
 
 inline int split_len(int n_keys, int split_keys, int n_splits_max, int page_size) {
-    if (split_keys > 0) return split_keys;
-    int per = (n_keys + n_splits_max - 1) / n_splits_max;
-    return (per + page_size - 1) / page_size * page_size;
+    return split_keys > 0 ? split_keys : even_split(n_keys, n_splits_max, log2_exact(page_size));
 }
 
 // Checks of a host copy of a segment table; see tf_paged_attn_decode.
@@ -43,7 +41,7 @@ inline tf_status check_segs_host(const tf_seg *sh, int n_segs, int n_rows_total,
         if ((int64_t)e.n_keys > (int64_t)e.n_pages * page_size) return TF_ERR_PAST_PAGES;
         if (e.n_rows > 0 && n_splits_max > 0) {
             const int per = split_len(e.n_keys, split_keys, n_splits_max, page_size);
-            if ((e.n_keys + per - 1) / per > n_splits_max) return TF_ERR_ARG;
+            if (splits_of(e.n_keys, per) > n_splits_max) return TF_ERR_ARG;
         }
         if (pt_host) {
             const int used = (e.n_keys + page_size - 1) / page_size;
@@ -58,6 +56,13 @@ inline tf_status check_segs_host(const tf_seg *sh, int n_segs, int n_rows_total,
     return TF_OK;
 }
 
+// Whether no entry has more keys than the serving calls take.
+inline bool keys_taken(const tf_seg *sh, int n_segs) {
+    for (int s = 0; s < n_segs; ++s)
+        if (sh[s].n_keys > kMaxKeys) return false;
+    return true;
+}
+
 // An 8-bit cache's type and sizes, its pointers, their alignment.
 inline tf_status check_q8_shape(const tf_q8_cache &c) {
     if (c.n_pages < 0 || c.n_kv_heads <= 0 || (c.kv_type != TF_KV_E4M3 && c.kv_type != TF_KV_INT8)) return TF_ERR_ARG;
@@ -66,8 +71,11 @@ inline tf_status check_q8_shape(const tf_q8_cache &c) {
 }
 
 // Bytes of partials [n_rows_total][n_q_heads][n_splits]: o, m, l, flag, each
-// part's start a multiple of 16 bytes from the last.
+// part's start a multiple of 16 bytes from the last.  More than 2^60: that many.
+constexpr size_t kTooManyBytes = (size_t)1 << 60;
 inline size_t part_bytes(int64_t n_rows_total, int n_q_heads, int head_dim, int n_splits) {
+    const double all = (double)n_rows_total * n_q_heads * n_splits * ((double)head_dim * 4 + 9);
+    if (all > (double)kTooManyBytes) return kTooManyBytes;
     const size_t parts = (size_t)n_rows_total * n_q_heads * n_splits;
     return (parts * ((size_t)head_dim * 4 + 9) + 255) / 256 * 256;
 }

@@ -16,7 +16,8 @@ extern "C" {
 size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
                                         int32_t n_splits_max) {
     if (n_rows_total < 0 || n_q_heads <= 0 || head_dim <= 0 || n_splits_max <= 0) return 0;
-    return part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+    const size_t n = part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+    return n < kTooManyBytes ? n : 0;
 }
 
 tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_heads, const tf_q8_cache *cache_host,
@@ -35,12 +36,13 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
     if (n_segs == 0 || n_rows_total == 0) return TF_OK;
     if (!q || !page_table || !segs || !workspace || !out || !flags || !status || !q8_pointers(c)) return TF_ERR_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !q8_aligned(c)) return TF_ERR_ALIGN;
-    if (workspace_bytes < tf_paged_attn_q8_workspace_bytes(n_rows_total, n_q_heads, c.head_dim, n_splits_max))
+    if (workspace_bytes < part_bytes(n_rows_total, n_q_heads, c.head_dim, n_splits_max))
         return TF_ERR_WORKSPACE;
     const int group = n_q_heads / c.n_kv_heads;
     int max_rows = n_rows_total, splits = n_splits_max, split = split_keys;
     bool ws = false;  // decode-shaped: the warp-specialized kernel
     if (segs_host) {
+        if (!keys_taken(segs_host, n_segs)) return TF_ERR_UNSUPPORTED;
         rc = check_segs_host(segs_host, n_segs, n_rows_total, page_table_len, c.page_size, c.n_pages, page_table_host,
                              split_keys, n_splits_max, &max_rows, full != 0);
         if (rc != TF_OK) return rc;
@@ -84,6 +86,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         w.k_scale = c.k_scale;
         w.v_scale = c.v_scale;
         w.max_rows = max_rows;
+        w.max_keys = kMaxKeys;
         w.scale_log2 = scale_log2;
         w.split_keys = split;
         w.n_splits_max = splits;
@@ -155,6 +158,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         p.n_pages = c.n_pages;
         p.log2_page = lp;
         p.pt_len = page_table_len;
+        p.max_keys = kMaxKeys;
         p.page_table = page_table;
         p.segs = segs;
         p.scale_log2 = scale_log2;

@@ -55,8 +55,9 @@ extern "C" {
 size_t tf_paged_attn_shared_workspace_bytes(int32_t n_rows_total, int32_t n_q_heads, int32_t head_dim,
                                             int32_t n_prefix_splits, int32_t n_splits_max) {
     if (n_rows_total < 0 || n_q_heads <= 0 || head_dim <= 0 || n_prefix_splits <= 0 || n_splits_max <= 0) return 0;
-    return part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits) +
-           part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+    const size_t n = part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits) +
+                     part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max);
+    return n < kTooManyBytes ? n : 0;
 }
 
 tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
@@ -82,14 +83,15 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         return TF_ERR_ARG;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out) || !aligned16(workspace))
         return TF_ERR_ALIGN;
-    if (workspace_bytes < tf_paged_attn_shared_workspace_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits,
-                                                              n_splits_max))
+    if (workspace_bytes < part_bytes(n_rows_total, n_q_heads, head_dim, n_prefix_splits) +
+                              part_bytes(n_rows_total, n_q_heads, head_dim, n_splits_max))
         return TF_ERR_WORKSPACE;
     const int group = n_q_heads / n_kv_heads;
     int max_rows = n_rows_total, own_splits = n_splits_max, own_split = split_keys;
     int pre_rows = n_rows_total, pre_splits = n_prefix_splits, pre_split = split_keys;
     // a table's checks, its split size and the partial slots it needs
     auto plan = [&](const tf_seg *host, int n, bool full, int &rows, int &splits, int &split) -> tf_status {
+        if (!keys_taken(host, n)) return TF_ERR_UNSUPPORTED;
         const tf_status rc = check_segs_host(host, n, n_rows_total, page_table_len, page_size, n_pages,
                                              page_table_host, split_keys, splits, &rows, full);
         if (rc != TF_OK || rows == 0) return rc;
@@ -125,14 +127,14 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
     const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                         n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
                                         page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
-                                        status, stream);
+                                        status, stream, false, kMaxKeys);
     if (rc != TF_OK) return rc;
 
     if (n_prefixes > 0 && pre_rows > 0) {
         const tf_status rc = paged_partials(true, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                             n_kv_heads, head_dim, page_table, page_table_len, prefixes, n_prefixes,
                                             prefixes_host, page_table_host, scale, pre_split, pre_splits, pre.o,
-                                            pre.m, pre.l, pre.flag, status, stream, true);
+                                            pre.m, pre.l, pre.flag, status, stream, true, kMaxKeys);
         if (rc != TF_OK) return rc;
     }
     MergeSegsParams m{};

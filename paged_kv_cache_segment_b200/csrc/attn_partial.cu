@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
         w.n_pg = sg.n_pages;
         const bool bad = w.q_row < 0 || w.n_rows < 0 || (int64_t)w.q_row + w.n_rows > p.n_rows_total ||
                          w.n_keys < (p.full ? (w.n_rows > 0 ? 1 : 0) : w.n_rows) || w.pt_base < 0 || w.n_pg < 0 ||
-                         (int64_t)w.pt_base + w.n_pg > p.pt_len;
+                         (int64_t)w.pt_base + w.n_pg > p.pt_len ||
+                         (!p.seg_inline && w.n_keys > p.max_keys);
         if (bad) {
             if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
             return;
@@ -233,12 +234,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
             if (tid == 0) atomicOr(p.status, TF_DEV_PAST_PAGES);
             return;
         }
-        if (p.split_keys > 0) {
-            per = p.split_keys;
-        } else {
-            per = (w.n_keys + p.n_splits_max - 1) / p.n_splits_max;
-            per = ((per + (1 << p.log2_page) - 1) >> p.log2_page) << p.log2_page;
-        }
+        per = p.split_keys > 0 ? p.split_keys : even_split(w.n_keys, p.n_splits_max, p.log2_page);
     } else {
         const tf_ring_seg rs = p.rsegs[w.s];
         w.q_row = rs.q_row;
@@ -258,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
         per = p.split_keys;
     }
     if (w.n_rows == 0) return;
-    const int n_sp = (w.n_keys + per - 1) / per;
+    const int n_sp = splits_of(w.n_keys, per);
     if (n_sp > p.n_splits_max) {
         if (tid == 0) atomicOr(p.status, TF_DEV_SPLITS);
         return;
@@ -281,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
         return;
     }
     w.key_lo = w.c * per;
-    w.key_hi = min(w.n_keys, w.key_lo + per);
+    w.key_hi = split_end(w.n_keys, w.key_lo, per);
     const int i_min = w.q0 / p.group, i_max = (w.q0 + w.nq - 1) / p.group;
     // keys every row sees: [0, causal0) (with the full flag: all of them)
     const int causal0 = p.full ? w.n_keys : w.n_keys - w.n_rows + 1;

@@ -28,9 +28,9 @@ namespace tfp {
 namespace {
 
 // Partials an entry's rows have (0: a bad entry, no keys, or more rows than the
-// partials' launch was sized for, which only this kernel reports).
+// partials' launch was sized for or more keys than a call takes, which this kernel reports).
 __device__ __forceinline__ int seg_parts(const tf_seg &e, const PartSet &s, const MergeSegsParams &p, bool full) {
-    if (e.n_rows > s.max_rows) {
+    if (e.n_rows > s.max_rows || e.n_keys > kMaxKeys) {
         atomicOr(p.status, TF_DEV_BAD_SEG);
         return 0;
     }

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
             n_pg = sg.n_pages;
             const int keys_needed = p.full ? (T > 0 ? 1 : 0) : T;  // the causal count needs a key per row
             const bool bad = q_row < 0 || T < 0 || (int64_t)q_row + T > p.n_rows_total || N < keys_needed ||
-                             pt_base < 0 || n_pg < 0 || (int64_t)pt_base + n_pg > p.pt_len;
+                             pt_base < 0 || n_pg < 0 || (int64_t)pt_base + n_pg > p.pt_len || N > p.max_keys;
             if (bad) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
                 leave();
@@ -208,14 +208,14 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
                 leave();
                 return;
             }
-            n_sp = (N + p.split_keys - 1) / p.split_keys;
+            n_sp = splits_of(N, p.split_keys);
             if (n_sp > p.n_splits_max) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_SPLITS);
                 leave();
                 return;
             }
-            key_lo = split * p.split_keys;
-            key_hi_split = min(N, key_lo + p.split_keys);
+            key_lo = split < n_sp ? split * p.split_keys : N;
+            key_hi_split = split_end(N, key_lo, p.split_keys);
         }
         if (qt * RT >= T) {
             leave();

@@ -9,6 +9,26 @@
 
 namespace tfp {
 
+// The most keys of a stream (or prefix) in tf_paged_attn_q8 and
+// tf_paged_attn_shared: keys and their tiles' ends then stay below 2^31.
+constexpr int kMaxKeys = 1 << 30;
+
+// The keys a partial covers where none are given: n_keys in n_splits parts,
+// rounded up to whole pages.
+__host__ __device__ inline int even_split(int n_keys, int n_splits, int log2_page) {
+    const uint32_t per = ((uint32_t)n_keys + (uint32_t)n_splits - 1u) / (uint32_t)n_splits;
+    const uint32_t len = (per + (1u << log2_page) - 1u) >> log2_page << log2_page;
+    return len > 0x7fffffffu ? 0x7fffffff : (int)len;
+}
+// Partials of `per` keys that n_keys take (a sum of two ints may pass 2^31, not 2^32).
+__host__ __device__ inline int splits_of(int n_keys, int per) {
+    return (int)(((uint32_t)n_keys + (uint32_t)per - 1u) / (uint32_t)per);
+}
+// The end of the partial that starts at key_lo.
+__host__ __device__ inline int split_end(int n_keys, int key_lo, int per) {
+    return per < n_keys - key_lo ? key_lo + per : n_keys;
+}
+
 // Parameters of the split-KV attention kernel (paged or ring source).
 struct AttnParams {
     const uint16_t *q;
@@ -19,6 +39,7 @@ struct AttnParams {
     int kv_type;
     // paged source
     int n_pages, log2_page, pt_len;
+    int max_keys;  // an entry of more is bad
     const int32_t *page_table;
     const tf_seg *segs;
     tf_seg seg0;     // used instead of segs[0] when seg_inline != 0 (one-stream prompt calls)
@@ -69,6 +90,7 @@ struct PromptTcParams {
     // split-KV partials: segment table, splits, q-tiles of the grid, outputs
     const tf_seg *segs;
     int pt_len, split_keys, n_splits_max, n_qt;
+    int max_keys;  // an entry of more is bad
     int full;  // every row sees all of its stream's keys (no causal count)
     // partials that run beside the partial kernel launched before this one: as
     // its programmatic dependent, waiting for that grid only at the end, so that
@@ -130,6 +152,7 @@ struct WsParams {
     const tf_seg *segs;
     const int32_t *page_table;
     int n_pages, log2_page, pt_len;
+    int max_keys;  // an entry of more is bad
     // ring
     const tf_ring_seg *rsegs;
     int64_t ring_slots_total;
@@ -168,13 +191,14 @@ uint64_t test_wait_runout_ns();
 // Split-KV partials of tf_paged_attn_decode / tf_paged_attn_block, arguments
 // checked (csrc/api.cu).  `beside`: the launch before it on the stream is another
 // call of this function, whose outputs it neither reads nor writes; the
-// tensor-core kernel then runs beside it (PromptTcParams::beside).
+// tensor-core kernel then runs beside it (PromptTcParams::beside).  `max_keys`: the
+// most keys an entry on the device may have (a host table is the caller's to check).
 tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                          const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
                          const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
                          const tf_seg *segs_host, const int32_t *page_table_host, float scale, int32_t split_keys,
                          int32_t n_splits_max, float *part_o, float *part_m, float *part_l, uint8_t *part_flag,
-                         uint32_t *status, tf_stream_t stream, bool beside = false);
+                         uint32_t *status, tf_stream_t stream, bool beside = false, int max_keys = 0x7fffffff);
 
 // Partials of one kind for the merge of tf_paged_attn_q8 and
 // tf_paged_attn_shared: arrays [n_rows_total][hq][n_splits](*D), of which a row

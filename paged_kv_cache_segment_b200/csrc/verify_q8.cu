@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     {
         const bool bad = q_row < 0 || T < 0 || (int64_t)q_row + T > p.n_rows_total ||
                          N < (p.full ? (T > 0 ? 1 : 0) : T) || pt_base < 0 || n_pg < 0 ||
-                         (int64_t)pt_base + n_pg > p.pt_len || T > p.max_rows;
+                         (int64_t)pt_base + n_pg > p.pt_len || T > p.max_rows || N > kMaxKeys;
         uint32_t bit = 0;
         if (bad)
             bit = TF_DEV_BAD_SEG;

@@ -45,7 +45,8 @@ __device__ __forceinline__ int ws_stream_splits(const WsParams &p, int s, uint32
         const tf_seg e = p.segs[s];
         const bool bad = e.q_row < 0 || e.n_rows < 0 || (int64_t)e.q_row + e.n_rows > p.n_rows_total ||
                          e.n_keys < (p.full ? (e.n_rows > 0 ? 1 : 0) : e.n_rows) || e.pt_base < 0 || e.n_pages < 0 ||
-                         (int64_t)e.pt_base + e.n_pages > p.pt_len || (p.max_rows > 0 && e.n_rows > p.max_rows);
+                         (int64_t)e.pt_base + e.n_pages > p.pt_len ||
+                         e.n_keys > p.max_keys || (p.max_rows > 0 && e.n_rows > p.max_rows);
         if (bad) {
             bits |= TF_DEV_BAD_SEG;
             return 0;
@@ -56,11 +57,8 @@ __device__ __forceinline__ int ws_stream_splits(const WsParams &p, int s, uint32
         }
         if (e.n_rows == 0 || e.n_rows * p.group > kWsQ) return 0;
         int per = p.split_keys;
-        if (per <= 0) {
-            per = (e.n_keys + p.n_splits_max - 1) / p.n_splits_max;
-            per = ((per + (1 << p.log2_page) - 1) >> p.log2_page) << p.log2_page;
-        }
-        const int n = (e.n_keys + per - 1) / per;
+        if (per <= 0) per = even_split(e.n_keys, p.n_splits_max, p.log2_page);
+        const int n = splits_of(e.n_keys, per);
         if (n > p.n_splits_max) {
             bits |= TF_DEV_SPLITS;
             return 0;
@@ -85,13 +83,8 @@ __device__ __forceinline__ int ws_split_len(const WsParams &p, int s) {
     if constexpr (RING) {
         return p.split_keys;
     } else {
-        int per = p.split_keys;
-        if (per <= 0) {
-            const tf_seg e = p.segs[s];
-            per = (e.n_keys + p.n_splits_max - 1) / p.n_splits_max;
-            per = ((per + (1 << p.log2_page) - 1) >> p.log2_page) << p.log2_page;
-        }
-        return per;
+        const int per = p.split_keys;
+        return per > 0 ? per : even_split(p.segs[s].n_keys, p.n_splits_max, p.log2_page);
     }
 }
 
@@ -147,12 +140,9 @@ __device__ __forceinline__ WsItem ws_resolve(const WsParams &p, const int *prefi
         it.pt_base = e.pt_base;
         it.n_pg = e.n_pages;
         int per = p.split_keys;
-        if (per <= 0) {
-            per = (e.n_keys + p.n_splits_max - 1) / p.n_splits_max;
-            per = ((per + (1 << p.log2_page) - 1) >> p.log2_page) << p.log2_page;
-        }
+        if (per <= 0) per = even_split(e.n_keys, p.n_splits_max, p.log2_page);
         it.key_lo = it.c * per;
-        it.key_hi = min(it.n_keys, it.key_lo + per);
+        it.key_hi = split_end(it.n_keys, it.key_lo, per);
         it.base = 0;
         it.size = it.start = 0;
         it.wrap_at = 0x7fffffff;

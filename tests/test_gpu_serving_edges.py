@@ -310,3 +310,55 @@ def test_a_damaged_entry_touches_its_own_rows_only(hq, hkv, held, keys, dt):
         case(put(3, 0, n - 1), slice(n - 1, n))  # past the last one
     case(put(1, 4, 0), slice(q1, q1 + held), binding.TF_DEV_PAST_PAGES)
     case(put(3, 3, -1), slice(q3, q3 + held))
+
+
+@pytest.mark.parametrize("hq,hkv,rows,keys,host", [(8, 2, 1, 60, True), (8, 2, 1, 1500, True), (16, 2, 12, 60, True),
+                                                   (16, 2, 12, 1500, True), (12, 1, 3, 300, True), (8, 2, 1, 60, False)])
+def test_a_device_entry_of_two_billion_keys_is_refused(hq, hkv, rows, keys, host):
+    """A page table of 2^21 entries, all of one page of 1,024 keys, and an entry on the device that names all of its
+    2^31 - 1 keys: past what a call takes, reported and flagged, the other stream as it should be."""
+    b, sides, c = q8_batch("int8", 16, rows=[rows, rows], keys=[keys, keys // 2], n_q_heads=hq, n_kv_heads=hkv,
+                           head_dim=128, page_size=1024)
+    n, _, d = b.q.shape
+    pt = torch.full((1 << 21,), int(b.page_table[0]), dtype=torch.int32, device=DEV)
+    pt[: len(b.page_table)] = dev(b.page_table)
+    segs = b.segs.copy()
+    segs[1] = [rows, rows, 2**31 - 1, 0, 1 << 21]
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(n, hq, d, 64), dtype=torch.uint8, device=DEV)
+    for split in (0, 1 << 30):
+        out, fl = torch.full((n, hq, d), 5.0, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV)
+        st = status_word()
+        tf.tf_paged_attn_q8(dev(b.q), c, pt, dev(segs), scale=b.scale, n_splits_max=64, split_keys=split, workspace=ws,
+                            out=out, flags=fl, status=st, segs_host=b.segs if host else None)
+        ref, rf, vmax = reference(b, sides, "int8")
+        assert int(st.item()) == binding.TF_DEV_BAD_SEG
+        out, fl = out.cpu().numpy(), fl.cpu().numpy()
+        sv.check_attention(out[:rows], fl[:rows], ref[:rows], rf[:rows], vmax, False)
+        assert np.isnan(out[rows:]).all() and (fl[rows:] == 1).all()
+
+
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 8, 2), (12, 16, 2), (3, 12, 1)])
+@pytest.mark.parametrize("prefix", [False, True])
+def test_a_shared_device_entry_of_two_billion_keys_is_refused(rows, hq, hkv, prefix):
+    b, prefixes, segs = batch(19, [300], [0, 0], [rows] * 2, [200, 100], hq, hkv, 128, 1024)
+    n, _, d = b.q.shape
+    pt = torch.full((1 << 21,), int(b.page_table[0]), dtype=torch.int32, device=DEV)
+    pt[: len(b.page_table)] = dev(b.page_table)
+    dpre, dsegs = prefixes.copy(), segs.copy()
+    if prefix:
+        dpre[0, 2:] = [2**31 - 1, 0, 1 << 21]
+    else:
+        dsegs[1, 2:] = [2**31 - 1, 0, 1 << 21]
+    ws = torch.empty(tf.tf_paged_attn_shared_workspace_bytes(n, hq, d, 8, 8), dtype=torch.uint8, device=DEV)
+    out, fl = torch.full((n, hq, d), 5.0, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV)
+    st = status_word()
+    tf.tf_paged_attn_shared(dev(b.q), dev(b.k_pool), dev(b.v_pool), pt, dev(dpre), dev(dsegs), scale=b.scale,
+                            n_prefix_splits=8, n_splits_max=8, workspace=ws, out=out, flags=fl, status=st,
+                            prefixes_host=prefixes, segs_host=segs)
+    assert int(st.item()) & binding.TF_DEV_BAD_SEG
+    gone = slice(0, n) if prefix else slice(rows, n)
+    out, fl = out.cpu().numpy(), fl.cpu().numpy()
+    assert np.isnan(out[gone]).all() and (fl[gone] == 1).all()
+    if not prefix:
+        ref, rf, vmax = shared_reference(b, prefixes, segs, [0, 0])
+        sv.check_attention(out[:rows], fl[:rows], ref[:rows], rf[:rows], vmax, False)

@@ -138,6 +138,28 @@ def test_attention_checks():
     assert attn(full=1, segs_host=host(np.array([[0, 2, 0, 0, 3], [1, 0, 0, 3, 5]], np.int32))) == 1
 
 
+def test_lengths_and_workspaces_past_their_limits():
+    """2^30 keys a stream or prefix; sizes whose products pass 64 bits."""
+    long = np.array([[0, 1, 37, 0, 3], [1, 1, 2**31 - 1, 3, 1 << 21]], np.int32)
+    over = np.array([[0, 1, 37, 0, 3], [1, 1, 2**30 + 1, 3, 1 << 21]], np.int32)
+    big = dict(pt_len=(1 << 21) + 3)
+    for table in (long, over):
+        for split, nsm in ((0, 4), (1 << 30, 4), (0, 1)):
+            kw = dict(big, split=split, nsm=nsm)
+            assert attn(segs_host=host(table), cache_kw=dict(page_size=1024), **kw) == 4
+            assert shared(segs_host=host(table), psz=1024, **kw) == 4
+            assert shared(pre_host=host(table), n_pre=2, segs_host=host(SEGS), psz=1024, **kw) == 4
+    most = 2**31 - 1
+    for n in (most, 1 << 24):
+        assert tf.tf_paged_attn_q8_workspace_bytes(most, 1 << 20, 256, n) == 0
+        assert tf.tf_paged_attn_shared_workspace_bytes(most, 1 << 20, 256, n, 1) == 0
+        assert tf.tf_paged_attn_shared_workspace_bytes(most, 1 << 20, 256, 1, n) == 0
+    assert tf.tf_paged_attn_q8_workspace_bytes(1 << 20, 64, 256, 64) == (1 << 32) * (256 * 4 + 9)
+    # 2^16 rows x 2^20 heads x 2^24 partials: 2^60 partials, whose bytes were taken modulo 2^64
+    assert attn(rows=1 << 16, hq=1 << 20, nsm=1 << 24, cache_kw=dict(head_dim=256)) == 7
+    assert shared(rows=1 << 16, hq=1 << 20, nsm=1 << 24, d=256) == 7
+
+
 def test_shared_prefix_checks():
     pre = np.array([[0, 2, 40, 0, 3]], np.int32)
     ok = dict(segs_host=host(SEGS))
