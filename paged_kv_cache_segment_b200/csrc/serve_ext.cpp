@@ -288,9 +288,9 @@ PyObject *logprob(PyObject *, Args a, Py_ssize_t n) {
             must(l.n() == rows, per_row);
             lse = (float *)l.p;
         }
+        const char *top = "top_ids and top_logprobs must be [rows][top_k], both or neither";
+        must((a[7] == Py_None) == (a[8] == Py_None), top);
         if (a[7] != Py_None) {
-            const char *top = "top_ids and top_logprobs must be [rows][top_k]";
-            must(a[8] != Py_None, top);
             const Arg i(a[7], "top_ids", kI32, dev), t(a[8], "top_logprobs", kF32, dev);
             must(i.t->dim() == 2 && i.dim(0) == rows && t.t->sizes() == i.t->sizes(), top);
             k = len32(i.dim(1));

@@ -281,3 +281,14 @@ def test_a_cold_row_of_logits_from_end_to_end(dtype, rows, cols):
             assert (np.isneginf(g) == np.isneginf(w)).all()
             ok = np.isfinite(w)
             assert (np.abs(g[:, ok] - w[ok]) <= 2.0**-23 * np.abs(w[ok])).all()
+
+
+def test_alternatives_need_both_of_their_outputs():
+    x = torch.zeros((2, 10), device=DEV)
+    tok = torch.zeros((2, 1), device=DEV, dtype=torch.int32)
+    kw = dict(token_logprobs=torch.empty((2, 1), device=DEV), flags=torch.empty(2, device=DEV, dtype=torch.uint8),
+              status=status_word())
+    with pytest.raises(ValueError, match="both or neither"):
+        tf.tf_logprob_rows(x, tok, top_logprobs=torch.empty((2, 3), device=DEV), **kw)
+    with pytest.raises(ValueError, match="both or neither"):
+        tf.tf_logprob_rows(x, tok, top_ids=torch.empty((2, 3), device=DEV, dtype=torch.int32), **kw)
