@@ -95,11 +95,6 @@ __device__ __forceinline__ uint64_t key64(float x, int col) {
     const uint32_t k = key32(x);
     return k == 0u ? 0ull : ((uint64_t)k << 32) | (uint32_t)~col;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 // A row's running statistics: the largest logit, sum 2^(c (x - m)), and the same
 // sum weighted by x - m.

@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
     __shared__ uint32_t s_tmem, s_err, s_abort;
     __shared__ float s_xmax[2][2][kM];      // [tile parity][column half][row]: the largest score
     __shared__ float s_ymax[2][kM];         // [column half][row]: the largest score + value exponent
-    __shared__ uint32_t s_xv[2][2][4];      // [tile parity][column half][warp pair]: the tile's largest value scale byte
     __shared__ float s_xl[2][kM];           // [column half][row]: final partial sums
     __shared__ uint32_t s_x[2][2][kM];      // [exchange][column half][row]: row maxima of Q, findings
     __shared__ uint32_t s_vnan[kFactors][2];  // value rows marked nonfinite, a bit a key
@@ -494,7 +493,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             const int b = j & 1, kt = key_lo + j * kN;
             const uint32_t colS = b ? kColS1 : kColS0;
             const int kh = kt + 32 * h;
-            vq_wait(bar(kBarS + b), (uint32_t)((j >> 1) & 1), abort_flag, lim);
+            const bool there = vq_wait(bar(kBarS + b), (uint32_t)((j >> 1) & 1), abort_flag, lim);
             tc_fence_after();
             float sv[32];
             {
@@ -537,12 +536,12 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 for (uint32_t v = vnan; v; v &= v - 1)
                     if (kh + __ffs(v) - 1 < lim_k) tail_bad = 1;
             }
-            // (the scale byte too, so that both warps of a pair decide alike below, where they
-            // meet at a barrier: once a wait has run out the converters may be rewriting it)
-            s_xmax[b][h][qi] = mx;
-            if (lane == 0) s_xv[b][h][quad] = s_vmax[fs][h];
+            // (NaN where the wait for the scores gave up, for both warps of the pair: no reference
+            // moves.  They have to decide alike below, where they meet at a barrier, and s_vmax
+            // is the same for both only while the tile's scores are there)
+            s_xmax[b][h][qi] = there ? mx : __int_as_float(0x7fc00000);
             named_bar_sync(pair_bar, 64);
-            mx = fmaxf(mx, s_xmax[b][h ^ 1][qi]);
+            mx = max_nan(there ? mx : __int_as_float(0x7fc00000), s_xmax[b][h ^ 1][qi]);
             // lazy references: they move when a term would pass 2^15 (both halves see
             // the same maxima, so they move together)
             if (mx > m_ref + kRefTop) {
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             float alpha = 1.f;
             // score + value exponent is at most mx + vmax: its own maximum is
             // looked for only when that bound is past the reference
-            const float vmax = (float)((int)max(s_xv[b][0][quad], s_xv[b][1][quad]) - kE8Bias);
+            const float vmax = (float)((int)max(s_vmax[fs][0], s_vmax[fs][1]) - kE8Bias);
             if (__any_sync(0xffffffffu, mx + vmax > r_ref + kRefTop)) {
                 float my = -INFINITY;
 #pragma unroll
