@@ -452,19 +452,23 @@ __global__ void __launch_bounds__(Q8Cfg<D>::kThreads, Q8Cfg<D>::kMinBlocks)
                         float x0, x1, x2, x3;
                         unpk2(xa, x0, x1);
                         unpk2(xb, x2, x3);
-                        float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
-                        float b0 = fmaxf(x0 + fva, x2 + fvb), b1 = fmaxf(x1 + fva, x3 + fvb);
+                        auto rows_max = [](float &a, float &b) {  // over the warp's keys
 #pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) {
-                            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, s));
-                            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, s));
-                            b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, s));
-                            b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, s));
-                        }
-                        // to the tile's largest score and score + scale; the factors of what was summed so far
-                        auto move = [](float &m, float &r, float top, float both, float &fo) -> float {
-                            const float n = fmaxf(m, top - kRefLift), down = m - n;
-                            const float rn = fmaxf(ceilf(both - n) - kRefLift, ceilf(down + r));
+                            for (int s = 4; s < 32; s <<= 1) {
+                                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, s));
+                                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, s));
+                            }
+                        };
+                        // to the tile's largest score and, beside it (large scores would round the
+                        // exponents away), score + scale; the factors of what was summed so far
+                        float a0 = fmaxf(x0, x2), a1 = fmaxf(x1, x3);
+                        rows_max(a0, a1);
+                        a0 = fmaxf(m0, a0 - kRefLift);
+                        a1 = fmaxf(m1, a1 - kRefLift);
+                        float b0 = fmaxf(x0 - a0 + fva, x2 - a0 + fvb), b1 = fmaxf(x1 - a1 + fva, x3 - a1 + fvb);
+                        rows_max(b0, b1);
+                        auto move = [](float &m, float &r, float n, float both, float &fo) -> float {
+                            const float down = m - n, rn = fmaxf(ceilf(both) - kRefLift, ceilf(down + r));
                             fo = ex2(down + (r - rn));
                             m = n;
                             r = rn;

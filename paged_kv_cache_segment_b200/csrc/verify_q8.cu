@@ -442,6 +442,8 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         const bool valid_row = row_i < T;
         const int lim_k = valid_row && !p.full ? min(key_hi_eff, causal0 + row_i) : key_hi_eff;
         const uint32_t pair_bar = 2 + quad;
+        // m_ref: reference of the scores; m_ref + r_ref: that of score + value exponent (base 2
+        // both; r_ref apart, or exponents would round away beside large scores)
         float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
         uint32_t emax = 0, tail_bad = 0, lane_base = 0;
         float fq;  // scale * log2(e) over the row's power of two
@@ -542,49 +544,60 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             s_xmax[b][h][qi] = there ? mx : __int_as_float(0x7fc00000);
             named_bar_sync(pair_bar, 64);
             mx = max_nan(there ? mx : __int_as_float(0x7fc00000), s_xmax[b][h ^ 1][qi]);
+            // large scores are rounded before the reference is taken off them: fq times the sums,
+            // unrounded, may lie any distance from a reference of their own rounding
+            float f = fq;
+            if (__any_sync(0xffffffffu, fabsf(mx) >= 0x1p20f)) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sv[c] *= fq;
+                f = 1.f;
+            }
+            const uint64_t fq2 = pk2(f, f);
             // lazy references: they move when a term would pass 2^15 (both halves see
             // the same maxima, so they move together)
-            if (mx > m_ref + kRefTop) {
-                l_run *= ex2(m_ref - (mx - kRefLift));
-                m_ref = mx - kRefLift;
+            if (mx - m_ref > kRefTop) {
+                const float n = mx - kRefLift, down = m_ref - n;
+                l_run *= ex2(down);
+                r_ref += down;
+                m_ref = n;
             }
-            const uint64_t fq2 = pk2(fq, fq);
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+            const uint64_t nmu2 = pk2(-mu, -mu);
             float alpha = 1.f;
             // score + value exponent is at most mx + vmax: its own maximum is
             // looked for only when that bound is past the reference
             const float vmax = (float)((int)max(s_vmax[fs][0], s_vmax[fs][1]) - kE8Bias);
-            if (__any_sync(0xffffffffu, mx + vmax > r_ref + kRefTop)) {
+            if (__any_sync(0xffffffffu, mx - mu + vmax - r_ref > kRefTop)) {
                 float my = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const float4 v4 = fv[q];
                     float y0, y1, y2, y3;
-                    unpk2(fma2(pk2(sv[4 * q], sv[4 * q + 1]), fq2, pk2(v4.x, v4.y)), y0, y1);
-                    unpk2(fma2(pk2(sv[4 * q + 2], sv[4 * q + 3]), fq2, pk2(v4.z, v4.w)), y2, y3);
+                    unpk2(add2(fma2(pk2(sv[4 * q], sv[4 * q + 1]), fq2, nmu2), pk2(v4.x, v4.y)), y0, y1);
+                    unpk2(add2(fma2(pk2(sv[4 * q + 2], sv[4 * q + 3]), fq2, nmu2), pk2(v4.z, v4.w)), y2, y3);
                     my = max3(my, max3(y0, y1, y2), y3);
                 }
                 s_ymax[h][qi] = my;
                 named_bar_sync(pair_bar, 64);
                 my = fmaxf(my, s_ymax[h ^ 1][qi]);
-                if (my > r_ref + kRefTop) {
+                if (my - r_ref > kRefTop) {
                     alpha = ex2(r_ref - (my - kRefLift));
                     r_ref = my - kRefLift;
                 }
             }
-            const float mu = m_ref == -INFINITY ? 0.f : m_ref, ru = r_ref == -INFINITY ? 0.f : r_ref;
+            const float ru = r_ref == -INFINITY ? 0.f : r_ref;
             {
                 uint32_t hi[16], lo[16];
                 uint64_t ls2 = 0;  // two zeros
-                const uint64_t nmu2 = pk2(-mu, -mu);
                 auto split = [&](int c, float w0, float w1) {
                     hi[c / 2] = pack_f16x2(w0, w1);
                     const float2 f = f16x2_to_f32(hi[c / 2]);
                     lo[c / 2] = pack_f16x2(w0 - f.x, w1 - f.y);
                 };
-                if (__all_sync(0xffffffffu, vmax + mu - ru <= 90.f)) {
-                    // a weight is its probability times 2^(e + mu - ru): a probability
+                if (__all_sync(0xffffffffu, vmax - ru <= 90.f)) {
+                    // a weight is its probability times 2^(e - ru): a probability
                     // below the floats would give one below 2^-36
-                    const float rho = ex2(mu - ru);
+                    const float rho = ex2(-ru);
                     const uint64_t rho2 = pk2(rho, rho);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -608,11 +621,11 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
                             const int c = 4 * q + i;
-                            const uint64_t x2 = pk2(sv[c], sv[c + 1]);
+                            const uint64_t d2 = fma2(pk2(sv[c], sv[c + 1]), fq2, nmu2);
                             float p0, p1, w0, w1;
-                            unpk2(fma2(x2, fq2, nmu2), p0, p1);
+                            unpk2(d2, p0, p1);
                             ls2 = add2(ls2, pk2(ex2(p0), ex2(p1)));
-                            unpk2(fma2(x2, fq2, add2(i ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y), nru2)), w0, w1);
+                            unpk2(add2(d2, add2(i ? pk2(v4.z, v4.w) : pk2(v4.x, v4.y), nru2)), w0, w1);
                             split(c, ex2(w0), ex2(w1));
                         }
                     }
@@ -654,8 +667,8 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         const float l_sum = s_xl[0][qi] + s_xl[1][qi];
         uint32_t bad = s_x[1][0][qi] | s_x[1][1][qi] | s_err | (aborted ? 1u : 0u) | (isfinite(l_sum) ? 0u : 1u);
         const int64_t at = ((int64_t)(q_row + row_i) * p.hq + g * G + qi % G) * p.n_splits + split;
-        // 2^(r - m) in two steps: it may itself be past the floats where o is small
-        const float gf = r_ref == -INFINITY ? 0.f : ex2(0.5f * (r_ref - (m_ref == -INFINITY ? 0.f : m_ref)));
+        // 2^r in two steps: it may itself be past the floats where o is small
+        const float gf = r_ref == -INFINITY ? 0.f : ex2(0.5f * r_ref);
         const int d0 = h * (D / 2);
         if (p.out) {
             // ---- one split: normalise, look the row over, write it

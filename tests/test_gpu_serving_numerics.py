@@ -92,3 +92,45 @@ def test_value_scales_and_scores_far_from_one(kind, rows, hq, hkv):
     ref, _ = sv.attend(sv.bf16(b.q), k, v, [n - rows + i + 1 for i in range(rows)], b.scale)
     err = np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
     assert err.max() <= 2.0**-15, err.max()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,hq,hkv,d,n,split", [(1, 8, 2, 64, 300, 0), (1, 8, 2, 128, 120, 128), (2, 4, 1, 256, 700, 256),  # decode
+                                                   (12, 4, 2, 64, 300, 64), (5, 8, 2, 128, 120, 128),  # tcgen05
+                                                   (9, 2, 1, 256, 700, 256), (9, 2, 1, 256, 700, 704)])
+@pytest.mark.parametrize("size", [2.0**18, 2.0**23, 2.0**26, 2.0**27, 2.0**28, 2.0**31, 2.0**40, 2.0**90, -(2.0**28), -(2.0**35)])
+def test_scores_of_any_size(kind, rows, hq, hkv, d, n, split, size):
+    """Scores of up to 2^90: two keys share the largest, `size` (or the smallest magnitude of the negative ones), all
+    others are 7/8 of it or less (for a negative one, 9/8 of it), 2^15 below even at 2^18, so the two weigh 1/2 each and
+    nothing else weighs anything.  Every score is the exact sum of two products (of 20 bits, so that the scale's product
+    with it is rounded), the two keys' are the same float, and their value rows differ in scale by 2^12 in columns of
+    their own.  So each column is one weight (22 bits, half of a step off, and the floats' ex2, good to 2^-22, twice)
+    times one value, over a sum of two: 2^-20 of it."""
+    psz = 32
+    b = wl.make_paged_batch(19, rows=[rows], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=psz,
+                            unused="normal")
+    rng = np.random.default_rng(20)
+    sign, mag = np.sign(size), abs(size)
+    steps = rng.choice([0.25, 0.5, 0.75, 0.875] if sign > 0 else [1.125, 1.25, 1.5, 1.75], size=n)
+    one, two = n // 2 - n // 2 % 64 + 11, n // 2 - n // 2 % 64 + 43  # the two halves of a tile
+    steps[[one, two]] = 1.0
+    k, v = np.zeros(b.k_pool.shape, np.float32), np.zeros(b.v_pool.shape, np.float32)
+    for j in range(n):
+        page = b.page_table[b.segs[0][3] + j // psz]
+        k[page, :, j % psz, 3:5] = sign * steps[j], sign * 0.8125
+        v[page, :, j % psz] = 3.0
+    for j, col, x in ((one, 1, 1.75), (two, 2, 1.5 * 2.0**-12)):
+        page = b.page_table[b.segs[0][3] + j // psz]
+        v[page, :, j % psz] = 0.0
+        v[page, :, j % psz, col] = x
+    sides = [sv.quantise(wl.f32_to_bf16_bits(x), kind) for x in (k, v)]
+    q = np.zeros((rows, hq, d), np.float32)
+    q[..., 3] = mag * 2.0 ** -np.floor(np.log2(b.scale))
+    q[..., 4] = q[..., 3] * 2.0**-9 * 175 / 128
+    b.q = wl.f32_to_bf16_bits(q)
+    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
+    out, flags, st = attn(c, b, kind, split=split, n_splits_max=-(-n // split) if split else 16)
+    assert st == 0 and (flags == 0).all()
+    want = np.zeros(d)
+    want[1], want[2] = 1.75 / 2, 1.5 * 2.0**-12 / 2
+    assert (np.abs(out.astype(np.float64) - want) <= 2.0**-20 * want).all(), out[0, 0, :4]
