@@ -134,3 +134,22 @@ def test_scores_of_any_size(kind, rows, hq, hkv, d, n, split, size):
     want = np.zeros(d)
     want[1], want[2] = 1.75 / 2, 1.5 * 2.0**-12 / 2
     assert (np.abs(out.astype(np.float64) - want) <= 2.0**-20 * want).all(), out[0, 0, :4]
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 2, 128), (4, 4, 256)])
+def test_a_long_decode_sum_is_rounded_not_truncated(kind, hq, hkv, d):
+    """All values 1.75 and scores of all sizes: the output is 1.75, from 4,096 weights summed twice (with the values and
+    without).  A tile's 16 keys a warp are summed by the matrix unit, which truncates, twice: 2^-22 of them and of the
+    whole.  The 64 tiles' sums are rounded, by half a step each way: 8 of 64 roundings' size, 2^-25 sqrt(64) / 2 for
+    sums that grow evenly, over four warps' sums halved again, 2^-24 each; six such are 2^-22 with room.  (Truncated,
+    64 tiles would lose half a step of the sum so far twice each: 64 2^-24, 2^-18.)"""
+    n = 4096
+    b = wl.make_paged_batch(21, rows=[1], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=64,
+                            unused="normal")
+    sides = [sv.quantise(b.k_pool, kind), sv.quantise(wl.f32_to_bf16_bits(np.full(b.v_pool.shape, 1.75, np.float32)), kind)]
+    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
+    out, flags, st = attn(c, b, kind, split=n, n_splits_max=1)
+    assert st == 0 and (flags == 0).all()
+    err = np.abs(out.astype(np.float64) / 1.75 - 1)
+    assert err.max() <= 2.0**-21, err.max()
