@@ -472,7 +472,10 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             s_x[0][h][qi] = amax;
             named_bar_sync(pair_bar, 64);
             amax = max(amax, s_x[0][h ^ 1][qi]);
-            const int ex = min(120, 14 + 127 - (int)(amax >> 7));
+            // (no more than keeps fq normal: a masked score is -infinity times fq, and fq was 0 for a
+            // row of zeros under a scale of 2^-30)
+            const int ex = min(min(120, 14 + 127 - (int)(amax >> 7)),
+                               126 + (int)(exp_bits(p.scale_log2) >> 23) - 127);
             const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
             fq = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
             if (amax >= 0x7f80u) tail_bad = 1;  // a nonfinite query

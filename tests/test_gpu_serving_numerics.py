@@ -7,7 +7,7 @@ import torch
 from paged_kv_cache_segment_b200 import workloads as wl
 
 import _serving as sv
-from test_gpu_q8 import attn, cache_of, q8_batch
+from test_gpu_q8 import attn, cache_of, q8_batch, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -97,7 +97,8 @@ def test_value_scales_and_scores_far_from_one(kind, rows, hq, hkv):
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 @pytest.mark.parametrize("rows,hq,hkv,d,n,split", [(1, 8, 2, 64, 300, 0), (1, 8, 2, 128, 120, 128), (2, 4, 1, 256, 700, 256),  # decode
                                                    (12, 4, 2, 64, 300, 64), (5, 8, 2, 128, 120, 128),  # tcgen05
-                                                   (9, 2, 1, 256, 700, 256), (9, 2, 1, 256, 700, 704)])
+                                                   (9, 2, 1, 256, 700, 256), (9, 2, 1, 256, 700, 704),
+                                                   (3, 24, 2, 64, 300, 64), (3, 24, 2, 256, 300, 320)])  # the general kernel
 @pytest.mark.parametrize("size", [2.0**18, 2.0**23, 2.0**26, 2.0**27, 2.0**28, 2.0**31, 2.0**40, 2.0**90, -(2.0**28), -(2.0**35)])
 def test_scores_of_any_size(kind, rows, hq, hkv, d, n, split, size):
     """Scores of up to 2^90: two keys share the largest, `size` (or the smallest magnitude of the negative ones), all
@@ -153,3 +154,24 @@ def test_a_long_decode_sum_is_rounded_not_truncated(kind, hq, hkv, d):
     assert st == 0 and (flags == 0).all()
     err = np.abs(out.astype(np.float64) / 1.75 - 1)
     assert err.max() <= 2.0**-21, err.max()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("scale", [1e-3, 2.0**-29, 2.0**-40, 2.0**-100, 2.0**-126])
+@pytest.mark.parametrize("rows,hq,hkv,d,n,split", [(1, 8, 2, 64, 300, 0), (2, 4, 1, 128, 90, 128),  # decode
+                                                   (12, 4, 2, 64, 300, 64), (5, 8, 2, 128, 90, 128), (9, 2, 1, 256, 700, 0),
+                                                   (70, 4, 2, 128, 300, 0),  # tcgen05
+                                                   (3, 24, 2, 128, 300, 320)])  # the general kernel
+@pytest.mark.parametrize("size", [0.0, 2.0**-100, 1.0, 2.0**100])
+def test_rows_of_zeros_and_small_scales(kind, scale, rows, hq, hkv, d, n, split, size):
+    """Every positive scale is taken: scores next to 0 weigh all keys alike, and so does a query of zeros."""
+    if size * scale > 1:
+        size = 1 / scale  # scores of the usual size
+    b, sides, c = q8_batch(kind, 3, rows=[rows], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32)
+    q = wl.bf16_bits_to_f32(b.q) * np.float32(size)
+    q[0, 0] = 0
+    b.q, b.scale = wl.f32_to_bf16_bits(q), scale
+    out, flags, st = attn(c, b, kind, split=split)
+    assert st == 0
+    ref, fl, vmax = reference(b, sides, kind)
+    sv.check_attention(out, flags, ref, fl, vmax, False)
