@@ -59,11 +59,6 @@ constexpr int kStages = 2;                          // f16 K and V tiles
 constexpr int kFactors = 4;                         // tiles whose per-key factors are kept
 constexpr uint32_t kColS0 = 0, kColS1 = 64, kColQ = 128, kColO = 256;
 constexpr int kPids = 1024;                         // page ids held in shared memory
-// Tiles summed in tensor memory before O is added, with rounding, to the rows'
-// running sums (in their partials' place).  The tensor unit truncates its sums,
-// twice every 16 keys, so an O would lose some 2^-23 of itself every three tiles: streams of
-// 2,048-4,000 keys in one split (32 of 5-16 rows, D 128) came out 7.2e-6 of their norm off.
-constexpr int kSpan = 32;
 
 template <int D>
 struct VqCfg {
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
                 for (int kk = 0; kk < kN / 16; ++kk) {
                     const uint64_t bd = umma_desc_sw128(sV(s) + kk * 16 * 128, kSlab, 1024);
-                    umma_ts(tmem + kColO, sb + kk * 8, bd, idesc_wv, (j % kSpan > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts(tmem + kColO, sb + kk * 8, bd, idesc_wv, (j > 0 || kk > 0) ? 1u : 0u);
                     umma_ts(tmem + kColO, sb + 32 + kk * 8, bd, idesc_wv, 1u);
                 }
                 umma_commit(bar(kBarO + b));
@@ -447,11 +442,9 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         const bool valid_row = row_i < T;
         const int lim_k = valid_row && !p.full ? min(key_hi_eff, causal0 + row_i) : key_hi_eff;
         const uint32_t pair_bar = 2 + quad;
-        const int64_t at = ((int64_t)(q_row + row_i) * p.hq + g * G + qi % G) * p.n_splits + split;
         // m_ref: reference of the scores; m_ref + r_ref: that of score + value exponent (base 2
         // both; r_ref apart, or exponents would round away beside large scores)
         float m_ref = -INFINITY, r_ref = -INFINITY, l_run = 0.f;
-        float behind = 0.f;  // the running sums' reference less O's (base 2)
         uint32_t emax = 0, tail_bad = 0, lane_base = 0;
         float fq;  // scale * log2(e) over the row's power of two
 
@@ -591,9 +584,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 named_bar_sync(pair_bar, 64);
                 my = fmaxf(my, s_ymax[h ^ 1][qi]);
                 if (my - r_ref > kRefTop) {
-                    const float down = r_ref - (my - kRefLift);
-                    alpha = ex2(down);
-                    behind += down;
+                    alpha = ex2(r_ref - (my - kRefLift));
                     r_ref = my - kRefLift;
                 }
             }
@@ -648,13 +639,10 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 tmem_st16(lane_base + colS + 32 + 16 * h, lo);
                 tmem_st16(lane_base + colS + 16 * h, hi);
             }
-            // O holds the tiles of its span before this one: rescale it once W V(j - 1) is done,
-            // or, at a span's start, move it to the running sums
-            const bool span = j > 0 && j % kSpan == 0;
-            if (j > 0 && (span || __any_sync(0xffffffffu, alpha != 1.f))) {
+            // O holds the tiles before this one: rescale it once W V(j - 1) is done
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                 vq_wait(bar(kBarO + ((j - 1) & 1)), (uint32_t)(((j - 1) >> 1) & 1), abort_flag, lim);
                 tc_fence_after();
-                const float f = j > kSpan ? ex2(behind) : 0.f;
 #pragma unroll 1
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t r[32];
@@ -663,22 +651,8 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                     tmem_wait_ld();
 #pragma unroll
                     for (int w = 0; w < 32; ++w) r[w] = __float_as_uint(__uint_as_float(r[w]) * alpha);
-                    if (!span) {
-                        tmem_st32(lane_base + col, r);
-                    } else if (valid_row) {
-                        float4 *to = reinterpret_cast<float4 *>(p.part_o + at * D + h * (D / 2) + c * 32);
-#pragma unroll
-                        for (int w = 0; w < 8; ++w) {
-                            float4 y = j > kSpan ? to[w] : make_float4(0.f, 0.f, 0.f, 0.f);
-                            y.x = fmaf(y.x, f, __uint_as_float(r[4 * w]));
-                            y.y = fmaf(y.y, f, __uint_as_float(r[4 * w + 1]));
-                            y.z = fmaf(y.z, f, __uint_as_float(r[4 * w + 2]));
-                            y.w = fmaf(y.w, f, __uint_as_float(r[4 * w + 3]));
-                            to[w] = y;
-                        }
-                    }
+                    tmem_st32(lane_base + col, r);
                 }
-                if (span) behind = 0.f;
             }
             tmem_wait_st();
             tc_fence_before();
@@ -695,37 +669,19 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
         named_bar_sync(pair_bar, 64);
         const float l_sum = s_xl[0][qi] + s_xl[1][qi];
         uint32_t bad = s_x[1][0][qi] | s_x[1][1][qi] | s_err | (aborted ? 1u : 0u) | (isfinite(l_sum) ? 0u : 1u);
+        const int64_t at = ((int64_t)(q_row + row_i) * p.hq + g * G + qi % G) * p.n_splits + split;
         // 2^r in two steps: it may itself be past the floats where o is small
         const float gf = r_ref == -INFINITY ? 0.f : ex2(0.5f * r_ref);
         const int d0 = h * (D / 2);
-        // 32 columns of the row's sum: O and what its earlier spans left
-        const bool spans = n_tiles > kSpan;
-        const float fs = ex2(behind);
-        auto sums = [&](int cc, float(&o)[32]) {
-            uint32_t r[32];
-            tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
-            tmem_wait_ld();
-#pragma unroll
-            for (int w = 0; w < 32; ++w) o[w] = __uint_as_float(r[w]);
-            if (spans && valid_row) {
-                const float4 *from = reinterpret_cast<const float4 *>(p.part_o + at * D + d0 + cc * 32);
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const float4 y = from[w];
-                    o[4 * w] = fmaf(y.x, fs, o[4 * w]);
-                    o[4 * w + 1] = fmaf(y.y, fs, o[4 * w + 1]);
-                    o[4 * w + 2] = fmaf(y.z, fs, o[4 * w + 2]);
-                    o[4 * w + 3] = fmaf(y.w, fs, o[4 * w + 3]);
-                }
-            }
-        };
         if (p.out) {
             // ---- one split: normalise, look the row over, write it
             const float il = 1.f / l_sum;
             auto load = [&](int cc, float(&o)[32]) {
-                sums(cc, o);
+                uint32_t r[32];
+                tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
+                tmem_wait_ld();
 #pragma unroll
-                for (int w = 0; w < 32; ++w) o[w] = o[w] * gf * gf * il;
+                for (int w = 0; w < 32; ++w) o[w] = __uint_as_float(r[w]) * gf * gf * il;
             };
             uint32_t obad = 0;
 #pragma unroll 1
@@ -762,19 +718,20 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             }
             if (valid_row && h == 0) p.out_flags[at] = (uint8_t)(bad ? 1 : 0);
         } else {
-            // see prompt_tc.cu: many rows leave by bulk copies (not over sums written by this thread's stores)
-            const bool staged = rows_here * G >= 64 && !spans;
+            const bool staged = rows_here * G >= 64;  // see prompt_tc.cu: many rows leave by bulk copies
             uint32_t *stage = reinterpret_cast<uint32_t *>(base_ptr + C::kOffK) + qi * (D + 4) + d0;
             uint32_t *gout = reinterpret_cast<uint32_t *>(p.part_o + at * D + d0);
             const bool direct = !staged && valid_row && !aborted;
             uint32_t obad = 0;
 #pragma unroll 1
             for (int cc = 0; cc < D / 64; ++cc) {
+                uint32_t r[32];
+                tmem_ld32(lane_base + kColO + d0 + cc * 32, r);
+                tmem_wait_ld();
                 float o[32];
-                sums(cc, o);
 #pragma unroll
                 for (int w = 0; w < 32; ++w) {
-                    o[w] = o[w] * gf * gf;
+                    o[w] = __uint_as_float(r[w]) * gf * gf;
                     obad |= !isfinite(o[w]);
                 }
                 if ((staged && !aborted) || direct) {

@@ -175,48 +175,3 @@ def test_rows_of_zeros_and_small_scales(kind, scale, rows, hq, hkv, d, n, split,
     assert st == 0
     ref, fl, vmax = reference(b, sides, kind)
     sv.check_attention(out, flags, ref, fl, vmax, False)
-
-
-@pytest.mark.parametrize("kind", ["e4m3", "int8"])
-@pytest.mark.parametrize("rows,hq,hkv,d", [(12, 4, 2, 64), (9, 8, 2, 128), (40, 4, 1, 256)])
-@pytest.mark.parametrize("n,split", [(20000, 20032), (20000, 8192), (2100, 2112), (6150, 6208)])
-def test_a_long_verify_sum_loses_no_more_than_a_short_one(kind, rows, hq, hkv, d, n, split):
-    """All values 1.75, scores of all sizes: the output is 1.75, however many keys a partial covers.  The tensor unit
-    truncates, twice every 16 keys, over at most 2,048 keys: 256 times less than a step, 2^-23, of a sum that grows
-    evenly: 2^-16 of it.  Beyond that sums are rounded: n / 2,048 half steps here, n / 64 in the weights' sum, both
-    ways, so with room their square root of them: 2^-20 at 20,000 keys."""
-    b = wl.make_paged_batch(22, rows=[rows], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=64,
-                            unused="normal")
-    sides = [sv.quantise(b.k_pool, kind), sv.quantise(wl.f32_to_bf16_bits(np.full(b.v_pool.shape, 1.75, np.float32)), kind)]
-    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
-    out, flags, st = attn(c, b, kind, split=split, n_splits_max=-(-n // split))
-    assert st == 0 and (flags == 0).all()
-    err = np.abs(out.astype(np.float64) / 1.75 - 1)
-    assert err.max() <= 2.0**-16 + 2.0**-20, err.max()
-
-
-@pytest.mark.parametrize("kind", ["e4m3", "int8"])
-@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("rows,keys,hq,hkv,d,split", [([7, 16], [9000, 5000], 8, 2, 64, 0), ([5, 20], [4200, 2049], 16, 2, 256, 4224),
-                                                      ([3, 70], [2048, 6300], 16, 4, 128, 2112), ([17], [8191], 8, 1, 128, 8192)])
-def test_growing_scores_over_long_splits(kind, dt, rows, keys, hq, hkv, d, split):
-    """Scores and value scales that grow along the keys, so that the references move in every part of a long split."""
-    b = wl.make_paged_batch(23, rows=rows, keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32,
-                            unused="normal")
-    k, v = wl.bf16_bits_to_f32(b.k_pool).copy(), wl.bf16_bits_to_f32(b.v_pool).copy()
-    for s, (_, _, n, base, _) in enumerate(b.segs):
-        for page in range(-(-n // 32)):
-            at, x = b.page_table[base + page], page * 32 / n
-            k[at, ..., 0] = (x * 30 - 10) / 8  # a score of up to 20 nats more at the end
-            v[at] *= 2.0 ** int(6 * x)
-    q = wl.bf16_bits_to_f32(b.q).copy()
-    q[..., 0] = 8 / b.scale
-    b.q = wl.f32_to_bf16_bits(q)
-    sides = [sv.quantise(wl.f32_to_bf16_bits(x), kind) for x in (k, v)]
-    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
-    out, flags, st = attn(c, b, kind, split=split, n_splits_max=4, out_dtype=dt)
-    assert st == 0
-    ref, fl, vmax = reference(b, sides, kind)
-    sv.check_attention(out, flags, ref, fl, vmax, dt == torch.bfloat16)
-    again, _, _ = attn(c, b, kind, split=split, n_splits_max=4, out_dtype=dt)
-    assert (again == out).all()
