@@ -472,8 +472,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             s_x[0][h][qi] = amax;
             named_bar_sync(pair_bar, 64);
             amax = max(amax, s_x[0][h ^ 1][qi]);
-            // (no more than keeps fq normal: a masked score is -infinity times fq, and fq was 0 for a
-            // row of zeros under a scale of 2^-30)
+            // (no more than keeps fq normal)
             const int ex = min(min(120, 14 + 127 - (int)(amax >> 7)),
                                126 + (int)(exp_bits(p.scale_log2) >> 23) - 127);
             const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
@@ -508,17 +507,20 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
                 for (int c = 0; c < 32; ++c) sv[c] = __uint_as_float(r[c]);
             }
-            // scores over fq (> 0: maxima commute with it) and their largest
+            // scores in base 2, rounded (large ones, unrounded, may lie any distance from a reference
+            // of their own rounding), and their largest
             const int fs = j % kFactors;
             const float4 *fk = reinterpret_cast<const float4 *>(factor + fs * 3 * kN + 32 * h);
             const float4 *fv = fk + kN / 4, *vs = fk + 2 * (kN / 4);
             const uint32_t vnan = s_vnan[fs][h];
             float mx = -INFINITY;
+            const uint64_t fq2 = pk2(fq, fq);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float4 k4 = fk[q];
-                unpk2(mul2(pk2(sv[4 * q], sv[4 * q + 1]), pk2(k4.x, k4.y)), sv[4 * q], sv[4 * q + 1]);
-                unpk2(mul2(pk2(sv[4 * q + 2], sv[4 * q + 3]), pk2(k4.z, k4.w)), sv[4 * q + 2], sv[4 * q + 3]);
+                unpk2(mul2(mul2(pk2(sv[4 * q], sv[4 * q + 1]), pk2(k4.x, k4.y)), fq2), sv[4 * q], sv[4 * q + 1]);
+                unpk2(mul2(mul2(pk2(sv[4 * q + 2], sv[4 * q + 3]), pk2(k4.z, k4.w)), fq2), sv[4 * q + 2],
+                      sv[4 * q + 3]);
             }
             if (kt + kN > full_hi) {
 #pragma unroll
@@ -535,7 +537,6 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             }
 #pragma unroll
             for (int c = 0; c < 32; c += 2) mx = max3(mx, sv[c], sv[c + 1]);
-            mx *= fq;
             if (vnan) {  // value rows marked nonfinite: flag the rows that see one
 #pragma unroll 1
                 for (uint32_t v = vnan; v; v &= v - 1)
@@ -547,15 +548,6 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             s_xmax[b][h][qi] = there ? mx : __int_as_float(0x7fc00000);
             named_bar_sync(pair_bar, 64);
             mx = max_nan(there ? mx : __int_as_float(0x7fc00000), s_xmax[b][h ^ 1][qi]);
-            // large scores are rounded before the reference is taken off them: fq times the sums,
-            // unrounded, may lie any distance from a reference of their own rounding
-            float f = fq;
-            if (__any_sync(0xffffffffu, fabsf(mx) >= 0x1p20f)) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) sv[c] *= fq;
-                f = 1.f;
-            }
-            const uint64_t fq2 = pk2(f, f);
             // lazy references: they move when a term would pass 2^15 (both halves see
             // the same maxima, so they move together)
             if (mx - m_ref > kRefTop) {
@@ -576,8 +568,8 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                 for (int q = 0; q < 8; ++q) {
                     const float4 v4 = fv[q];
                     float y0, y1, y2, y3;
-                    unpk2(add2(fma2(pk2(sv[4 * q], sv[4 * q + 1]), fq2, nmu2), pk2(v4.x, v4.y)), y0, y1);
-                    unpk2(add2(fma2(pk2(sv[4 * q + 2], sv[4 * q + 3]), fq2, nmu2), pk2(v4.z, v4.w)), y2, y3);
+                    unpk2(add2(add2(pk2(sv[4 * q], sv[4 * q + 1]), nmu2), pk2(v4.x, v4.y)), y0, y1);
+                    unpk2(add2(add2(pk2(sv[4 * q + 2], sv[4 * q + 3]), nmu2), pk2(v4.z, v4.w)), y2, y3);
                     my = max3(my, max3(y0, y1, y2), y3);
                 }
                 s_ymax[h][qi] = my;
@@ -609,7 +601,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
                         for (int i = 0; i < 4; i += 2) {
                             const int c = 4 * q + i;
                             float p0, p1, w0, w1;
-                            unpk2(fma2(pk2(sv[c], sv[c + 1]), fq2, nmu2), p0, p1);
+                            unpk2(add2(pk2(sv[c], sv[c + 1]), nmu2), p0, p1);
                             const uint64_t p2 = pk2(ex2(p0), ex2(p1));
                             ls2 = add2(ls2, p2);
                             unpk2(mul2(p2, mul2(i ? pk2(s4.z, s4.w) : pk2(s4.x, s4.y), rho2)), w0, w1);
@@ -624,7 +616,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
                             const int c = 4 * q + i;
-                            const uint64_t d2 = fma2(pk2(sv[c], sv[c + 1]), fq2, nmu2);
+                            const uint64_t d2 = add2(pk2(sv[c], sv[c + 1]), nmu2);
                             float p0, p1, w0, w1;
                             unpk2(d2, p0, p1);
                             ls2 = add2(ls2, pk2(ex2(p0), ex2(p1)));
