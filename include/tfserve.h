@@ -119,6 +119,9 @@ TFS_API tf_status tf_kv_read_q8(const tf_q8_cache *cache_host, const int32_t *pa
  * codes stand for.  Scores, softmax statistics and sums are held in fp32; a
  * weight, times its value row's scale, enters the value product with 22 bits and
  * at least to 2^-32 of the largest such product of its partial.
+ * The tensor cores truncate their sums: with more than 8 queries a kv-head a
+ * partial of n keys may lose n 2^-27 of them (chosen splits have up to 8,192
+ * keys, as far as n_splits_max allows).
  *
  *  scale       > 0
  *  split_keys  keys a partial covers: 0 lets the library choose (from the host
@@ -182,6 +185,10 @@ TFS_API size_t tf_paged_attn_q8_workspace_bytes(int32_t n_rows_total, int32_t n_
  *              16-byte aligned; needs no initialisation
  *  out, out_dtype, flags  as for tf_paged_attn_q8; only the rows segs names
  *              are written
+ *
+ * Chosen splits of prefixes, and of streams with more than 8 queries a kv-head,
+ * have up to 8,192 keys, as far as the splits given allow: longer partials lose
+ * bits as tf_paged_attn_q8's do.
  *
  * Streams and prefixes have up to 2^30 keys each.  Other arguments, shapes and
  * errors: tf_paged_attn_decode.

@@ -128,13 +128,22 @@ inline int least_split(int longest, bool direct) {
     return longest <= 2048 ? 64 : longest <= 8192 ? 128 : 256;
 }
 
+// The longest split chosen for the tensor-core kernels.  Their unit truncates its sums,
+// twice every 16 keys (hi and lo weights), each time by less than a step, 2^-23, of a sum
+// that grows evenly: a partial of n keys loses up to n 2^-27 of its sum, 2^-14 here
+// (20,000 keys in one split: 1.2e-4 measured over an 8-bit cache, 6e-5 over bf16).
+// A chunk of 1,024 rows over 13,312 keys (D 256, 16/2 heads) takes 383 us in two such
+// splits, 342 in one; 20 streams of 9,000-10,000 keys (D 64, 8 kv-heads: 160 CTAs) 312
+// in two, 360 in one, 80 rows behind 20 bf16 prefixes of as many 227 and 297.
+constexpr int kLongestSplit = 8192;
+
 // A split size for kernels of one CTA an SM with a fixed cost a CTA (start-up
 // and epilogue, some eight 64-key tiles' worth): the smallest whole number of
 // tiles that leaves one wave of CTAs (streams x kv-heads x query tiles x splits)
 // on the SMs, since a second wave pays the fixed cost again; one split a stream
-// where even that is more.
+// where even that is more.  No split is longer than `most` keys, as far as n_splits_max allows.
 inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows_per_tile, int n_sms, int least,
-                          int n_splits_max) {
+                          int n_splits_max, int64_t most = kMaxKeys) {
     const int64_t longest = longest_keys(sh, n_segs);
     auto ctas = [&](int64_t tiles) {
         int64_t n = 0;
@@ -154,6 +163,10 @@ inline int one_wave_split(const tf_seg *sh, int n_segs, int n_kv_heads, int rows
             hi = mid;
         else
             lo = mid + 1;
+    }
+    if (lo * 64 > most) {  // even splits of up to `most`
+        const int64_t n = (longest + most - 1) / most, len = (longest + n - 1) / n;
+        lo = ((len > fit ? len : fit) + 63) / 64;
     }
     return lo > (0x40000000 >> 6) ? 0x40000000 : (int)(lo * 64);
 }

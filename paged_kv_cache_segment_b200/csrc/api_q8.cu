@@ -56,7 +56,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
             split = ws ? decode_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 1280,
                                       least, n_splits_max)
                        : one_wave_split(segs_host, n_segs, c.n_kv_heads, std::max(1, 128 / group), device_sms(), least,
-                                        n_splits_max);
+                                        n_splits_max, kLongestSplit);
         // the partial slots (and, in the tensor-core kernel, the CTAs) that the longest stream takes
         splits = (int)(((int64_t)longest_keys(segs_host, n_segs) + split - 1) / split);
     }

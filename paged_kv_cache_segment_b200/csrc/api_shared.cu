@@ -100,7 +100,8 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
         const int least = least_split(longest_keys(host, n), false);
         if (split == 0)
             split = (int64_t)rows * group > 8
-                        ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), least, splits)
+                        ? one_wave_split(host, n, n_kv_heads, std::max(1, 128 / group), device_sms(), least, splits,
+                                         kLongestSplit)
                         : decode_split(host, n, n_kv_heads, device_sms() * 2, 1024, least, splits);
         splits = (int)(((int64_t)longest_keys(host, n) + split - 1) / split);
         return TF_OK;

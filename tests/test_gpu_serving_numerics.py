@@ -175,3 +175,21 @@ def test_rows_of_zeros_and_small_scales(kind, scale, rows, hq, hkv, d, n, split,
     assert st == 0
     ref, fl, vmax = reference(b, sides, kind)
     sv.check_attention(out, flags, ref, fl, vmax, False)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,hq,hkv,d,split", [(12, 4, 2, 64, 20032), (9, 8, 2, 128, 4096), (40, 4, 1, 256, 1024),
+                                                 (19300, 1, 1, 64, 0)])  # more query tiles than SMs: one wave is one split
+def test_what_a_long_partial_loses(kind, rows, hq, hkv, d, split):
+    """All values 1.75, scores of all sizes: the output is 1.75.  The tensor unit truncates its sums, twice every 16 keys,
+    each time by less than a step, 2^-23, of a sum that grows evenly: n / 16 * 2 * 2^-23 / 2 = n 2^-27 of it for a partial
+    of n keys.  Chosen splits have up to 8,192 keys.  The rest is rounded: with room 2^-20."""
+    n = 20000
+    b = wl.make_paged_batch(22, rows=[rows], keys=[n], n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=64,
+                            unused="normal")
+    sides = [sv.quantise(b.k_pool, kind), sv.quantise(wl.f32_to_bf16_bits(np.full(b.v_pool.shape, 1.75, np.float32)), kind)]
+    c = cache_of(sides[0][0], sides[1][0], sides[0][1], sides[1][1], kind)
+    out, flags, st = attn(c, b, kind, split=split, n_splits_max=-(-n // split) if split else 16)
+    assert st == 0 and (flags == 0).all()
+    err = np.abs(out.astype(np.float64) / 1.75 - 1)
+    assert err.max() <= (split or 8192) * 2.0**-27 + 2.0**-20, err.max()
