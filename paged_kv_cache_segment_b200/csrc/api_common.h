@@ -118,9 +118,9 @@ inline int longest_keys(const tf_seg *sh, int n_segs) {
 // The least split worth a CTA of its own: one 64-key tile, more for a longer stream,
 // whose partials the merge has to read; two tiles where that leaves one split and the
 // kernel needs no merge (`direct`).  8-bit, 1 stream, us by splits of 64, 128 and 256:
-// 8 rows, D 256, 512 keys 13.8, 14.5 and 17.6; 4,096 keys 17.4, 15.6 and 18.3; 8,000
-// 19.2 by 128, 18.5 by 256; 100 keys 13.5, 12.6 direct; one row, D 128, 600 keys 8.9,
-// 9.1 and 10.8; 16,000 11.2 and 11.1.  (2 one-row streams of 353-2,000 keys behind a
+// 8 rows, D 256, 512 keys 14.5, 15.7 and 18.6; 4,096 keys 18.8, 16.9 and 20.2; 8,000
+// 20.3 by 128 or 256; 100 keys 14.3, 13.2 direct; one row, D 128, 600 keys 9.0, 9.3
+// and 10.8.  (2 one-row streams of 353-2,000 keys behind a
 // short prefix, 16/8 heads: 17.7 against 24.2 by 256; 15 streams of 2,000 behind 3 of
 // 846 lose 1.4 to a wider merge.)
 inline int least_split(int longest, bool direct) {

@@ -49,8 +49,8 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         if (max_rows == 0) return TF_OK;
         ws = (int64_t)max_rows * group <= 8 && decode_q8_supported(c.head_dim, n_segs) &&
              (split == 0 || split % std::min(c.page_size, 64) == 0);
-        // (64 streams of 256-4,096 keys take 70 us in one split each, 57 us in splits of 1,280 keys; 16 of
-        // 1,024-8,192 take 29.8 us in one wave of 1,152, 35 in splits of 768)
+        // (64 streams of 256-4,096 keys take 70 us in one split each, 60 us in splits of 1,280 keys; 16 of
+        // 1,024-8,192 take 31 us in one wave of 1,152, 36.5 in splits of 768)
         const int least = least_split(longest_keys(segs_host, n_segs), true);
         if (split == 0)
             split = ws ? decode_split(segs_host, n_segs, c.n_kv_heads, decode_q8_grid(c.head_dim, c.kv_type), 1280,

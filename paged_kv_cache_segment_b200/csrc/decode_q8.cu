@@ -29,12 +29,14 @@
 //  - The references move only when a term would pass 2^15, so a tile takes one
 //    vote instead of two butterfly maxima.
 // Measured (partials and merge): 16 streams of 1,024-8,192 keys, 32/8 heads, D 128
-// (123 MB) in 30 us, 4.1 TB/s, 28 of them this kernel; D 256 32 us, D 64 39 us for
-// as many bytes (a key there has a quarter of the time; four CTAs an SM, where
-// three took 45 us); one stream of 32,000 keys 20 us; two streams of 37 and 70
-// keys, written directly, 6.5 us (8.3 with a merge).  What is left over the bytes'
-// 19 us is some 5 us of start-up (table, page ids, first tiles, one after
-// another) and the merge.  Tried and not kept: four CTAs an SM at D 128 with two
+// (123 MB) in 31.7 us, 3.9 TB/s, 30 of them this kernel; D 256 33.6 us, D 64 42.5 us
+// for as many bytes (a key there has a quarter of the time; four CTAs an SM, where
+// three took 45 us); one stream of 32,000 keys 20.7 us; two streams of 37 and 70
+// keys, written directly, 7.2 us.  By stamps in a copy a CTA of the first has its first
+// tile after 4.8 us (table, page ids, copies, one after another), then takes 20 tiles
+// of 0.97 us and 1.5 us to combine and write: 26 us in the middle, 28 at the slowest.
+// Of a tile's 1,830 cycles its warps wait 290 for the copies (D 64 570 of 1,740, D 256
+// 560 of 2,560): what holds it is the codes' way through the MMAs, more than the loads.  Tried and not kept: four CTAs an SM at D 128 with two
 // stages each (36 us), one with three stages at D 256 (43 us).
 #include <atomic>
 #include <cfloat>

@@ -184,7 +184,7 @@ cudaError_t launch_kv_q8_u(const KvQ8Params &p, bool read, int n_segs, int64_t u
 template <int D, int TYPE>
 cudaError_t launch_kv_q8(const KvQ8Params &p, bool read, int n_segs, int max_rows, cudaStream_t st) {
     const int64_t units = (int64_t)max_rows * p.hkv;
-    // several units a thread, their loads in flight together, once that still fills the GPU (15,000 rows: 22.7 us
+    // several units a thread, their loads in flight together, once that still fills the GPU (15,000 rows: 22.1 us
     // against 23.5 with one; 16 rows: one, so that they spread over the SMs)
     const int64_t wave = (int64_t)device_sms() * (2048 / (D / 8));  // units of one a group on every SM
     if (units * n_segs >= 4 * wave) return launch_kv_q8_u<D, TYPE, 4>(p, read, n_segs, units, st);

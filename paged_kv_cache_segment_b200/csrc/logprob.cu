@@ -34,8 +34,9 @@
 //    eight CTAs a row, whose statistics and lists meet in distributed shared memory.
 //  - warp mode, for short rows: a warp streams and ends a row of its own.
 // Measured (bf16): 1,024 rows x 128,000 columns 59 us with 5 alternatives (262 MB,
-// 4.4 TB/s), 67 with 20, 50 without; 62 rows with 20 12 us; one row of 128,000 f32
-// with 5 8.6 us; 20,000 rows x 3,000 45 us by warps, 151 by CTAs.  A persistent
+// 4.4 TB/s), 68 with 20, 51 without; 62 rows with 20 14 us (12.5 with the logits in
+// L2); one row of 128,000 f32 with 5 9 us; 20,000 rows x 3,000 51 us by warps, 151 by
+// CTAs.  A persistent
 // form with a warp of each CTA for the row ends was slower (75 us): one warp is
 // slow at them.  So were five or six smaller CTAs an SM (56-60 us without
 // alternatives).
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const
     }
     if (DEEP && n_chunks == 1) {
         // of one chunk, the second of its vectors' largest: a row may fill two vectors only (60,000 rows x 512 with 32:
-        // 156 us; 336 when it was the smaller of the two halves' largest, of which such rows have one)
+        // 158 us; 340 when it was the smaller of the two halves' largest, of which such rows have one)
         static_assert(kLpBatch == 4, "the second of four");
         const float v0 = Elem<T>::most(a[0]), v1 = Elem<T>::most(a[1]), v2 = Elem<T>::most(a[2]), v3 = Elem<T>::most(a[3]);
         other = max3(fminf(v0, v1), fminf(v2, v3), fminf(fmaxf(v0, v1), fmaxf(v2, v3)));
@@ -874,23 +875,23 @@ template <typename T, bool TOP>
 cudaError_t launch_logprob(const LogprobParams &p, cudaStream_t st) {
     const int sms = device_sms();
     const int chunk = Elem<T>::kPer * kLpBatch;  // columns a thread holds
-    // short rows (up to four chunks of a warp): a warp a row (60,000 rows x 1,000 with 5: 77 us; 356 by CTAs of 64)
+    // short rows (up to four chunks of a warp): a warp a row (60,000 rows x 1,000 with 5: 91 us; 356 by CTAs of 64)
     if (p.n_cols <= 4 * 32 * chunk && p.n_rows > 4 * sms) {
         const int64_t grid = ((int64_t)p.n_rows + kLpWarpRows - 1) / kLpWarpRows;
-        // (20,000 rows x 3,000 with 32: 98 us deep, 298 not; 60,000 x 1,000 with 20: 140 and 130)
+        // (20,000 rows x 3,000 with 32: 102 us deep, 298 not; 60,000 x 1,000 with 20: 140 and 134)
         if (TOP && p.top_k > 24)
             logprob_warp_kernel<T, TOP, TOP><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
         else
             logprob_warp_kernel<T, TOP, false><<<(unsigned)grid, kLpWarpRows * 32, 0, st>>>(p);
         return cudaGetLastError();
     }
-    // many rows: eight CTAs an SM where a row is short (4,000 rows x 32,000 with 20: 93 us, 106 by four), else four
-    // (1,024 x 128,000 with 5: 64 us, 68 by eight)
+    // many rows: eight CTAs an SM where a row is short (4,000 rows x 32,000 with 20: 85 us, 106 by four), else four
+    // (1,024 x 128,000 with 20: 68 us, 71 by eight)
     if (p.n_rows > 4 * sms && p.n_cols <= 2 * 1024 * chunk) return launch_cta<T, TOP, 128>(p, 1, st);
     if (p.n_rows > 2 * sms || p.n_cols <= 256 * chunk) return launch_cta<T, TOP, 256>(p, 1, st);
     if (p.n_rows > sms) return launch_cta<T, TOP, 512>(p, 1, st);
     // a CTA an SM: a cluster a row while there are SMs for it and columns to fill its threads (62 rows x 128,000 with
-    // 20: 12 us; two more by clusters of four CTAs of 512, two an SM)
+    // 20: 14 us; two more by clusters of four CTAs of 512, two an SM)
     int cl = 1;
     while (cl < kLpMaxCluster && p.n_rows * 2 * cl <= sms && cl * 1024 * chunk < p.n_cols) cl *= 2;
     return launch_cta<T, TOP, 1024>(p, cl, st);

@@ -27,7 +27,7 @@ constexpr uint32_t kE8Nan = 255;  // the scale byte of a row that held a NaN or 
 // at the largest exponent that floor is 2^-25: 32,000 keys just below it, behind one
 // that weighs 1, lost 8e-4 of an output whose sum counted them.  A lift of 11 would
 // put it at 2^-36, but the references then move oftener: a verify round of 1-16
-// rows takes 58.5 us a call instead of 54.8, a decode step 32.8 with either.)
+// rows took 58.5 us a call instead of 54.8, a decode step 32.8 with either.)
 constexpr float kRefLift = 7.f, kRefTop = 15.f;
 
 // 2^(e - 127) (e = 0: the subnormal 2^-127), NaN for 255.

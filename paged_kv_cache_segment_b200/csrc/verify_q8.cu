@@ -21,22 +21,21 @@
 // instruction: with bf16 tiles that carry the scales it would be four.
 //
 // Measured: 8 streams of 1-16 rows over 2,048-16,384 keys, 16/2 heads, D 256, int8
-// (87 MB) in 47 us for bf16 output, 51 for f32; the kernel 45 us of it: 5 us until
-// the first tile's scores, then 19 tiles a CTA, 3.5 us of epilogue.  A tile takes
-// some 2,600 cycles, and no unit is busy that long: its MMAs take 1,500 (QK at N =
-// 64 runs at half rate; 2,000 with W V twice), shared memory as much (33 KB of codes
-// in, out and back as 64 KB of f16, read by the MMAs).  It is a chain: 1,900 cycles
-// from a tile's scores to its weights, then W V, then the scores that take the
-// weights' place in tensor memory (at D 256 there is no room for a third buffer).
-// Without the converters' work it would take 43 us, without the exponentials 47,
-// with half of the MMAs 45.  Four converter warps took 64 us where eight take 51;
-// slower or no faster: four converter warps for K and four for V (53), fetching the
-// next codes before converting the last (47), sixteen softmax warps, registers moved
-// to them from the converters, one poll of the MMA warp for all three barriers
-// (46 for bf16 output but 53 for f32).
+// (87 MB) in 52 us, 50 of them this kernel, by stamps in a copy: a CTA starts within
+// 3 us of the first, has its first scores after 6.5, the second tile's 2.5 later and
+// 17 more tiles at 1.75, then 2 us for the last W V and 3 of epilogue; the middle one
+// of the full CTAs is done after 46, the last after 50.  The softmax warps are what a
+// tile waits for: of 3,300 cycles with the stamps (3,000 without) they work 3,050, to
+// the maxima 1,030, the references 360, the weights 1,360, in tensor memory 300.  The
+// tensor pipe is active 29% of the kernel, shared memory's 27%, the issue slots 37%.
+// (At D 128 a tile takes 1.6 us, at D 64 1.55: the softmax is the same.)
+// Tried when it took 46-51 us: four converter warps took 64 where eight took 51;
+// slower or no faster were four converter warps for K and four for V, fetching the
+// next codes before converting the last, sixteen softmax warps, registers moved to
+// them from the converters, one poll of the MMA warp for all three barriers.
 // One split a stream is written as final rows (18 streams of 10-16 rows over 20-121
-// keys, 64/8 heads, D 128: 13 us, 25 with partials and a merge; over 900-1,100 keys
-// 28 and 36 us).
+// keys, 64/8 heads, D 128: 14 us, 25 with partials and a merge; over 900-1,100 keys
+// 36 us).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
