@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
                 return;
             }
             n_sp = splits_of(N, p.split_keys);
-            if (n_sp > p.n_splits_max) {
+            if (T > 0 && n_sp > p.n_splits_max) {  // (no rows, no partials)
                 if (tid == 0) atomicOr(p.status, TF_DEV_SPLITS);
                 leave();
                 return;

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kVqThreads, 1) verify_q8_kernel(const Q8TcPara
             bit = TF_DEV_BAD_SEG;
         else if ((int64_t)N > ((int64_t)n_pg << p.log2_page))
             bit = TF_DEV_PAST_PAGES;
-        else if (((int64_t)N + p.split_keys - 1) / p.split_keys > p.n_splits)
+        else if (T > 0 && ((int64_t)N + p.split_keys - 1) / p.split_keys > p.n_splits)
             bit = TF_DEV_SPLITS;
         if (bit) {
             if (tid == 0) atomicOr(p.status, bit);

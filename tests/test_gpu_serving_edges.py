@@ -362,3 +362,40 @@ def test_a_shared_device_entry_of_two_billion_keys_is_refused(rows, hq, hkv, pre
     if not prefix:
         ref, rf, vmax = shared_reference(b, prefixes, segs, [0, 0])
         sv.check_attention(out[:rows], fl[:rows], ref[:rows], rf[:rows], vmax, False)
+
+
+@pytest.mark.parametrize("rows,keys,hq,hkv,d", [([12, 0, 3], [300, 2000, 90], 4, 2, 64),  # tcgen05, partials and merge
+                                                ([9, 0], [60, 1500], 8, 1, 128),  # tcgen05, one split
+                                                ([1, 0, 1], [300, 2000, 90], 8, 2, 128), ([0, 1], [1500, 60], 8, 2, 64),  # decode
+                                                ([5, 0], [300, 2000], 24, 2, 128)])  # the general kernel
+def test_a_stream_without_rows_may_have_any_keys(rows, keys, hq, hkv, d):
+    """The launch holds the partials of the streams with rows; a longer stream without rows needs none."""
+    b, sides, c = q8_batch("int8", 31, rows=rows, keys=keys, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=32)
+    ref, fl, vmax = reference(b, sides, "int8")
+    out, flags, st = attn(c, b, "int8", n_splits_max=2)
+    assert st == 0
+    sv.check_attention(out, flags, ref, fl, vmax, False)
+
+
+@pytest.mark.parametrize("rows,own,hq,hkv", [([5, 0, 2], [40, 900, 70], 16, 2), ([1, 0, 1], [40, 900, 70], 8, 2)])
+def test_prefixes_and_streams_without_rows_may_have_any_keys(rows, own, hq, hkv):
+    """The third prefix has no rows, as every stream of it has none."""
+    b, prefixes, segs = batch(32, [90, 33, 1000], [0, 0, 1], rows, own, hq, hkv, 128, 16)
+    assert prefixes[2, 1] == 0 and segs[1, 1] == 0
+    ref, fl, vmax = shared_reference(b, prefixes, segs, [0, 0, 1])
+    for host in (True, "segs", "prefixes"):
+        out, flags, st = shared(b, prefixes, segs, host=host, split=64, n_pre=2, n_own=2)
+        assert st == 0
+        sv.check_attention(out, flags, ref, fl, vmax, False)
+
+
+@pytest.mark.parametrize("fn", [tf.tf_paged_attn_decode, tf.tf_paged_attn_block])
+def test_bf16_partials_of_a_stream_without_rows(fn):
+    b = wl.make_paged_batch(33, rows=[12, 0], keys=[100, 1000], n_q_heads=16, n_kv_heads=2, head_dim=128, page_size=16,
+                            split_keys=64, n_splits_max=2)
+    n, f = b.q.shape[0], dict(device=DEV, dtype=torch.float32)
+    po, pm, pl = torch.zeros((n, 16, 2, 128), **f), torch.zeros((n, 16, 2), **f), torch.zeros((n, 16, 2), **f)
+    pf, st = torch.zeros((n, 16, 2), dtype=torch.uint8, device=DEV), status_word()
+    fn(dev(b.q), dev(b.k_pool), dev(b.v_pool), dev(b.page_table), dev(b.segs), scale=b.scale, split_keys=64,
+       n_splits_max=2, part_o=po, part_m=pm, part_l=pl, part_flag=pf, status=st, segs_host=b.segs)
+    assert int(st.item()) == 0
