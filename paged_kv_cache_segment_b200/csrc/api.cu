@@ -90,7 +90,8 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
                                const tf_seg *segs, int32_t n_segs, const tf_seg *segs_host,
                                const int32_t *page_table_host, float scale, int32_t split_keys,
                                int32_t n_splits_max, float *part_o, float *part_m, float *part_l,
-                               uint8_t *part_flag, uint32_t *status, tf_stream_t stream, bool beside, int max_keys) {
+                               uint8_t *part_flag, uint32_t *status, tf_stream_t stream, bool beside, int max_keys,
+                               bool held) {
     if (n_rows_total < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_pages < 0 || page_table_len < 0 || n_segs < 0 ||
         split_keys < 0 || n_splits_max <= 0 || !std::isfinite(scale))
         return TF_ERR_ARG;
@@ -141,6 +142,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
         w.log2_page = lp;
         w.pt_len = page_table_len;
         w.max_keys = max_keys;
+        w.max_rows = held ? max_rows : 0;
         w.scale_log2 = scale * 1.4426950408889634f;
         w.split_keys = split_keys;
         w.n_splits_max = n_splits_max;
@@ -173,6 +175,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
             t.segs = segs;
             t.pt_len = page_table_len;
             t.max_keys = max_keys;
+            t.max_rows = held ? max_rows : 0;
             t.split_keys = split_keys;
             t.n_splits_max = n_splits_max;
             t.n_qt = (int)n_qt;
@@ -200,6 +203,7 @@ tf_status tfp::paged_partials(bool full, const void *q, int32_t n_rows_total, in
     p.log2_page = lp;
     p.pt_len = page_table_len;
     p.max_keys = max_keys;
+    p.max_rows = held ? max_rows : 0;
     p.page_table = page_table;
     p.segs = segs;
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -159,6 +159,7 @@ tf_status tf_paged_attn_q8(const void *q, int32_t n_rows_total, int32_t n_q_head
         p.log2_page = lp;
         p.pt_len = page_table_len;
         p.max_keys = kMaxKeys;
+        p.max_rows = max_rows;
         p.page_table = page_table;
         p.segs = segs;
         p.scale_log2 = scale_log2;

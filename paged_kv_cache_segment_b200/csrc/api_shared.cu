@@ -128,14 +128,14 @@ tf_status tf_paged_attn_shared(const void *q, int32_t n_rows_total, int32_t n_q_
     const tf_status rc = paged_partials(false, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                         n_kv_heads, head_dim, page_table, page_table_len, segs, n_segs, segs_host,
                                         page_table_host, scale, own_split, own_splits, own.o, own.m, own.l, own.flag,
-                                        status, stream, false, kMaxKeys);
+                                        status, stream, false, kMaxKeys, true);
     if (rc != TF_OK) return rc;
 
     if (n_prefixes > 0 && pre_rows > 0) {
         const tf_status rc = paged_partials(true, q, n_rows_total, n_q_heads, k_pool, v_pool, n_pages, page_size,
                                             n_kv_heads, head_dim, page_table, page_table_len, prefixes, n_prefixes,
                                             prefixes_host, page_table_host, scale, pre_split, pre_splits, pre.o,
-                                            pre.m, pre.l, pre.flag, status, stream, true, kMaxKeys);
+                                            pre.m, pre.l, pre.flag, status, stream, true, kMaxKeys, true);
         if (rc != TF_OK) return rc;
     }
     MergeSegsParams m{};

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, (D == 256) ? 1 : 2) attn_partial_ker
         const bool bad = w.q_row < 0 || w.n_rows < 0 || (int64_t)w.q_row + w.n_rows > p.n_rows_total ||
                          w.n_keys < (p.full ? (w.n_rows > 0 ? 1 : 0) : w.n_rows) || w.pt_base < 0 || w.n_pg < 0 ||
                          (int64_t)w.pt_base + w.n_pg > p.pt_len ||
-                         (!p.seg_inline && w.n_keys > p.max_keys);
+                         (!p.seg_inline && w.n_keys > p.max_keys) || (p.max_rows > 0 && w.n_rows > p.max_rows);
         if (bad) {
             if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
             return;

@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kPTThreads, pt_paired<D, PARTIAL>() ? 2 : 1)
             n_pg = sg.n_pages;
             const int keys_needed = p.full ? (T > 0 ? 1 : 0) : T;  // the causal count needs a key per row
             const bool bad = q_row < 0 || T < 0 || (int64_t)q_row + T > p.n_rows_total || N < keys_needed ||
-                             pt_base < 0 || n_pg < 0 || (int64_t)pt_base + n_pg > p.pt_len || N > p.max_keys;
+                             pt_base < 0 || n_pg < 0 || (int64_t)pt_base + n_pg > p.pt_len || N > p.max_keys ||
+                             (p.max_rows > 0 && T > p.max_rows);
             if (bad) {
                 if (tid == 0) atomicOr(p.status, TF_DEV_BAD_SEG);
                 leave();

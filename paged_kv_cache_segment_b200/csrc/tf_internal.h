@@ -40,6 +40,7 @@ struct AttnParams {
     // paged source
     int n_pages, log2_page, pt_len;
     int max_keys;  // an entry of more is bad
+    int max_rows;  // so is one of more rows (0: any number)
     const int32_t *page_table;
     const tf_seg *segs;
     tf_seg seg0;     // used instead of segs[0] when seg_inline != 0 (one-stream prompt calls)
@@ -91,6 +92,7 @@ struct PromptTcParams {
     const tf_seg *segs;
     int pt_len, split_keys, n_splits_max, n_qt;
     int max_keys;  // an entry of more is bad
+    int max_rows;  // so is one of more rows (0: any number)
     int full;  // every row sees all of its stream's keys (no causal count)
     // partials that run beside the partial kernel launched before this one: as
     // its programmatic dependent, waiting for that grid only at the end, so that
@@ -193,12 +195,14 @@ uint64_t test_wait_runout_ns();
 // call of this function, whose outputs it neither reads nor writes; the
 // tensor-core kernel then runs beside it (PromptTcParams::beside).  `max_keys`: the
 // most keys an entry on the device may have (a host table is the caller's to check).
+// `held`: an entry on the device with more rows than the host table's is bad.
 tf_status paged_partials(bool full, const void *q, int32_t n_rows_total, int32_t n_q_heads, const void *k_pool,
                          const void *v_pool, int32_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
                          const int32_t *page_table, int32_t page_table_len, const tf_seg *segs, int32_t n_segs,
                          const tf_seg *segs_host, const int32_t *page_table_host, float scale, int32_t split_keys,
                          int32_t n_splits_max, float *part_o, float *part_m, float *part_l, uint8_t *part_flag,
-                         uint32_t *status, tf_stream_t stream, bool beside = false, int max_keys = 0x7fffffff);
+                         uint32_t *status, tf_stream_t stream, bool beside = false, int max_keys = 0x7fffffff,
+                         bool held = false);
 
 // Partials of one kind for the merge of tf_paged_attn_q8 and
 // tf_paged_attn_shared: arrays [n_rows_total][hq][n_splits](*D), of which a row

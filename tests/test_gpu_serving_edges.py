@@ -399,3 +399,58 @@ def test_bf16_partials_of_a_stream_without_rows(fn):
     fn(dev(b.q), dev(b.k_pool), dev(b.v_pool), dev(b.page_table), dev(b.segs), scale=b.scale, split_keys=64,
        n_splits_max=2, part_o=po, part_m=pm, part_l=pl, part_flag=pf, status=st, segs_host=b.segs)
     assert int(st.item()) == 0
+
+
+HELD = [(12, 1, 128), (4, 1, 128), (16, 1, 64), (1, 1, 128), (2, 2, 256), (32, 2, 256)]  # general, decode, tcgen05
+
+
+@pytest.mark.parametrize("hq,hkv,d", HELD)
+@pytest.mark.parametrize("n_splits", [1, 8])
+@pytest.mark.parametrize("more", [2, 5])
+def test_an_entry_with_more_rows_than_the_launch_leaves_its_neighbours(hq, hkv, d, n_splits, more):
+    """Five one-row streams; on the device the first entry has grown over the rows of the next ones: its one row that
+    the launch holds is flagged, the others' are right."""
+    b, sides, c = q8_batch("e4m3", 41, rows=[1] * 5, keys=[300, 90, 64, 500, 40], n_q_heads=hq, n_kv_heads=hkv, head_dim=d,
+                           page_size=16)
+    ref, fl, vmax = reference(b, sides, "e4m3")
+    segs = b.segs.copy()
+    segs[0, 1] = more
+    q, pt = dev(b.q), dev(b.page_table)
+    out, flags, st = torch.full(b.q.shape, 5.0, device=DEV), torch.full((5, hq), 9, dtype=torch.uint8, device=DEV), status_word()
+    ws = torch.empty(tf.tf_paged_attn_q8_workspace_bytes(5, hq, d, n_splits), dtype=torch.uint8, device=DEV)
+    for _ in range(5):
+        tf.tf_paged_attn_q8(q, c, pt, dev(segs), scale=b.scale, n_splits_max=n_splits, workspace=ws, out=out, flags=flags,
+                            status=st, segs_host=b.segs)
+        assert int(st.item()) == binding.TF_DEV_BAD_SEG
+        o, f = out.cpu().numpy(), flags.cpu().numpy()
+        assert (f[0] == 1).all() and np.isnan(o[0]).all()
+        sv.check_attention(o[1:], f[1:], ref[1:], fl[1:], vmax, False)
+
+
+@pytest.mark.parametrize("hq,hkv,d", HELD)
+@pytest.mark.parametrize("which", ["segs", "prefixes"])
+def test_a_shared_entry_with_more_rows_than_the_launch_leaves_its_neighbours(hq, hkv, d, which):
+    """The same behind two prefixes: a stream that has grown over the next ones' rows, or the first prefix over the
+    second's."""
+    groups = [0, 0, 1, 1, 1] if which == "segs" else [0, 1, 1, 1, 1]
+    b, prefixes, segs = batch(42, [90, 200], groups, [1] * 5, [300, 90, 64, 500, 40], hq, hkv, d, 16)
+    ref, fl, vmax = shared_reference(b, prefixes, segs, groups)
+    bad_segs, bad_prefixes = segs.copy(), prefixes.copy()
+    if which == "segs":
+        bad_segs[0, 1] = 3
+        wrong = [0]
+    else:
+        bad_prefixes[0, 1] = 5  # more than the four that the launch holds
+        wrong = [0, 1, 2, 3, 4]
+    n = b.q.shape[0]
+    out, flags, st = torch.full(b.q.shape, 5.0, device=DEV), torch.full((n, hq), 9, dtype=torch.uint8, device=DEV), status_word()
+    ws = torch.empty(tf.tf_paged_attn_shared_workspace_bytes(n, hq, d, 8, 8), dtype=torch.uint8, device=DEV)
+    tf.tf_paged_attn_shared(dev(b.q), dev(b.k_pool).view(torch.bfloat16), dev(b.v_pool).view(torch.bfloat16),
+                            dev(b.page_table), dev(bad_prefixes), dev(bad_segs), scale=b.scale, n_prefix_splits=8,
+                            n_splits_max=8, workspace=ws, out=out, flags=flags, status=st, prefixes_host=prefixes,
+                            segs_host=segs)
+    assert int(st.item()) == binding.TF_DEV_BAD_SEG
+    o, f = out.cpu().numpy(), flags.cpu().numpy()
+    right = [r for r in range(n) if r not in wrong]
+    assert (f[wrong] == 1).all() and np.isnan(o[wrong]).all()
+    sv.check_attention(o[right], f[right], ref[right], fl[right], vmax, False)
