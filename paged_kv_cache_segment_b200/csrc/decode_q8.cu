@@ -36,8 +36,9 @@
 // tile after 4.8 us (table, page ids, copies, one after another), then takes 20 tiles
 // of 0.97 us and 1.5 us to combine and write: 26 us in the middle, 28 at the slowest.
 // Of a tile's 1,830 cycles its warps wait 290 for the copies (D 64 570 of 1,740, D 256
-// 560 of 2,560): what holds it is the codes' way through the MMAs, more than the loads.  Tried and not kept: four CTAs an SM at D 128 with two
-// stages each (36 us), one with three stages at D 256 (43 us).
+// 560 of 2,560): what holds it is the codes' way through the MMAs, more than the loads.
+// Tried and not kept: four CTAs an SM at D 128 with two stages each (36 us where three
+// took 30), one with three stages at D 256 (43 us, 32).
 #include <atomic>
 #include <cfloat>
 #include <cstdint>

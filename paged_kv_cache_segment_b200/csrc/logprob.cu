@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(kLpWarpRows * 32, 4) logprob_warp_kernel(const
         // of one chunk, the second of its vectors' largest: a row may fill two vectors only (60,000 rows x 512 with 32:
         // 158 us; 340 when it was the smaller of the two halves' largest, of which such rows have one)
         static_assert(kLpBatch == 4, "the second of four");
-        const float v0 = Elem<T>::most(a[0]), v1 = Elem<T>::most(a[1]), v2 = Elem<T>::most(a[2]), v3 = Elem<T>::most(a[3]);
+        const float v0 = Elem<T>::most(a[0]), v1 = Elem<T>::most(a[1]);
+        const float v2 = Elem<T>::most(a[2]), v3 = Elem<T>::most(a[3]);
         other = max3(fminf(v0, v1), fminf(v2, v3), fminf(fmaxf(v0, v1), fmaxf(v2, v3)));
     }
     given.fetch(p, w.at);

@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) merge_segs_kernel(const Merg
     const int64_t u = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (4 / SL) + warp / SL;
     const tf_seg e = p.segs[blockIdx.y];
     const int i = (int)(u / p.hq), h = (int)(u - (int64_t)i * p.hq);
-    if (i >= min(e.n_rows, p.own.max_rows) || e.q_row < 0 || (int64_t)e.q_row + i >= p.n_rows_total) {  // all warps of a unit leave
+    // (all warps of a unit leave together)
+    if (i >= min(e.n_rows, p.own.max_rows) || e.q_row < 0 || (int64_t)e.q_row + i >= p.n_rows_total) {
         asm volatile("griddepcontrol.wait;" ::: "memory");  // no grid of this kernel ends before the partials' does
         return;
     }

@@ -811,8 +811,8 @@ static cudaError_t launch_tc_t(const PromptTcParams &p, const void *k, const voi
     // library's previous chunk, or another of its attention calls) finishes:
     // it reads q, the pools and the page table, which none of them writes, so
     // the next chunk's tiles fill the SMs the previous chunk's last wave
-    // leaves idle; it ends after that call (leave() in the kernel).  (So may partials beside another partial kernel, whose outputs
-    // they neither read nor write.)
+    // leaves idle; it ends after that call (leave() in the kernel).  (So may partials
+    // beside another partial kernel, whose outputs they neither read nor write.)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kPTThreads);
