@@ -310,7 +310,8 @@ struct FinishBuf {
 };
 
 // A warp ends a row of its own, `own` being the lane's statistics and, if DEEP,
-// `other` the largest of another part of the lane's columns.  Returns the joined ones; with TOP the K largest keys are in b.top, largest first, 0 past the
+// `other` the largest of another part of the lane's columns.  Returns the joined
+// ones; with TOP the K largest keys are in b.top, largest first, 0 past the
 // unmasked columns.
 template <typename T, bool TOP, bool DEEP, int LIST>
 __device__ __forceinline__ Stat finish(const RowView<T> &w, const Stat &own, float other, FinishBuf<LIST> &b, int K,
